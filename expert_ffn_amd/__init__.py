@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(HERE, "libexpert_ffn.so")
 F32, BF16 = 0, 1
 W_BF16, W_INT8_ROW, W_INT4_G64 = 0, 1, 2
 ACT_GELU_TANH, ACT_SILU = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
 FMT_NAMES = {"bf16": W_BF16, "int8": W_INT8_ROW, "int4": W_INT4_G64}
 
 _lib = None
@@ -65,6 +67,17 @@ def lib():
         L.moe_fill_slots.argtypes = [i32, i32, P, i32, i32, P, P, P]
         L.moe_verify_slot.argtypes = [i32, P, i32, i32, P, P, P]
         L.moe_slot_admit.argtypes = [P, i32, P, i32, i32]
+        f32, i64 = ctypes.c_float, ctypes.c_int64
+        L.moe_route_score_topk.argtypes = [P, i32, i64, P, i32, i32, i32, i32, i32, i32, i32, i32, f32, P, P, P]
+        L.moe_norm_in.argtypes = [P, i32, i64, i32, i32, P, i32, f32, f32, P, i32, i64, P, i64, P, P]
+        L.moe_norm_out.argtypes = [P, i32, P, P, i32, P, i32, i64, i32, i32, P, i32, f32, f32, P, i32, i64, i64, f32, f32,
+                                   P, i32, i64, P, i64, i32, P, P, i32, i64, P, i64, P, P]
+        L.moe_quantize_tokens.argtypes = [P, i32, i64, i32, i32, P, i64, P, P]
+        L.moe_matmul_i8.argtypes = [P, i64, P, P, i64, P, P, i32, i32, i32, P, i32, i64, P]
+        L.moe_gated_matmul_i8.argtypes = [P, i64, P, P, i64, P, i32, i32, i32, i32, P, i32, i64, P]
+        for name in ("moe_route_score_topk", "moe_norm_in", "moe_norm_out", "moe_quantize_tokens", "moe_matmul_i8",
+                     "moe_gated_matmul_i8"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("moe_blob_layout", "moe_route_topk", "moe_permute", "moe_route_permute", "moe_expert_ffn",
                      "moe_ffn_gate_up", "moe_ffn_down", "moe_expert_ffn_noalloc", "moe_combine", "moe_quantize",
                      "moe_pack_expert", "moe_router_topk", "moe_residency_refresh", "moe_min_weight", "moe_fill_slot", "moe_fill_slots", "moe_verify_slot",
@@ -263,3 +276,193 @@ def refresh_due(every: int, step: int, prefill_block: bool, offload: bool) -> bo
 def budget_from_memory(free_bytes: int, reserve_bytes: int, expert_bytes: int, layers: int, max_per_layer: int,
                        E: int) -> int:
     return int(lib().moe_budget_from_memory(free_bytes, reserve_bytes, expert_bytes, layers, max_per_layer, E))
+
+
+# --------------------------------------------- around the expert FFN --
+# These calls check shapes, types and devices here, take rows at any stride
+# (elements of a row contiguous), and run on the tensors' device: on its
+# current stream when none is given.
+_DT = None
+
+
+def _dtypes():
+    global _DT
+    if _DT is None:
+        import torch
+        _DT = {torch.float32: F32, torch.bfloat16: BF16}
+    return _DT
+
+
+def _mat(name, t, rows, cols, dev, dt=None):
+    """(pointer, dtype code, row stride) of t [rows, cols] on dev; dt: the only type allowed (else fp32 or bf16)."""
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    code = _dtypes().get(t.dtype)
+    if (code is None) if dt is None else (t.dtype != dt):
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"the elements of a row of {name} are not contiguous")
+    return t.data_ptr(), code, (s0 if rows > 1 else cols)
+
+
+def _vec(name, t, n, dev, dt=None):
+    """(pointer, dtype code) of the n contiguous elements of t on dev (n in all, whatever the shape)."""
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    code = _dtypes().get(t.dtype)
+    if (code is None) if dt is None else (t.dtype != dt):
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    return t.data_ptr(), code
+
+
+def _on(dev, stream, name, *args):
+    """Call the entry point on dev's current stream (or `stream`), with dev current."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors are on {dev}: a GPU is needed")
+    s = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = getattr(lib(), name)(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(lib(), name)(*args, s)
+    if rc:
+        _check(rc)
+
+
+def route_score_topk(logits, k: int, topk_ids, topk_w, score: int = SCORE_SOFTMAX, bias=None, n_group: int = 1,
+                     topk_group: int = 1, group_rank: int = GROUP_MAX, renorm: int = 1, scale: float = 1.0,
+                     stream=None):
+    """Top-k of softmax or sigmoid scores of logits [T, E] plus a bias [E] that counts for the choice
+    only, inside the topk_group best of n_group expert groups; ids int32 and weights fp32 [T, k]."""
+    import torch
+    T, E = logits.shape
+    dev = logits.device
+    lp, ldt, ld = _mat("logits", logits, T, E, dev)
+    bp = None if bias is None else _vec("bias", bias, E, dev, torch.float32)[0]
+    ip = _vec("topk_ids", topk_ids, T * k, dev, torch.int32)[0]
+    wp = _vec("topk_w", topk_w, T * k, dev, torch.float32)[0]
+    _on(dev, stream, "moe_route_score_topk", lp, ldt, ld, bp, T, E, k, score, n_group, topk_group, group_rank, renorm,
+        scale, ip, wp)
+
+
+def _norm_outputs(T, H, dev, x, xq, xq_scale):
+    import torch
+    xp, xdt, ldx = (None, F32, 0) if x is None else _mat("x", x, T, H, dev)
+    if (xq is None) != (xq_scale is None):
+        raise ValueError("xq and xq_scale go together")
+    if xq is None:
+        return xp, xdt, ldx, None, 0, None
+    qp, _, ldq = _mat("xq", xq, T, H, dev, torch.int8)
+    return xp, xdt, ldx, qp, ldq, _vec("xq_scale", xq_scale, T, dev, torch.float32)[0]
+
+
+def norm_in(h, w, eps: float, x=None, xq=None, xq_scale=None, w_offset: float = 0.0, stream=None):
+    """RMS norm of the rows of h [T, H] with weight w_offset + w [H] (w None: 1), into x (fp32 or bf16),
+    as int8 codes xq with one fp32 scale per row (xq_scale [T]), or both."""
+    T, H = h.shape
+    dev = h.device
+    hp, hdt, ldh = _mat("h", h, T, H, dev)
+    wp, wdt = (None, F32) if w is None else _vec("w", w, H, dev)
+    _on(dev, stream, "moe_norm_in", hp, hdt, ldh, T, H, wp, wdt, w_offset, eps,
+        *_norm_outputs(T, H, dev, x, xq, xq_scale))
+
+
+def quantize_tokens(x, xq, xq_scale, stream=None):
+    """int8 codes and the scale of each row of x [T, K] (the rule of the int8 weight rows)."""
+    import torch
+    T, K = x.shape
+    dev = x.device
+    xp, xdt, ldx = _mat("x", x, T, K, dev)
+    qp, _, ldq = _mat("xq", xq, T, K, dev, torch.int8)
+    _on(dev, stream, "moe_quantize_tokens", xp, xdt, ldx, T, K, qp, ldq,
+        _vec("xq_scale", xq_scale, T, dev, torch.float32)[0])
+
+
+def norm_out(h, h_out, w_post, eps: float, out_routes=None, topk_w=None, route_pos=None, y=None, gate=None,
+             block_scale: float = 1.0, res_scale: float = 1.0, w_next=None, x=None, xq=None, xq_scale=None,
+             w_offset: float = 0.0, stream=None):
+    """End of a block: h_out = res_scale * h + block_scale * gate * norm(b; w_post), where b is the weighted
+    combine of out_routes (topk_w, route_pos [T, k] as for combine) plus y [T, H]; then, when x or xq is
+    given, the next block's norm of h_out (w_next) into them.  w_post None: b is not normed.  gate
+    broadcasts to [T, H].  h_out may be h."""
+    import torch
+    T, H = h.shape
+    dev = h.device
+    hp, hdt, ldh = _mat("h", h, T, H, dev)
+    op, odt, ldo = _mat("h_out", h_out, T, H, dev, h.dtype)
+    rp = wp = pp = None
+    rdt, k = F32, 0
+    if out_routes is not None:
+        if topk_w is None or route_pos is None:
+            raise ValueError("out_routes needs topk_w and route_pos")
+        R = route_pos.numel()
+        k = R // T if T else 0
+        if k * T != R:
+            raise ValueError(f"route_pos has {R} elements, not a multiple of T={T}")
+        if not out_routes.is_contiguous():
+            raise ValueError("out_routes is not contiguous")
+        rp, rdt, _ = _mat("out_routes", out_routes, R, H, dev)
+        wp = _vec("topk_w", topk_w, R, dev, torch.float32)[0]
+        pp = _vec("route_pos", route_pos, R, dev, torch.int32)[0]
+    yp, ydt, ldy = (None, F32, 0) if y is None else _mat("y", y, T, H, dev)
+    pw, wdt = (None, F32) if w_post is None else _vec("w_post", w_post, H, dev)
+    nw = None
+    if w_next is not None:
+        nw, ndt = _vec("w_next", w_next, H, dev)
+        if w_post is not None and ndt != wdt:
+            raise TypeError("w_post and w_next have different dtypes")
+        wdt = ndt
+    gp, gdt, gst, gsh = None, F32, 0, 0
+    if gate is not None:
+        g = gate.expand(T, H)
+        if g.device != dev:
+            raise ValueError(f"gate is on {g.device}, expected {dev}")
+        gdt = _dt(g)
+        gst, gsh = g.stride()
+        gst = gst if T > 1 else 0
+        gp = g.data_ptr()
+    outs = _norm_outputs(T, H, dev, x, xq, xq_scale)
+    nxt = int(x is not None or xq is not None)
+    if w_next is not None and not nxt:
+        raise ValueError("w_next is given, but neither x nor xq to write the next norm into")
+    _on(dev, stream, "moe_norm_out", rp, rdt, wp, pp, k, yp, ydt, ldy, T, H, pw, wdt, w_offset, eps, gp, gdt, gst, gsh,
+        block_scale, res_scale, hp, hdt, ldh, op, ldo, nxt, nw, *outs)
+
+
+def matmul_i8(xq, x_scale, wq, w_scale, out, bias=None, stream=None):
+    """out [T, N] = (xq [T, K] . wq [N, K]) * x_scale [T] * w_scale [N] (+ bias [N] fp32): int8 codes, exact
+    int32 sums, out fp32 or bf16."""
+    import torch
+    T, K = xq.shape
+    N = wq.shape[0]
+    dev = xq.device
+    xp, _, ldx = _mat("xq", xq, T, K, dev, torch.int8)
+    wp, _, ldw = _mat("wq", wq, N, K, dev, torch.int8)
+    op, odt, ldo = _mat("out", out, T, N, dev)
+    _on(dev, stream, "moe_matmul_i8", xp, ldx, _vec("x_scale", x_scale, T, dev, torch.float32)[0], wp, ldw,
+        _vec("w_scale", w_scale, N, dev, torch.float32)[0],
+        None if bias is None else _vec("bias", bias, N, dev, torch.float32)[0], T, N, K, op, odt, ldo)
+
+
+def gated_matmul_i8(xq, x_scale, wq, w_scale, act: int, out, stream=None):
+    """out [T, F] = act(gate) * up of the int8 product of xq [T, K] with wq [2F, K] (gate rows, then up rows,
+    as an expert's w13)."""
+    import torch
+    T, K = xq.shape
+    N2 = wq.shape[0]
+    if N2 % 2:
+        raise ValueError(f"wq has {N2} rows: gate and up rows come in pairs")
+    dev = xq.device
+    xp, _, ldx = _mat("xq", xq, T, K, dev, torch.int8)
+    wp, _, ldw = _mat("wq", wq, N2, K, dev, torch.int8)
+    op, odt, ldo = _mat("out", out, T, N2 // 2, dev)
+    _on(dev, stream, "moe_gated_matmul_i8", xp, ldx, _vec("x_scale", x_scale, T, dev, torch.float32)[0], wp, ldw,
+        _vec("w_scale", w_scale, N2, dev, torch.float32)[0], T, N2 // 2, K, act, op, odt, ldo)

@@ -9,11 +9,16 @@
 #include "../../include/expert_ffn.h"
 #include "common.h"
 #include "kernels.h"
+#include "status.h"
 #include <algorithm>
 
 namespace {
 
 thread_local std::string g_last_error;
+
+}  // namespace
+
+namespace moe {
 
 moe_status fail(moe_status st, const char* fn, const char* fmt, ...) {
     char buf[512];
@@ -30,8 +35,15 @@ moe_status hip_status(const char* fn, hipError_t e) {
     return fail(MOE_E_HIP, fn, "%s", hipGetErrorString(e));
 }
 
+}  // namespace moe
+
+using moe::dt_ok;
+using moe::fail;
+using moe::hip_status;
+
+namespace {
+
 bool fmt_ok(int32_t f) { return f == MOE_W_BF16 || f == MOE_W_INT8_ROW || f == MOE_W_INT4_G64; }
-bool dt_ok(int32_t d) { return d == MOE_F32 || d == MOE_BF16; }
 
 uint64_t up256(uint64_t x) { return (x + 255u) / 256u * 256u; }
 

@@ -1,0 +1,356 @@
+// RMS norms before and after the block, fused with what stands next to them:
+// the 8-bit codes of the integer products before, and after the block the
+// combine, the dense expert's rows, the gate, the residual and the next norm.
+//
+//   norm:   r = 1 / sqrt(mean h^2 + eps),  x = (h r) (off + w)
+//   codes:  u = h (off + w),  a = max |u|,  s = a / 127,  q = rint(u / s),
+//           scale = s r: r cancels in the codes of the normed row, so they
+//           depend on no order of summation, and one pass over the row gives
+//           the sum of squares and the maximum together.
+//   after:  b = sum_j w_j o_pos(j) + y,  n = norm(b),
+//           h' = res h + block gate n,  x = norm(h' as stored)
+//
+// Memory bound: every input is read once and every output written once.  One
+// workgroup takes one row and keeps it in registers between the reduction and
+// the write; a thread holds C chunks of 8 elements, chunk i at
+// threadIdx + i * blockDim.  Sums and statistics are fp32, in a fixed order
+// (chunks in a thread, lanes, waves), so results are reproducible.
+#include "block.h"
+#include "common.h"
+#include "route.h"
+
+#pragma clang fp contract(off)
+
+namespace moe {
+
+struct Raw8 {
+    u32x4 a, b;   // 8 elements: bf16 in a, fp32 in a and b
+};
+
+__device__ __forceinline__ Raw8 load_raw8(const void* p, int dt, int64_t i) {
+    Raw8 r;
+    if (dt == F32) {
+        const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
+        r.a = s[0];
+        r.b = s[1];
+    } else {
+        r.a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+        r.b = u32x4{0u, 0u, 0u, 0u};
+    }
+    return r;
+}
+__device__ __forceinline__ void widen8(const Raw8& r, int dt, float (&v)[8]) {
+    if (dt == F32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = __uint_as_float(r.a[j]);
+            v[4 + j] = __uint_as_float(r.b[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(r.a[j] << 16);
+            v[2 * j + 1] = __uint_as_float(r.a[j] & 0xFFFF0000u);
+        }
+    }
+}
+__device__ __forceinline__ u32x4 narrow8(const float (&v)[8]) {
+    u32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+    return o;
+}
+__device__ __forceinline__ void store8(void* p, int dt, int64_t i, const float (&v)[8]) {
+    if (dt == F32) {
+        f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(p) + i);
+        d[0] = f32x4{v[0], v[1], v[2], v[3]};
+        d[1] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = narrow8(v);
+    }
+}
+
+// off + w of 8 channels (1 without a weight)
+__device__ __forceinline__ void weight8(const Raw8& r, const void* w, int dt, float off, float (&v)[8]) {
+    if (w == nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 1.0f;
+        return;
+    }
+    widen8(r, dt, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = off + v[j];
+}
+
+// |v| as bits: ordered like |v|, infinities above every number and NaN above them
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// 8 codes of u at scale s (all 0 when s is 0, infinite or NaN)
+__device__ __forceinline__ u32x2 codes8(const float (&u)[8], float s) {
+    u32x2 o = {0u, 0u};
+    if (s > 0.0f && s < __builtin_inff()) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float c = fminf(fmaxf(rintf(u[j] / s), -127.0f), 127.0f);
+            o[j >> 2] |= (static_cast<uint32_t>(static_cast<int>(c)) & 0xFFu) << (8 * (j & 3));
+        }
+    }
+    return o;
+}
+
+struct RowStat {
+    float sum;
+    uint32_t top;
+};
+constexpr int MAX_WAVES = 16;
+
+// Sum and maximum over the workgroup; red has MAX_WAVES entries of its own for
+// each use in a kernel, so one barrier is enough.
+__device__ __forceinline__ RowStat block_stat(RowStat s, RowStat* red, bool top) {
+    s.sum = wave_sum_f32(s.sum);
+    if (top) s.top = wave_max_u32(s.top);
+    const int nw = blockDim.x >> 6;
+    if (nw == 1) return s;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    RowStat r = red[0];
+    for (int i = 1; i < nw; ++i) {
+        r.sum += red[i].sum;
+        r.top = max(r.top, red[i].top);
+    }
+    return r;
+}
+
+template <int HT, int C, bool NORM>
+__global__ __launch_bounds__(1024) void norm_in_kernel(const void* __restrict__ h, int64_t ldh, int H, NormOut o) {
+    __shared__ RowStat red[MAX_WAVES];
+    const int t = blockIdx.x, nt = blockDim.x, nchunk = H >> 3;
+    const int64_t hb = static_cast<int64_t>(t) * ldh;
+    Raw8 hr[C], wr[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int c = threadIdx.x + i * nt;
+        if (c < nchunk) {
+            hr[i] = load_raw8(h, HT, hb + 8 * c);
+            if (NORM && o.w != nullptr) wr[i] = load_raw8(o.w, o.w_dt, 8 * c);
+        }
+    }
+    RowStat st = {0.0f, 0u};
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        if (static_cast<int>(threadIdx.x) + i * nt >= nchunk) continue;
+        float v[8], w[8];
+        widen8(hr[i], HT, v);
+        if (NORM) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) st.sum = fmaf(v[j], v[j], st.sum);
+            weight8(wr[i], o.w, o.w_dt, o.w_offset, w);
+        }
+        if (o.xq != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) st.top = max(st.top, abs_bits(NORM ? v[j] * w[j] : v[j]));
+        }
+    }
+    st = block_stat(st, red, o.xq != nullptr);
+    const float r = NORM ? 1.0f / sqrtf(st.sum / static_cast<float>(H) + o.eps) : 1.0f;
+    const float s = __uint_as_float(st.top) / 127.0f;
+    if (o.xq != nullptr && threadIdx.x == 0) o.xq_scale[t] = s * r;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int c = threadIdx.x + i * nt;
+        if (c >= nchunk) continue;
+        float v[8], w[8], x[8];
+        widen8(hr[i], HT, v);
+        if (NORM) weight8(wr[i], o.w, o.w_dt, o.w_offset, w);
+        if (NORM && o.x != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = v[j] * r * w[j];
+            store8(o.x, o.x_dt, static_cast<int64_t>(t) * o.ldx + 8 * c, x);
+        }
+        if (o.xq != nullptr) {
+            if (NORM) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = v[j] * w[j];
+            }
+            *reinterpret_cast<u32x2*>(o.xq + static_cast<int64_t>(t) * o.ldq + 8 * c) = codes8(v, s);
+        }
+    }
+}
+
+// Threads and chunks per thread of a row of nchunk chunks: one chunk each while
+// at most `cap` threads take part, then 2 or 4 (at most 1024 threads then:
+// NORM_H_MAX = 1024 * 4 * 8).
+static int row_threads(int nchunk, int cap, int* C) {
+    int c = 1;
+    while (c < 4 && (nchunk + c - 1) / c > cap) c *= 2;
+    *C = c;
+    return ((nchunk + c - 1) / c + 63) / 64 * 64;
+}
+constexpr int NORM_MANY_ROWS = 2048;
+
+template <int HT, bool NORM>
+static hipError_t norm_in_by_chunks(const void* h, int64_t ldh, int T, int H, const NormOut& o, hipStream_t s) {
+    int C;
+    const int nt = row_threads(H / 8, T >= NORM_MANY_ROWS ? 256 : 1024, &C);
+    const dim3 grid(T), block(nt);
+    auto kn = C == 1 ? norm_in_kernel<HT, 1, NORM>
+                     : C == 2 ? norm_in_kernel<HT, 2, NORM> : norm_in_kernel<HT, 4, NORM>;
+    hipLaunchKernelGGL(kn, grid, block, 0, s, h, ldh, H, o);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_in(const void* h, int h_dt, int64_t ldh, int T, int H, const NormOut& o, hipStream_t s) {
+    return h_dt == F32 ? norm_in_by_chunks<F32, true>(h, ldh, T, H, o, s)
+                       : norm_in_by_chunks<BF16, true>(h, ldh, T, H, o, s);
+}
+
+hipError_t launch_quantize_tokens(const void* x, int x_dt, int64_t ldx, int T, int K, int8_t* q, int64_t ldq,
+                                  float* scale, hipStream_t s) {
+    NormOut o{};
+    o.xq = q;
+    o.ldq = ldq;
+    o.xq_scale = scale;
+    return x_dt == F32 ? norm_in_by_chunks<F32, false>(x, ldx, T, K, o, s)
+                       : norm_in_by_chunks<BF16, false>(x, ldx, T, K, o, s);
+}
+
+// After the block.  The routes of a row are requested NO_CH at a time, all
+// loads before the first addition; the sums run in ascending j, then y, fp32.
+template <int OT, int C>
+__global__ __launch_bounds__(1024) void norm_out_kernel(NormOutParams p) {
+    constexpr int NO_CH = C == 4 ? 4 : 8;   // 8 would not fit the registers beside 4 chunks
+    __shared__ RowStat red[2][MAX_WAVES];
+    const int t = blockIdx.x, nt = blockDim.x, H = p.H, nchunk = H >> 3;
+    float b[C][8];
+    Raw8 hr[C];
+    RowStat st = {0.0f, 0u};
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int c = threadIdx.x + i * nt;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[i][j] = 0.0f;
+        if (c >= nchunk) continue;
+        hr[i] = load_raw8(p.h, p.h_dt, static_cast<int64_t>(t) * p.ldh + 8 * c);
+        Raw8 yr;
+        if (p.y != nullptr) yr = load_raw8(p.y, p.y_dt, static_cast<int64_t>(t) * p.ldy + 8 * c);
+        for (int j0 = 0; j0 < p.k; j0 += NO_CH) {
+            int pj[NO_CH];
+            float wj[NO_CH];
+            Raw8 rows[NO_CH];
+#pragma unroll
+            for (int q = 0; q < NO_CH; ++q) {
+                const int64_t j = static_cast<int64_t>(t) * p.k + min(j0 + q, p.k - 1);
+                pj[q] = j0 + q < p.k ? p.route_pos[j] : -1;
+                if (pj[q] >= p.T * p.k) pj[q] = -1;
+                wj[q] = p.topk_w[j];
+            }
+#pragma unroll
+            for (int q = 0; q < NO_CH; ++q)
+                if (pj[q] >= 0) rows[q] = load_raw8(p.out_routes, OT, static_cast<int64_t>(pj[q]) * H + 8 * c);
+#pragma unroll
+            for (int q = 0; q < NO_CH; ++q) {
+                if (pj[q] < 0) continue;
+                float v[8];
+                widen8(rows[q], OT, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) b[i][j] = fmaf(wj[q], v[j], b[i][j]);
+            }
+        }
+        if (p.y != nullptr) {
+            float v[8];
+            widen8(yr, p.y_dt, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[i][j] += v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) st.sum = fmaf(b[i][j], b[i][j], st.sum);
+    }
+    float r = 1.0f;
+    if (p.w_post != nullptr) {
+        st = block_stat(st, red[0], false);
+        r = 1.0f / sqrtf(st.sum / static_cast<float>(H) + p.eps);
+    }
+    st = {0.0f, 0u};
+    const bool codes = p.next && p.n.xq != nullptr;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int c = threadIdx.x + i * nt;
+        if (c >= nchunk) continue;
+        float v[8], g[8];
+        if (p.w_post != nullptr) {
+            weight8(load_raw8(p.w_post, p.w_dt, 8 * c), p.w_post, p.w_dt, p.w_offset, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[i][j] = b[i][j] * r * v[j];
+        }
+        if (p.gate != nullptr) {
+            const int64_t g0 = static_cast<int64_t>(t) * p.gate_st;
+            if (p.gate_sh == 0) {
+                const float gt = p.gate_dt == F32 ? static_cast<const float*>(p.gate)[g0]
+                                                  : bf16_to_f32(static_cast<const uint16_t*>(p.gate)[g0]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] = gt;
+            } else {
+                widen8(load_raw8(p.gate, p.gate_dt, g0 + 8 * c), p.gate_dt, g);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[i][j] = b[i][j] * g[j];
+        }
+        widen8(hr[i], p.h_dt, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = p.res_scale * v[j] + p.block_scale * b[i][j];
+        store8(p.h_out, p.h_dt, static_cast<int64_t>(t) * p.ldho + 8 * c, v);
+        if (!p.next) continue;
+        if (p.h_dt == BF16) {   // the next norm is that of the row as it is stored
+            Raw8 s;
+            s.a = narrow8(v);
+            widen8(s, BF16, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) st.sum = fmaf(v[j], v[j], st.sum);
+        if (codes) {
+            weight8(p.n.w != nullptr ? load_raw8(p.n.w, p.n.w_dt, 8 * c) : Raw8{}, p.n.w, p.n.w_dt, p.n.w_offset, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) st.top = max(st.top, abs_bits(v[j] * g[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[i][j] = v[j];
+    }
+    if (!p.next) return;
+    st = block_stat(st, red[1], codes);
+    r = 1.0f / sqrtf(st.sum / static_cast<float>(H) + p.n.eps);
+    const float s = __uint_as_float(st.top) / 127.0f;
+    if (codes && threadIdx.x == 0) p.n.xq_scale[t] = s * r;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int c = threadIdx.x + i * nt;
+        if (c >= nchunk) continue;
+        float w[8], x[8];
+        weight8(p.n.w != nullptr ? load_raw8(p.n.w, p.n.w_dt, 8 * c) : Raw8{}, p.n.w, p.n.w_dt, p.n.w_offset, w);
+        if (p.n.x != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = b[i][j] * r * w[j];
+            store8(p.n.x, p.n.x_dt, static_cast<int64_t>(t) * p.n.ldx + 8 * c, x);
+        }
+        if (codes) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = b[i][j] * w[j];
+            *reinterpret_cast<u32x2*>(p.n.xq + static_cast<int64_t>(t) * p.n.ldq + 8 * c) = codes8(x, s);
+        }
+    }
+}
+
+template <int OT>
+static hipError_t norm_out_by_chunks(const NormOutParams& p, hipStream_t s) {
+    int C;
+    const int nt = row_threads(p.H / 8, 1024, &C);
+    auto kn = C == 1 ? norm_out_kernel<OT, 1>
+                     : C == 2 ? norm_out_kernel<OT, 2> : norm_out_kernel<OT, 4>;
+    hipLaunchKernelGGL(kn, dim3(p.T), dim3(nt), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_out(const NormOutParams& p, hipStream_t s) {
+    return p.out_dt == F32 ? norm_out_by_chunks<F32>(p, s) : norm_out_by_chunks<BF16>(p, s);
+}
+
+}  // namespace moe

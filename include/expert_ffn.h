@@ -413,6 +413,120 @@ moe_status moe_verify_slot(int32_t wfmt, const void* src, int32_t H, int32_t FF,
  */
 int32_t moe_slot_admit(int32_t* slot_of, int32_t E, int32_t* owner, int32_t S, int32_t expert);
 
+/*
+ * ---- Around the expert FFN: routing by scores, the norms before and after the
+ * block, and the 8-bit products of a dense (shared) expert beside the routed
+ * ones.  Rows of the matrices below are `ld` elements apart (ld >= columns),
+ * their elements contiguous.  No output may overlap another output or an input
+ * unless said otherwise (MOE_E_ARG).  Nothing is written beside the rows and
+ * columns named.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_rank;
+
+/*
+ * Router top-k over scores.  For token t with logits l (device [T, E], fp32 or
+ * bf16, rows ld_logits apart):
+ *   s_e = softmax(l)_e or 1 / (1 + exp(-l_e));   c_e = s_e + bias_e (bias
+ *   device fp32 [E] or NULL: for the balance of the experts, it counts for the
+ *   choice only);
+ *   the E experts form n_group groups of consecutive ids; a group ranks by its
+ *   largest c (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2);
+ *   the topk_group best groups stay (equal ranks: lower group first);
+ *   topk_ids (device int32 [T, k]): the k experts of those groups with the
+ *   largest c, best first, equal ones by lower id;
+ *   topk_w (device fp32 [T, k]): s of the chosen, divided by their sum when
+ *   renorm != 0 (0 where the sum is 0), times scale; computed in 64 bits and
+ *   rounded once.
+ * Scores and c are taken in 64 bits, so the choice does not depend on 32-bit
+ * rounding.  A NaN logit scores 0 and ranks below every number, as does a NaN
+ * c; infinite logits take the limits (softmax: the experts at +inf share the
+ * weight; a row of -inf alone scores 0 everywhere).
+ * 1 <= k <= min(32, topk_group * E / n_group), E <= 512, n_group a divisor of E,
+ * at most 64; scale finite.  T = 0 enqueues nothing.
+ */
+moe_status moe_route_score_topk(const void* logits, int32_t logits_dtype, int64_t ld_logits, const float* bias, int32_t T,
+                                int32_t E, int32_t k, int32_t score, int32_t n_group, int32_t topk_group,
+                                int32_t group_rank, int32_t renorm, float scale, int32_t* topk_ids, float* topk_w,
+                                void* stream);
+
+/*
+ * RMS norm before a block: for each row of h (device [T, H], fp32 or bf16)
+ *   r = 1 / sqrt(mean(h^2) + eps),   x = (h * r) * (w_offset + w)
+ * with w device [H], fp32 or bf16 (NULL: the factor is 1).
+ *   x   (device [T, H], fp32 or bf16, or NULL) the normed rows
+ *   xq  (device int8 [T, H], or NULL) their codes for the 8-bit products, and
+ *       xq_scale (device fp32 [T]): with u = h * (w_offset + w) (fp32, each
+ *       operation rounded), a = max |u|, s = a / 127:
+ *       xq = clamp(rint(u / s), -127, 127) (0 if s = 0), xq_scale = s * r.
+ *       The codes are those of the normed row (r > 0 cancels), and do not
+ *       depend on the rounding of r.  A row that holds a NaN or an infinity has
+ *       a scale that is not finite where its codes cannot stand for it.
+ * At least one of x and xq.  The mean is an fp32 sum: squares beyond the fp32
+ * range are infinite.  H a multiple of 8 up to 32768; rows of h and x 16-byte
+ * aligned, w 16-byte, rows of xq 8-byte; eps > 0; T <= 2^21, T = 0 enqueues
+ * nothing.
+ */
+moe_status moe_norm_in(const void* h, int32_t h_dtype, int64_t ldh, int32_t T, int32_t H, const void* w, int32_t w_dtype,
+                       float w_offset, float eps, void* x, int32_t x_dtype, int64_t ldx, int8_t* xq, int64_t ldq,
+                       float* xq_scale, void* stream);
+
+/*
+ * The end of a block, for each row t in one pass:
+ *   b  = sum over j = 0..k-1 with 0 <= route_pos[t*k+j] < T*k of
+ *        topk_w[t*k+j] * out_routes[route_pos[t*k+j]] (as moe_combine), then + y[t]
+ *   n  = (b / sqrt(mean(b^2) + eps)) * (w_offset + w_post)     (w_post NULL: n = b)
+ *   h_out = res_scale * h + block_scale * (gate * n)           (rounded to h's type)
+ *   next_norm != 0: moe_norm_in of the rows of h_out as they are stored, with
+ *        w_next (NULL: 1), w_offset and eps, into x and / or xq, xq_scale.
+ *   out_routes device [T*k, H] contiguous, fp32 or bf16; topk_w fp32, route_pos
+ *        int32 [T*k] (moe_permute's); k = 0: no routes (they may be NULL)
+ *   y    device [T, H] or NULL: another summand, e.g. a dense expert's rows
+ *   gate device or NULL: element (t, h) at t * gate_stride_t + h * gate_stride_h,
+ *        gate_stride_h 0 (one value per row) or 1 (16-byte aligned rows);
+ *        stride 0 repeats
+ *   w_post and w_next have one type (w_dtype).  h_out may be h itself (same
+ *   pointer and stride).  Sums are fp32 in a fixed order.  Shapes and alignment
+ *   as in moe_norm_in; 0 <= k <= 32; routes or y must be given.
+ */
+moe_status moe_norm_out(const void* out_routes, int32_t out_dtype, const float* topk_w, const int32_t* route_pos, int32_t k,
+                        const void* y, int32_t y_dtype, int64_t ldy, int32_t T, int32_t H, const void* w_post,
+                        int32_t w_dtype, float w_offset, float eps, const void* gate, int32_t gate_dtype,
+                        int64_t gate_stride_t, int64_t gate_stride_h, float block_scale, float res_scale, const void* h,
+                        int32_t h_dtype, int64_t ldh, void* h_out, int64_t ldho, int32_t next_norm, const void* w_next,
+                        void* x, int32_t x_dtype, int64_t ldx, int8_t* xq, int64_t ldq, float* xq_scale, void* stream);
+
+/*
+ * Codes of activations: for each row of x (device [T, K], fp32 or bf16) the rule
+ * of MOE_W_INT8_ROW (moe_quantize): a = max |x|, s = a / 127, xq = clamp(rint(x /
+ * s), -127, 127), xq_scale = s.  A row that holds a NaN or an infinity gets codes
+ * 0 and that scale, so its products are NaN.  K a multiple of 8 up to 32768.
+ */
+moe_status moe_quantize_tokens(const void* x, int32_t x_dtype, int64_t ldx, int32_t T, int32_t K, int8_t* xq, int64_t ldq,
+                               float* xq_scale, void* stream);
+
+/*
+ * 8-bit integer product with a scale per token and per channel:
+ *   out[t][n] = ((sum_k xq[t][k] * wq[n][k]) * x_scale[t]) * w_scale[n] + bias[n]
+ *   xq device int8 [T, K], x_scale fp32 [T] (moe_norm_in, moe_quantize_tokens)
+ *   wq device int8 [N, K], w_scale fp32 [N]: what moe_quantize writes for
+ *      MOE_W_INT8_ROW, or the w13 / w2 blocks of an int8 blob (moe_blob_layout)
+ *   bias device fp32 [N] or NULL;  out device [T, N], fp32 or bf16
+ * moe_gated_matmul_i8 is the first half of a gated FFN: wq [2F, K] holds F gate
+ * rows, then F up rows (an expert's w13), and with the products g and u,
+ *   out[t][f] = act(g[t][f]) * u[t][f]   (device [T, F]).
+ * The integer sums are exact; the rest is fp32, rounded once to out's type.
+ * K a multiple of 16 up to 131056, rows of xq and wq 16-byte aligned with strides
+ * up to 2^22; any T and N.  T = 0 enqueues nothing.
+ */
+moe_status moe_matmul_i8(const int8_t* xq, int64_t ldx, const float* x_scale, const int8_t* wq, int64_t ldw,
+                         const float* w_scale, const float* bias, int32_t T, int32_t N, int32_t K, void* out,
+                         int32_t out_dtype, int64_t ldo, void* stream);
+
+moe_status moe_gated_matmul_i8(const int8_t* xq, int64_t ldx, const float* x_scale, const int8_t* wq, int64_t ldw,
+                               const float* w_scale, int32_t T, int32_t F, int32_t K, int32_t act, void* out,
+                               int32_t out_dtype, int64_t ldo, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
