@@ -283,56 +283,75 @@ def budget_from_memory(free_bytes: int, reserve_bytes: int, expert_bytes: int, l
 # (elements of a row contiguous), and run on the tensors' device: on its
 # current stream when none is given.
 _DT = None
+_raw_stream = _device = None
 
 
-def _dtypes():
-    global _DT
-    if _DT is None:
-        import torch
-        _DT = {torch.float32: F32, torch.bfloat16: BF16}
-    return _DT
+def _setup():
+    """torch's type codes and its raw-stream and device queries (torch is imported on first use only; the
+    public current_stream() builds a Stream object, 1.8 us of a call that takes 5)."""
+    global _DT, _raw_stream, _device
+    import torch
+    _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: "int8", torch.int32: "int32"}
 
 
-def _mat(name, t, rows, cols, dev, dt=None):
-    """(pointer, dtype code, row stride) of t [rows, cols] on dev; dt: the only type allowed (else fp32 or bf16)."""
+def _type(name, t, kind):
+    """fp32 or bf16 (kind None): its code; else t must be of that kind."""
+    code = _DT.get(t.dtype)
+    if code is None or (code not in (F32, BF16) if kind is None else code != kind):
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
+    return code
+
+
+def _mat(name, t, rows, cols, dev, kind=None):
+    """(pointer, dtype code, row stride) of t [rows, cols] on dev."""
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    code = _dtypes().get(t.dtype)
-    if (code is None) if dt is None else (t.dtype != dt):
-        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
+    code = _type(name, t, kind)
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
         raise ValueError(f"the elements of a row of {name} are not contiguous")
     return t.data_ptr(), code, (s0 if rows > 1 else cols)
 
 
-def _vec(name, t, n, dev, dt=None):
+def _first(name, t, kind=None):
+    """(device, rows, columns, pointer, dtype code, row stride) of the matrix whose shape the others follow."""
+    if _DT is None:
+        _setup()
+    if t.dim() != 2:
+        raise ValueError(f"{name} has {t.dim()} dimensions, expected 2")
+    rows, cols = t.shape
+    code = _type(name, t, kind)
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"the elements of a row of {name} are not contiguous")
+    return t.device, rows, cols, t.data_ptr(), code, (s0 if rows > 1 else cols)
+
+
+def _vec(name, t, n, dev, kind=None):
     """(pointer, dtype code) of the n contiguous elements of t on dev (n in all, whatever the shape)."""
     if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    code = _dtypes().get(t.dtype)
-    if (code is None) if dt is None else (t.dtype != dt):
-        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
-    return t.data_ptr(), code
+    return t.data_ptr(), _type(name, t, kind)
 
 
 def _on(dev, stream, name, *args):
     """Call the entry point on dev's current stream (or `stream`), with dev current."""
-    import torch
     if dev.type != "cuda":
         raise ValueError(f"the tensors are on {dev}: a GPU is needed")
-    s = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        rc = getattr(lib(), name)(*args, s)
+    s = _raw_stream(dev.index) if stream is None else stream.cuda_stream
+    if _device() == dev.index:
+        rc = getattr(_lib or lib(), name)(*args, s)
     else:
+        import torch
         with torch.cuda.device(dev):
-            rc = getattr(lib(), name)(*args, s)
+            rc = getattr(_lib or lib(), name)(*args, s)
     if rc:
         _check(rc)
 
@@ -342,48 +361,38 @@ def route_score_topk(logits, k: int, topk_ids, topk_w, score: int = SCORE_SOFTMA
                      stream=None):
     """Top-k of softmax or sigmoid scores of logits [T, E] plus a bias [E] that counts for the choice
     only, inside the topk_group best of n_group expert groups; ids int32 and weights fp32 [T, k]."""
-    import torch
-    T, E = logits.shape
-    dev = logits.device
-    lp, ldt, ld = _mat("logits", logits, T, E, dev)
-    bp = None if bias is None else _vec("bias", bias, E, dev, torch.float32)[0]
-    ip = _vec("topk_ids", topk_ids, T * k, dev, torch.int32)[0]
-    wp = _vec("topk_w", topk_w, T * k, dev, torch.float32)[0]
+    dev, T, E, lp, ldt, ld = _first("logits", logits)
+    bp = None if bias is None else _vec("bias", bias, E, dev, F32)[0]
+    ip = _vec("topk_ids", topk_ids, T * k, dev, "int32")[0]
+    wp = _vec("topk_w", topk_w, T * k, dev, F32)[0]
     _on(dev, stream, "moe_route_score_topk", lp, ldt, ld, bp, T, E, k, score, n_group, topk_group, group_rank, renorm,
         scale, ip, wp)
 
 
 def _norm_outputs(T, H, dev, x, xq, xq_scale):
-    import torch
     xp, xdt, ldx = (None, F32, 0) if x is None else _mat("x", x, T, H, dev)
     if (xq is None) != (xq_scale is None):
         raise ValueError("xq and xq_scale go together")
     if xq is None:
         return xp, xdt, ldx, None, 0, None
-    qp, _, ldq = _mat("xq", xq, T, H, dev, torch.int8)
-    return xp, xdt, ldx, qp, ldq, _vec("xq_scale", xq_scale, T, dev, torch.float32)[0]
+    qp, _, ldq = _mat("xq", xq, T, H, dev, "int8")
+    return xp, xdt, ldx, qp, ldq, _vec("xq_scale", xq_scale, T, dev, F32)[0]
 
 
 def norm_in(h, w, eps: float, x=None, xq=None, xq_scale=None, w_offset: float = 0.0, stream=None):
     """RMS norm of the rows of h [T, H] with weight w_offset + w [H] (w None: 1), into x (fp32 or bf16),
     as int8 codes xq with one fp32 scale per row (xq_scale [T]), or both."""
-    T, H = h.shape
-    dev = h.device
-    hp, hdt, ldh = _mat("h", h, T, H, dev)
+    dev, T, H, hp, hdt, ldh = _first("h", h)
     wp, wdt = (None, F32) if w is None else _vec("w", w, H, dev)
     _on(dev, stream, "moe_norm_in", hp, hdt, ldh, T, H, wp, wdt, w_offset, eps,
         *_norm_outputs(T, H, dev, x, xq, xq_scale))
 
 
 def quantize_tokens(x, xq, xq_scale, stream=None):
-    """int8 codes and the scale of each row of x [T, K] (the rule of the int8 weight rows)."""
-    import torch
-    T, K = x.shape
-    dev = x.device
-    xp, xdt, ldx = _mat("x", x, T, K, dev)
-    qp, _, ldq = _mat("xq", xq, T, K, dev, torch.int8)
-    _on(dev, stream, "moe_quantize_tokens", xp, xdt, ldx, T, K, qp, ldq,
-        _vec("xq_scale", xq_scale, T, dev, torch.float32)[0])
+    """int8 codes and the scale of each row of x [T, K]: codes rint(x / s), s = max |x| / 127."""
+    dev, T, K, xp, xdt, ldx = _first("x", x)
+    qp, _, ldq = _mat("xq", xq, T, K, dev, "int8")
+    _on(dev, stream, "moe_quantize_tokens", xp, xdt, ldx, T, K, qp, ldq, _vec("xq_scale", xq_scale, T, dev, F32)[0])
 
 
 def norm_out(h, h_out, w_post, eps: float, out_routes=None, topk_w=None, route_pos=None, y=None, gate=None,
@@ -393,11 +402,8 @@ def norm_out(h, h_out, w_post, eps: float, out_routes=None, topk_w=None, route_p
     combine of out_routes (topk_w, route_pos [T, k] as for combine) plus y [T, H]; then, when x or xq is
     given, the next block's norm of h_out (w_next) into them.  w_post None: b is not normed.  gate
     broadcasts to [T, H].  h_out may be h."""
-    import torch
-    T, H = h.shape
-    dev = h.device
-    hp, hdt, ldh = _mat("h", h, T, H, dev)
-    op, odt, ldo = _mat("h_out", h_out, T, H, dev, h.dtype)
+    dev, T, H, hp, hdt, ldh = _first("h", h)
+    op, _, ldo = _mat("h_out", h_out, T, H, dev, hdt)
     rp = wp = pp = None
     rdt, k = F32, 0
     if out_routes is not None:
@@ -410,8 +416,8 @@ def norm_out(h, h_out, w_post, eps: float, out_routes=None, topk_w=None, route_p
         if not out_routes.is_contiguous():
             raise ValueError("out_routes is not contiguous")
         rp, rdt, _ = _mat("out_routes", out_routes, R, H, dev)
-        wp = _vec("topk_w", topk_w, R, dev, torch.float32)[0]
-        pp = _vec("route_pos", route_pos, R, dev, torch.int32)[0]
+        wp = _vec("topk_w", topk_w, R, dev, F32)[0]
+        pp = _vec("route_pos", route_pos, R, dev, "int32")[0]
     yp, ydt, ldy = (None, F32, 0) if y is None else _mat("y", y, T, H, dev)
     pw, wdt = (None, F32) if w_post is None else _vec("w_post", w_post, H, dev)
     nw = None
@@ -425,7 +431,7 @@ def norm_out(h, h_out, w_post, eps: float, out_routes=None, topk_w=None, route_p
         g = gate.expand(T, H)
         if g.device != dev:
             raise ValueError(f"gate is on {g.device}, expected {dev}")
-        gdt = _dt(g)
+        gdt = _type("gate", g, None)
         gst, gsh = g.stride()
         gst = gst if T > 1 else 0
         gp = g.data_ptr()
@@ -440,29 +446,23 @@ def norm_out(h, h_out, w_post, eps: float, out_routes=None, topk_w=None, route_p
 def matmul_i8(xq, x_scale, wq, w_scale, out, bias=None, stream=None):
     """out [T, N] = (xq [T, K] . wq [N, K]) * x_scale [T] * w_scale [N] (+ bias [N] fp32): int8 codes, exact
     int32 sums, out fp32 or bf16."""
-    import torch
-    T, K = xq.shape
+    dev, T, K, xp, _, ldx = _first("xq", xq, "int8")
     N = wq.shape[0]
-    dev = xq.device
-    xp, _, ldx = _mat("xq", xq, T, K, dev, torch.int8)
-    wp, _, ldw = _mat("wq", wq, N, K, dev, torch.int8)
+    wp, _, ldw = _mat("wq", wq, N, K, dev, "int8")
     op, odt, ldo = _mat("out", out, T, N, dev)
-    _on(dev, stream, "moe_matmul_i8", xp, ldx, _vec("x_scale", x_scale, T, dev, torch.float32)[0], wp, ldw,
-        _vec("w_scale", w_scale, N, dev, torch.float32)[0],
-        None if bias is None else _vec("bias", bias, N, dev, torch.float32)[0], T, N, K, op, odt, ldo)
+    _on(dev, stream, "moe_matmul_i8", xp, ldx, _vec("x_scale", x_scale, T, dev, F32)[0], wp, ldw,
+        _vec("w_scale", w_scale, N, dev, F32)[0], None if bias is None else _vec("bias", bias, N, dev, F32)[0], T, N, K,
+        op, odt, ldo)
 
 
 def gated_matmul_i8(xq, x_scale, wq, w_scale, act: int, out, stream=None):
     """out [T, F] = act(gate) * up of the int8 product of xq [T, K] with wq [2F, K] (gate rows, then up rows,
     as an expert's w13)."""
-    import torch
-    T, K = xq.shape
+    dev, T, K, xp, _, ldx = _first("xq", xq, "int8")
     N2 = wq.shape[0]
     if N2 % 2:
         raise ValueError(f"wq has {N2} rows: gate and up rows come in pairs")
-    dev = xq.device
-    xp, _, ldx = _mat("xq", xq, T, K, dev, torch.int8)
-    wp, _, ldw = _mat("wq", wq, N2, K, dev, torch.int8)
+    wp, _, ldw = _mat("wq", wq, N2, K, dev, "int8")
     op, odt, ldo = _mat("out", out, T, N2 // 2, dev)
-    _on(dev, stream, "moe_gated_matmul_i8", xp, ldx, _vec("x_scale", x_scale, T, dev, torch.float32)[0], wp, ldw,
-        _vec("w_scale", w_scale, N2, dev, torch.float32)[0], T, N2 // 2, K, act, op, odt, ldo)
+    _on(dev, stream, "moe_gated_matmul_i8", xp, ldx, _vec("x_scale", x_scale, T, dev, F32)[0], wp, ldw,
+        _vec("w_scale", w_scale, N2, dev, F32)[0], T, N2 // 2, K, act, op, odt, ldo)

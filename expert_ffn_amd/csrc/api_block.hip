@@ -262,9 +262,8 @@ static moe_status matmul_entry(const char* fn, bool gated, const int8_t* xq, int
         return fail(MOE_E_ARG, fn, "rows of xq and wq must be 16-byte aligned");
     if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4) || !aligned(out, esize(out_dtype)))
         return fail(MOE_E_ARG, fn, "a pointer is not aligned to its elements");
-    // one workgroup per tile of at least 64 x 64 outputs
-    if ((static_cast<int64_t>(T) + 63) / 64 * ((static_cast<int64_t>(N) + 15) / 16) >= (1ll << 22))
-        return fail(MOE_E_SHAPE, fn, "T=%d N=%d too large", T, N);
+    if (T > (1 << 24) || static_cast<int64_t>(T) * N > (1ll << 36))
+        return fail(MOE_E_SHAPE, fn, "T=%d N=%d too large (T <= 2^24, T*N <= 2^36)", T, N);
     const int64_t rows = gated ? 2ll * N : N;
     const Span in[5] = {span(xq, T, ldx, K, 1), span(wq, rows, ldw, K, 1), span(x_scale, T, 1, 1, 4),
                         span(w_scale, rows, 1, 1, 4), span(bias, N, 1, 1, 4)};

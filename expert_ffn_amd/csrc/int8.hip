@@ -10,6 +10,8 @@
 // MFMA operands: A = channels (weight rows), B = tokens, D column = token, so a
 // lane holds 4 consecutive channels of one token.  A and B take their K bytes in
 // the same order, so any fixed order of K inside an instruction is right.
+#include <algorithm>
+
 #include "block.h"
 #include "common.h"
 
@@ -18,9 +20,6 @@ namespace moe {
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(16))) int i32x16;
 
-__device__ __forceinline__ i32x4 mfma16_i8(const u32x4& a, const u32x4& b, const i32x4& c) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
-}
 __device__ __forceinline__ i32x16 mfma32_i8(const u32x4& a, const u32x4& b, const i32x16& c) {
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
@@ -37,115 +36,51 @@ __device__ __forceinline__ void lds_copy16(rsrc_t r, uint8_t* dst, uint32_t off,
         r, reinterpret_cast<__attribute__((address_space(3))) void*>(reinterpret_cast<uintptr_t>(dst)), 16, off, soff, 0, 0);
 }
 
-__device__ __forceinline__ void store_out(const MatI8Params& p, int t, int n, float v) {
-    const int64_t i = static_cast<int64_t>(t) * p.ldo + n;
-    if (p.out_dt == F32)
-        static_cast<float*>(p.out)[i] = v;
-    else
-        static_cast<uint16_t*>(p.out)[i] = f32_to_bf16(v);
-}
-
-// ------------------------------------------------------------ few tokens --
-// Weight streaming for T <= 64: a workgroup takes 16 RT channels (gated: those
-// gate rows and the matching up rows) and all tokens (TT tiles of 16); its NW
-// waves take the 64-byte pieces of K in turn and their int32 sums meet in LDS.
-// Weights go from memory to registers, U pieces requested at a time; the tokens'
-// codes come from L2.
-template <int RT, int TT, int NW, int U, bool GATED>
-__global__ __launch_bounds__(64 * NW) void matmul_i8_stream_kernel(MatI8Params p) {
-    constexpr int R = GATED ? 2 * RT : RT;   // weight row tiles
-    __shared__ i32x4 red[NW][R * TT][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * 16 * RT, l16 = lane & 15, kq = (lane >> 4) * 16;
-    const int nrow = min(16 * RT, p.N - n0);
-    const rsrc_t wr0 = rows_rsrc(p.w, p.ldw, n0, nrow, p.K);
-    const rsrc_t wr1 = rows_rsrc(p.w, p.ldw, GATED ? p.N + n0 : n0, nrow, p.K);
-    const rsrc_t xr = rows_rsrc(p.x, p.ldx, 0, p.T, p.K);
-    uint32_t wo[RT], xo[TT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) wo[r] = 16 * r + l16 < nrow ? static_cast<uint32_t>((16 * r + l16) * p.ldw + kq) : NO_LANE;
-#pragma unroll
-    for (int i = 0; i < TT; ++i) xo[i] = 16 * i + l16 < p.T ? static_cast<uint32_t>((16 * i + l16) * p.ldx + kq) : NO_LANE;
-    i32x4 acc[R][TT] = {};
-    for (int k0 = 64 * wave; k0 < p.K; k0 += 64 * NW * U) {
-        u32x4 a[U][R], b[U][TT];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = k0 + 64 * NW * u;
-            const bool ok = k + kq < p.K;   // K is a multiple of 16
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                a[u][r] = bload16s(wr0, ok ? wo[r] : NO_LANE, k);
-                if (GATED) a[u][RT + r] = bload16s(wr1, ok ? wo[r] : NO_LANE, k);
-            }
-#pragma unroll
-            for (int i = 0; i < TT; ++i) b[u][i] = bload16s(xr, ok ? xo[i] : NO_LANE, k);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int i = 0; i < TT; ++i) acc[r][i] = mfma16_i8(a[u][r], b[u][i], acc[r][i]);
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < TT; ++i) red[wave][r * TT + i][lane] = acc[r][i];
-    __syncthreads();
-    // item = (row tile, token tile, lane): 4 consecutive channels of one token
-    for (int it = tid; it < RT * TT * 64; it += 64 * NW) {
-        const int tile = it >> 6, l = it & 63;
-        i32x4 s = red[0][tile][l], s2 = {};
-#pragma unroll
-        for (int v = 1; v < NW; ++v) s += red[v][tile][l];
-        if (GATED) {
-            s2 = red[0][RT * TT + tile][l];
-#pragma unroll
-            for (int v = 1; v < NW; ++v) s2 += red[v][RT * TT + tile][l];
-        }
-        const int t = 16 * (tile % TT) + (l & 15), n = n0 + 16 * (tile / TT) + 4 * (l >> 4);
-        if (t >= p.T) continue;
-        const float sx = p.sx[t];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (n + j >= p.N) continue;
-            float v = static_cast<float>(s[j]) * sx * p.sw[n + j];
-            if (GATED)
-                v = act_fn(p.act, v) * (static_cast<float>(s2[j]) * sx * p.sw[p.N + n + j]);
-            else if (p.bias != nullptr)
-                v += p.bias[n + j];
-            store_out(p, t, n + j, v);
-        }
-    }
-}
-
-// ----------------------------------------------------------- many tokens --
 // Tiles of BN weight rows x BT tokens, WN x WT waves, each wave a block of
-// 32-row by 32-token MFMA tiles.  128-byte K steps of both operands are copied by
-// LDS DMA into two stages in turn: a step's copies are requested right after the
-// barrier that ends the reads of the stage they overwrite, and waited for one
-// step later.  A copy writes 8 rows of 128 bytes in lane order; the 16-byte
-// chunk q of row r is stored at position q ^ (r & 7), so that the 8 rows that
-// are read together fall into different banks.  Gated: the tile's first BN / 2
-// rows are gate rows and the others the matching up rows; a wave owns both rows
-// of its channels.
-template <int BN, int BT, int WN, int WT, bool GATED>
-__global__ __launch_bounds__(64 * WN * WT, 1) void matmul_i8_tile_kernel(MatI8Params p, int nt_n, int nt_t) {
+// 32-row by 32-token MFMA tiles.  K steps of 128 bytes of both operands are copied
+// by LDS DMA into a ring of NSTG stages (64-byte steps with twice the stages took
+// 6 to 20 % longer: each copy then touches 16 half lines of L2).  A copy writes 8
+// rows in lane order; the 16-byte chunk q of row r is stored at position q ^
+// swz(r).  A 16-byte read is served 16 lanes at a time, lanes 0-3, 12-15, 20-27
+// (and 4-11, 16-19, 28-31) together: swz makes their 16 rows fall into all 64 banks.
+//
+// Within a step the operands of MFMA round s + 1 are read while round s runs.
+// The step's last round runs after the barrier: at the barrier every wave holds
+// the last operands of stage c in registers and its copies of stage c + 1 have
+// landed, so the reads of stage c + 1 begin, and the copies of stage c + NSTG go
+// to the buffer of stage c, while that round is computed.
+//
+// KG > 1: KG groups of WN x WT waves, each with a ring of its own, take the K
+// steps in turn and their int32 tiles are added through LDS.
+//
+// Gated: each 32-row block holds 16 gate rows, then the up rows of the same 16
+// channels, so a lane holds both products of its channels.
+__host__ __device__ constexpr int waitcnt_vm_lds(int n) { return waitcnt_vm(n) & ~0x0F00; }   // and LDS reads to 0
+
+// 16-byte chunk q of row r is stored at position q ^ swz(r)
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 3); }
+
+template <int BN, int BT, int WN, int WT, int NSTG, int KG, bool GATED, int OT>
+__global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(MatI8Params p, int nt_n, int nt_t) {
     constexpr int NW = WN * WT, NB = BN / WN / 32, TB = BT / WT / 32;
-    constexpr int STAGE = (BN + BT) * 128, DA = BN / 8 / NW, DB = BT / 8 / NW;
+    constexpr int BK = 128, RPC = 1024 / BK, CPR = BK / 16;   // K bytes of a step, rows of a copy, chunks of a row
+    constexpr int STAGE = (BN + BT) * BK, DA = BN / RPC / NW, DB = BT / RPC / NW, CPS = DA + DB;
     constexpr int CH = GATED ? BN / 2 : BN;   // output channels per tile
-    static_assert(DA * 8 * NW == BN && DB * 8 * NW == BT && (!GATED || (NB % 2 == 0 && DA % 2 == 0)), "tile shape");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
+    constexpr int CW = CH / WN;               // of a wave
+    constexpr int RING = NSTG * STAGE, NTH = 64 * NW * KG;
+    static_assert(DA * RPC * NW == BN && DB * RPC * NW == BT && BN % 32 == 0, "tile shape");
+    static_assert(NSTG >= 2 && CPS * (NSTG - 1) <= 63, "copies in flight");
+    static_assert((KG - 1) * BN * BT * 4 <= KG * RING && 32 * CW * 4 * NW <= KG * RING, "epilogue regions");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * RING];
     __shared__ float sws[BN], sxs[BT], bs[BN];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wn = wave % WN, wt = wave / WN;
+    const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kg = wid / NW, wave = wid % NW, wn = wave % WN, wt = wave / WN;
     // XCD-aware order: workgroups go to the 8 XCDs in turn, so XCD x takes one
     // contiguous range of the tile list, which runs down 8 token tiles before it
     // goes to the next channel tile
     const int ntile = nt_n * nt_t, per = (ntile + 7) / 8;
     const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (id >= ntile || (blockIdx.x >> 3) >= per) return;
+    if (id >= ntile) return;
     constexpr int GRP = 8;
     const int g0 = id / (GRP * nt_n) * GRP, gh = min(GRP, nt_t - g0), r = id - g0 * nt_n;
     const int t0 = (g0 + r % gh) * BT, n0 = r / gh * CH;
@@ -153,104 +88,176 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void matmul_i8_tile_kernel(MatI8Pa
     const rsrc_t wr0 = rows_rsrc(p.w, p.ldw, n0, nch, p.K);
     const rsrc_t wr1 = rows_rsrc(p.w, p.ldw, GATED ? p.N + n0 : n0, nch, p.K);
     const rsrc_t xr = rows_rsrc(p.x, p.ldx, t0, ntok, p.K);
-    for (int i = tid; i < BN; i += 64 * NW) {
-        const int c = GATED && i >= CH ? i - CH : i;
-        sws[i] = c < nch ? p.sw[(GATED && i >= CH ? p.N : 0) + n0 + c] : 0.0f;
-        bs[i] = !GATED && p.bias != nullptr && c < nch ? p.bias[n0 + c] : 0.0f;
-    }
-    for (int i = tid; i < BT; i += 64 * NW) sxs[i] = i < ntok ? p.sx[t0 + i] : 0.0f;
-    // copies: this wave's rows 8 (wave + NW i) .. + 7 of each operand
-    const int sub = lane >> 3, chunk = ((lane & 7) ^ sub) * 16;
+    uint8_t* ring = lds + kg * RING;
+    // copies: this wave's rows RPC (wave + NW i) .. of each operand, lane l row l / CPR
+    auto crow = [&](int i) { return RPC * (wave + NW * i) + lane / CPR; };
+    auto chunk = [&](int i) { return ((lane % CPR) ^ swz(crow(i))) * 16; };
+    auto channel = [](int row) { return GATED ? (row >> 5) * 16 + (row & 15) : row; };   // of a tile row
+    auto is_up = [](int row) { return GATED && (row & 16); };
     uint32_t ao[DA], bo[DB];
 #pragma unroll
     for (int i = 0; i < DA; ++i) {
-        const int row = 8 * (wave + NW * i) + sub, c = GATED && row >= CH ? row - CH : row;
-        ao[i] = c < nch ? static_cast<uint32_t>(c * p.ldw + chunk) : NO_LANE;
+        const int c = channel(crow(i));
+        ao[i] = c < nch ? static_cast<uint32_t>(c * p.ldw + chunk(i)) : NO_LANE;
     }
 #pragma unroll
     for (int i = 0; i < DB; ++i) {
-        const int row = 8 * (wave + NW * i) + sub;
-        bo[i] = row < ntok ? static_cast<uint32_t>(row * p.ldx + chunk) : NO_LANE;
+        const int row = crow(i);
+        bo[i] = row < ntok ? static_cast<uint32_t>(row * p.ldx + chunk(i)) : NO_LANE;
     }
-    const int nk = (p.K + 127) / 128;
-    auto dma = [&](int c, int buf) {
-        const int k = 128 * c;
-        const bool in = k + chunk < p.K;   // the last step may end inside (K is a multiple of 16)
-#pragma unroll
-        for (int i = 0; i < DA; ++i) {
-            // copies i >= DA / 2 are the up rows of a gated tile
-            uint8_t* dst = lds + buf * STAGE + 8 * (wave + NW * i) * 128;
-            if (GATED && i >= DA / 2)
-                lds_copy16(wr1, dst, in ? ao[i] : NO_LANE, k);
+    const int nk = ((p.K + BK - 1) / BK + KG - 1) / KG;   // steps of each group (past K: zeros)
+    // copy i of stage c: weight rows (RPC of them lie on one side of a gated
+    // block), then tokens.  Chunks past K, and whole stages past the last, are zeros:
+    // nothing is read for them, and the count of copies in flight stays uniform.
+    auto copy = [&](int c, uint8_t* st, int i) {
+        const int k = BK * (c * KG + kg);
+        if (i < DA) {
+            const uint32_t o = k + chunk(i) < p.K ? ao[i] : NO_LANE;
+            uint8_t* dst = st + RPC * (wave + NW * i) * BK;
+            if (is_up(RPC * (wave + NW * i)))
+                lds_copy16(wr1, dst, o, k);
             else
-                lds_copy16(wr0, dst, in ? ao[i] : NO_LANE, k);
+                lds_copy16(wr0, dst, o, k);
+        } else {
+            const int j = i - DA;
+            lds_copy16(xr, st + (BN + RPC * (wave + NW * j)) * BK, k + chunk(j) < p.K ? bo[j] : NO_LANE, k);
         }
-#pragma unroll
-        for (int i = 0; i < DB; ++i)
-            lds_copy16(xr, lds + buf * STAGE + (BN + 8 * (wave + NW * i)) * 128, in ? bo[i] : NO_LANE, k);
     };
-    // fragments: row l & 31 of a 32-row block, chunk 2 s + (l >> 5)
+    // fragments: row l & 31 of a 32-row block (blocks start at multiples of 32), chunk 2 s + (l >> 5)
     const int l32 = lane & 31, hh = lane >> 5;
     int arow[NB], brow[TB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        if (GATED)   // first half of the blocks: gate rows, second half: up rows
-            arow[b] = (b < NB / 2 ? 0 : CH) + wn * (CH / WN) + 32 * (b % (NB / 2 > 0 ? NB / 2 : 1)) + l32;
-        else
-            arow[b] = wn * (BN / WN) + 32 * b + l32;
-    }
+    for (int b = 0; b < NB; ++b) arow[b] = wn * (BN / WN) + 32 * b + l32;
 #pragma unroll
     for (int b = 0; b < TB; ++b) brow[b] = BN + wt * (BT / WT) + 32 * b + l32;
+    u32x4 fa[2][NB], fb[2][TB];
+    auto read = [&](const uint8_t* st, int s, int set) {
+        const int co = ((2 * s + hh) ^ swz(l32)) * 16;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) fa[set][i] = *reinterpret_cast<const u32x4*>(st + arow[i] * BK + co);
+#pragma unroll
+        for (int i = 0; i < TB; ++i) fb[set][i] = *reinterpret_cast<const u32x4*>(st + brow[i] * BK + co);
+    };
     i32x16 acc[NB][TB] = {};
-    dma(0, 0);
-    for (int c = 0; c < nk; ++c) {
-        // stage c has landed (for every wave after the barrier), and the reads of
-        // stage c - 1 are over: its buffer takes stage c + 1
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-        __syncthreads();
-        if (c + 1 < nk) dma(c + 1, (c + 1) & 1);
-        const uint8_t* st = lds + (c & 1) * STAGE;
+    // Round s of a step, with its share of the copies of stage c between its MFMAs
+    // (c < 0: none).  A stage is requested over M MFMAs, from the last round of one
+    // step into the next, so that the address unit (16 cycles a copy, for all waves
+    // of the CU) works beside the MFMAs: a wave that issues its copies in one go
+    // waits for it with its MFMAs behind them (T = 512, N = 5632, K = 2816: 16.6 us,
+    // spread 14.0).  With two stages the copies are wanted a step later and start
+    // within two rounds.
+    constexpr int S = BK / 32;   // rounds of a step (even: a step starts with set 0)
+    constexpr int M = (NSTG > 2 ? S : 2) * NB * TB;
+    auto round = [&](int s, int c, uint8_t* to) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int co = ((2 * s + hh) ^ (l32 & 7)) * 16;
-            u32x4 a[NB], b[TB];
+        for (int m = 0; m < NB * TB; ++m) {
+            const int i = m / TB, j = m % TB, slot = (s + 1) % S * NB * TB + m;
+            acc[i][j] = mfma32_i8(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
+            if (c >= 0) {
 #pragma unroll
-            for (int i = 0; i < NB; ++i) a[i] = *reinterpret_cast<const u32x4*>(st + arow[i] * 128 + co);
+                for (int q = slot * CPS / M; q < (slot + 1) * CPS / M && q < CPS; ++q) copy(c, to, q);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto most = [&](const uint8_t* st, int c, uint8_t* to) {   // rounds 0 .. S - 2, each reading the next one's operands first
 #pragma unroll
-            for (int i = 0; i < TB; ++i) b[i] = *reinterpret_cast<const u32x4*>(st + brow[i] * 128 + co);
+        for (int s = 0; s + 1 < S; ++s) {
+            read(st, s + 1, (s + 1) & 1);
+            __builtin_amdgcn_sched_barrier(0);
+            round(s, c, to);
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < NSTG; ++c)
+#pragma unroll
+        for (int q = 0; q < CPS; ++q) copy(c, ring + c * STAGE, q);
+    // per-row factors, behind the first copies
+    for (int i = tid; i < BN; i += NTH) {
+        const int c = channel(i);
+        sws[i] = c < nch ? p.sw[(is_up(i) ? p.N : 0) + n0 + c] : 0.0f;
+        bs[i] = !GATED && p.bias != nullptr && c < nch ? p.bias[n0 + c] : 0.0f;
+    }
+    for (int i = tid; i < BT; i += NTH) sxs[i] = i < ntok ? p.sx[t0 + i] : 0.0f;
+    // (those loads were issued after the copies, so their wait covered every copy)
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(0));
+    __syncthreads();
+    read(ring, 0, 0);
+    most(ring, -1, ring);
+    for (int c = 0, buf = 0; c + 1 < nk; ++c) {
+        // stages up to c + NSTG - 1 have been requested: all but the last NSTG - 2
+        // of them must have landed, and the operands of step c's last round too
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(CPS * (NSTG - 2)));
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        uint8_t* done = ring + buf * STAGE;
+        buf = buf + 1 == NSTG ? 0 : buf + 1;
+        const uint8_t* st = ring + buf * STAGE;
+        read(st, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        round(S - 1, c + NSTG, done);
+        most(st, c + NSTG, done);
+    }
+    round(S - 1, -1, ring);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(0));   // the zero stages past the last have landed too
+    __syncthreads();   // the rings are free
+    if (KG > 1) {
+        int* part = reinterpret_cast<int*>(lds);
+        if (kg > 0) {
 #pragma unroll
             for (int i = 0; i < NB; ++i)
 #pragma unroll
-                for (int j = 0; j < TB; ++j) acc[i][j] = mfma32_i8(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < TB; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        *reinterpret_cast<i32x4*>(part + (((((kg - 1) * NW + wave) * NB + i) * TB + j) * 4 + v) * 256 + lane * 4) =
+                            i32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
         }
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll
+        for (int q = 1; q < KG; ++q)
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int j = 0; j < TB; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const i32x4 o = *reinterpret_cast<const i32x4*>(
+                            part + (((((q - 1) * NW + wave) * NB + i) * TB + j) * 4 + v) * 256 + lane * 4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][4 * v + e] += o[e];
+                    }
     }
-    __syncthreads();   // the stages are free: each wave transposes through its own part
     // Epilogue, 32 tokens at a time: the wave's [32 tokens][CW channels] go through
-    // LDS (16-byte chunks at position c ^ token) and leave as row pieces.
-    constexpr int CW = CH / WN, NBO = CW / 32, REG = 2 * STAGE / NW;
-    static_assert(32 * CW * 4 <= REG, "epilogue region");
-    uint8_t* my = lds + wave * REG;
-    const bool f32 = p.out_dt == F32;
-    const int es = f32 ? 4 : 2, cpr = CW * es / 16;   // 16-byte chunks per row (a power of two)
+    // LDS (16-byte chunks at position c ^ token) and leave as row pieces.  With
+    // groups, the partial sums may lie where another wave of group 0 still reads:
+    // the waves' regions start behind them.
+    constexpr int PART = KG > 1 ? (KG - 1) * BN * BT * 4 : 0;
+    static_assert(PART + 32 * CW * 4 * NW <= KG * RING, "epilogue regions");
+    uint8_t* my = lds + PART + wave * 32 * CW * 4;
+    constexpr bool f32 = OT == F32;
+    constexpr int es = f32 ? 4 : 2, cpr = CW * es / 16;   // 16-byte chunks per row (a power of two)
     const bool vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo * es % 16 == 0;
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb) {
         const int tl = wt * (BT / WT) + 32 * tb;   // first token of the block in the tile
         const float sx = sxs[tl + l32];
 #pragma unroll
-        for (int b = 0; b < NBO; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {   // channels 32 b + 8 q + 4 hh .. + 3
-                const int cl = 32 * b + 8 * q + 4 * hh, cw = wn * CW + cl;
+            for (int q = 0; q < (GATED ? 2 : 4); ++q) {   // 4 channels: tile rows rw .. rw + 3 (and up rows 16 further)
+                const int cl = (GATED ? 16 : 32) * b + 8 * q + 4 * hh, rw = wn * (BN / WN) + 32 * b + 8 * q + 4 * hh;
                 float v[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    v[j] = static_cast<float>(acc[b][tb][4 * q + j]) * sx * sws[cw + j];
+                    v[j] = static_cast<float>(acc[b][tb][4 * q + j]) * sx * sws[rw + j];
                     if (GATED)
                         v[j] = act_fn(p.act, v[j]) *
-                               (static_cast<float>(acc[NB / 2 + b < NB ? NB / 2 + b : 0][tb][4 * q + j]) * sx * sws[CH + cw + j]);
+                               (static_cast<float>(acc[b][tb][GATED ? 8 + 4 * q + j : 0]) * sx * sws[rw + 16 + j]);
                     else
-                        v[j] += bs[cw + j];
+                        v[j] += bs[rw + j];
                 }
                 if (f32) {
                     *reinterpret_cast<f32x4*>(my + l32 * CW * 4 + (((cl >> 2) ^ (l32 & (cpr - 1))) << 4)) =
@@ -262,7 +269,9 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void matmul_i8_tile_kernel(MatI8Pa
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        for (int it = lane; it < 32 * cpr; it += 64) {
+#pragma unroll 4
+        for (int i0 = 0; i0 < 32 * cpr; i0 += 64) {
+            const int it = i0 + lane;
             const int tok = it / cpr, c = it & (cpr - 1);
             const u32x4 v = *reinterpret_cast<const u32x4*>(my + tok * CW * es + ((c ^ (tok & (cpr - 1))) << 4));
             const int t = tl + tok, ch = wn * CW + c * (16 / es);
@@ -293,32 +302,64 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void matmul_i8_tile_kernel(MatI8Pa
     }
 }
 
-template <int RT, int TT, int NW, int U, bool GATED>
-static hipError_t stream(const MatI8Params& p, hipStream_t s) {
-    hipLaunchKernelGGL((matmul_i8_stream_kernel<RT, TT, NW, U, GATED>), dim3((p.N + 16 * RT - 1) / (16 * RT)),
-                       dim3(64 * NW), 0, s, p);
-    return hipGetLastError();
-}
-
-template <int BN, int BT, int WN, int WT, bool GATED>
+template <int BN, int BT, int WN, int WT, int NSTG, int KG, bool GATED>
 static hipError_t tile(const MatI8Params& p, hipStream_t s) {
     constexpr int CH = GATED ? BN / 2 : BN;
     const int nt_n = (p.N + CH - 1) / CH, nt_t = (p.T + BT - 1) / BT;
     const int per = (nt_n * nt_t + 7) / 8;
-    hipLaunchKernelGGL((matmul_i8_tile_kernel<BN, BT, WN, WT, GATED>), dim3(8 * per), dim3(64 * WN * WT), 0, s, p, nt_n,
-                       nt_t);
+    auto kn = p.out_dt == F32 ? matmul_i8_tile_kernel<BN, BT, WN, WT, NSTG, KG, GATED, F32>
+                              : matmul_i8_tile_kernel<BN, BT, WN, WT, NSTG, KG, GATED, BF16>;
+    hipLaunchKernelGGL(kn, dim3(8 * per), dim3(64 * WN * WT * KG), 0, s, p, nt_n, nt_t);
     return hipGetLastError();
+}
+
+// Which tile: the one with the smallest estimated time.  A launch of W workgroups
+// over 256 CUs takes ceil(W / 256) of them after each other, so with `steps`
+// 128-byte K steps about steps * max(alone, ceil(W / 256) * full) + fixed: `alone` is
+// the time of a step when a CU has one workgroup and waits for its copies, `full`
+// that of a CU with work in reserve.  The figures (us) are fitted to times of every
+// tile at 96 shapes (T 1 to 4096, N 704 to 8192, K 704 to 8192, both kinds); the
+// choice is then within 1 % of the best tile on average, 6 % at worst.  The ends of
+// the range: T = 16, N = 5632, K = 2816: 32 x 32 6.5 us, 64 x 64 8.3; T = 4096, N =
+// 8192, K = 4096: 32 x 32 over 400 us, 256 x 128 143, 256 x 256 123.
+struct Tile {
+    int bn, bt;
+    float alone, full, fixed;
+};
+constexpr Tile TILES[] = {
+    {32, 32, 0.09f, 0.11f, 1.4f},  {32, 64, 0.11f, 0.12f, 1.5f},   {64, 64, 0.14f, 0.17f, 2.5f},  {64, 64, 0.31f, 0.18f, 0.0f},
+    {128, 64, 0.19f, 0.33f, 0.2f}, {128, 128, 0.43f, 0.49f, 0.2f}, {256, 128, 0.50f, 0.75f, 0.5f}, {256, 256, 1.06f, 1.15f, 0.9f},
+};
+constexpr int N_TILES = sizeof(TILES) / sizeof(TILES[0]);
+
+static int pick_tile(int64_t T, int64_t rows, int K) {
+    int best = N_TILES - 1;
+    float best_us = 1e30f;
+    for (int i = 0; i < N_TILES; ++i) {
+        const Tile& c = TILES[i];
+        const int64_t W = ((rows + c.bn - 1) / c.bn) * ((T + c.bt - 1) / c.bt);
+        if (W >= (1 << 22)) continue;   // keeps every launch below 2^32 threads
+        const float us = static_cast<float>((K + 127) / 128) * std::max(c.alone, static_cast<float>((W + 255) / 256) * c.full) + c.fixed;
+        if (us < best_us) {
+            best_us = us;
+            best = i;
+        }
+    }
+    return best;
 }
 
 template <bool GATED>
 static hipError_t dispatch(const MatI8Params& p, hipStream_t s) {
-    if (p.T <= 16) return stream<1, 1, 8, 6, GATED>(p, s);
-    if (p.T <= 32) return stream<1, 2, 8, 4, GATED>(p, s);
-    if (p.T <= 64) return stream<1, 4, 8, 3, GATED>(p, s);
-    const int64_t rows = static_cast<int64_t>(p.N) * (GATED ? 2 : 1);
-    const int64_t big = ((rows + 255) / 256) * ((p.T + 255) / 256);
-    if (big >= 200) return tile<256, 256, 2, 4, GATED>(p, s);
-    return tile<128, 128, 2, 2, GATED>(p, s);
+    switch (pick_tile(p.T, static_cast<int64_t>(p.N) * (GATED ? 2 : 1), p.K)) {
+        case 0: return tile<32, 32, 1, 1, 3, 4, GATED>(p, s);
+        case 1: return tile<32, 64, 1, 2, 3, 4, GATED>(p, s);
+        case 2: return tile<64, 64, 2, 2, 4, 2, GATED>(p, s);
+        case 3: return tile<64, 64, 2, 2, 3, 1, GATED>(p, s);
+        case 4: return tile<128, 64, 2, 2, 3, 1, GATED>(p, s);
+        case 5: return tile<128, 128, 2, 4, 4, 1, GATED>(p, s);
+        case 6: return tile<256, 128, 4, 2, 3, 1, GATED>(p, s);
+        default: return tile<256, 256, 4, 2, 2, 1, GATED>(p, s);
+    }
 }
 
 hipError_t launch_matmul_i8(const MatI8Params& p, bool gated, hipStream_t s) {

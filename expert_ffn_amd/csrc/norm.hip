@@ -3,7 +3,7 @@
 // combine, the dense expert's rows, the gate, the residual and the next norm.
 //
 //   norm:   r = 1 / sqrt(mean h^2 + eps),  x = (h r) (off + w)
-//   codes:  u = h (off + w),  a = max |u|,  s = a / 127,  q = rint(u / s),
+//   codes:  u = h (off + w),  a = max |u|,  s = a fl(1 / 127),  q = rint(u / s),
 //           scale = s r: r cancels in the codes of the normed row, so they
 //           depend on no order of summation, and one pass over the row gives
 //           the sum of squares and the maximum together.
@@ -85,6 +85,10 @@ __device__ __forceinline__ void weight8(const Raw8& r, const void* w, int dt, fl
 // |v| as bits: ordered like |v|, infinities above every number and NaN above them
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// step of the codes of a row whose largest |u| has the bits `top`: one product with
+// 1 / 127 rounded to fp32, as a division by a constant is usually computed
+__device__ __forceinline__ float code_step(uint32_t top) { return __uint_as_float(top) * (1.0f / 127.0f); }
+
 // 8 codes of u at scale s (all 0 when s is 0, infinite or NaN)
 __device__ __forceinline__ u32x2 codes8(const float (&u)[8], float s) {
     u32x2 o = {0u, 0u};
@@ -153,7 +157,7 @@ __global__ __launch_bounds__(1024) void norm_in_kernel(const void* __restrict__ 
     }
     st = block_stat(st, red, o.xq != nullptr);
     const float r = NORM ? 1.0f / sqrtf(st.sum / static_cast<float>(H) + o.eps) : 1.0f;
-    const float s = __uint_as_float(st.top) / 127.0f;
+    const float s = code_step(st.top);
     if (o.xq != nullptr && threadIdx.x == 0) o.xq_scale[t] = s * r;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -318,7 +322,7 @@ __global__ __launch_bounds__(1024) void norm_out_kernel(NormOutParams p) {
     if (!p.next) return;
     st = block_stat(st, red[1], codes);
     r = 1.0f / sqrtf(st.sum / static_cast<float>(H) + p.n.eps);
-    const float s = __uint_as_float(st.top) / 127.0f;
+    const float s = code_step(st.top);
     if (codes && threadIdx.x == 0) p.n.xq_scale[t] = s * r;
 #pragma unroll
     for (int i = 0; i < C; ++i) {

@@ -457,7 +457,7 @@ moe_status moe_route_score_topk(const void* logits, int32_t logits_dtype, int64_
  *   x   (device [T, H], fp32 or bf16, or NULL) the normed rows
  *   xq  (device int8 [T, H], or NULL) their codes for the 8-bit products, and
  *       xq_scale (device fp32 [T]): with u = h * (w_offset + w) (fp32, each
- *       operation rounded), a = max |u|, s = a / 127:
+ *       operation rounded), a = max |u|, s = a * (1 / 127 rounded to fp32):
  *       xq = clamp(rint(u / s), -127, 127) (0 if s = 0), xq_scale = s * r.
  *       The codes are those of the normed row (r > 0 cancels), and do not
  *       depend on the rounding of r.  A row that holds a NaN or an infinity has
@@ -497,10 +497,13 @@ moe_status moe_norm_out(const void* out_routes, int32_t out_dtype, const float* 
                         void* x, int32_t x_dtype, int64_t ldx, int8_t* xq, int64_t ldq, float* xq_scale, void* stream);
 
 /*
- * Codes of activations: for each row of x (device [T, K], fp32 or bf16) the rule
- * of MOE_W_INT8_ROW (moe_quantize): a = max |x|, s = a / 127, xq = clamp(rint(x /
- * s), -127, 127), xq_scale = s.  A row that holds a NaN or an infinity gets codes
- * 0 and that scale, so its products are NaN.  K a multiple of 8 up to 32768.
+ * Codes of activations: for each row of x (device [T, K], fp32 or bf16)
+ *   a = max |x|,  s = a * (1 / 127 rounded to fp32),
+ *   xq = clamp(rint(x / s), -127, 127) (0 if s = 0),  xq_scale = s
+ * in fp32: the rule of MOE_W_INT8_ROW but for the step, which moe_quantize divides
+ * (s differs by at most one unit in the last place).  A row that holds a NaN or an
+ * infinity gets codes 0 and that scale, so its products are NaN.  K a multiple of 8
+ * up to 32768.
  */
 moe_status moe_quantize_tokens(const void* x, int32_t x_dtype, int64_t ldx, int32_t T, int32_t K, int8_t* xq, int64_t ldq,
                                float* xq_scale, void* stream);
@@ -517,7 +520,7 @@ moe_status moe_quantize_tokens(const void* x, int32_t x_dtype, int64_t ldx, int3
  *   out[t][f] = act(g[t][f]) * u[t][f]   (device [T, F]).
  * The integer sums are exact; the rest is fp32, rounded once to out's type.
  * K a multiple of 16 up to 131056, rows of xq and wq 16-byte aligned with strides
- * up to 2^22; any T and N.  T = 0 enqueues nothing.
+ * up to 2^22; T and N up to 2^24, T*N up to 2^36.  T = 0 enqueues nothing.
  */
 moe_status moe_matmul_i8(const int8_t* xq, int64_t ldx, const float* x_scale, const int8_t* wq, int64_t ldw,
                          const float* w_scale, const float* bias, int32_t T, int32_t N, int32_t K, void* out,

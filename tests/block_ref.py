@@ -81,7 +81,7 @@ def codes(u):
     u = np.asarray(u, np.float32)
     with np.errstate(all="ignore"):
         a = np.abs(u).max(axis=1, keepdims=True)
-        s = (a / np.float32(127.0)).astype(np.float32)
+        s = (a * np.float32(1.0 / 127.0)).astype(np.float32)
         ok = (s > 0) & np.isfinite(s)
         q = np.where(ok, np.clip(np.rint((u / s).astype(np.float32)), -127, 127), 0)
     return q.astype(np.int8), s[:, 0]

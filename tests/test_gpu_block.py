@@ -223,12 +223,13 @@ def test_quantize_tokens(L, T, K, xt):
     check_padding(qbuf, K, 55)
     qw, s = ref.codes(x.float().cpu().numpy())
     assert np.array_equal(q.cpu().numpy(), qw) and np.array_equal(sc.cpu().numpy(), s)
-    if xt == BF16 and T <= 16:   # the same bytes as the weight quantiser writes
+    if xt == BF16 and T <= 16:   # the weight quantiser's rule but for the rounding of the step
         xc = x.contiguous()
         q2 = torch.empty(T, K, dtype=torch.int8, device="cuda")
         s2 = torch.empty(T, device="cuda")
         L.quantize(L.W_INT8_ROW, xc.view(torch.int16), q2, s2)
-        assert torch.equal(q2, q.contiguous()) and torch.equal(s2, sc)
+        close(f64(sc), f64(s2), 2 * U * f64(s2), "step")
+        assert (q2.int() - q.int()).abs().max() <= 1
 
 
 @pytest.mark.parametrize("T,H,k,rt,yt,ht,gate,off,drop,nxt", [
