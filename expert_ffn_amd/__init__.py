@@ -287,29 +287,32 @@ _raw_stream = _device = None
 
 
 def _setup():
-    """torch's type codes and its raw-stream and device queries (torch is imported on first use only; the
-    public current_stream() builds a Stream object, 1.8 us of a call that takes 5)."""
+    """torch's type codes and its queries of the current device and its raw stream (torch is imported on
+    first use only).  The public current_stream() and current_device() cost 2 us of a call that takes 6."""
     global _DT, _raw_stream, _device
     import torch
-    _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    lib()
+    _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: "int8", torch.int32: "int32"}
 
 
-def _type(name, t, kind):
-    """fp32 or bf16 (kind None): its code; else t must be of that kind."""
-    code = _DT.get(t.dtype)
-    if code is None or (code not in (F32, BF16) if kind is None else code != kind):
-        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
-    return code
+def _type_error(name, t):
+    return TypeError(f"unsupported dtype {t.dtype} of {name}")
+
+
+def _where_error(name, t, dev):
+    return ValueError(f"{name} is on {t.device}, expected GPU {dev}")
 
 
 def _mat(name, t, rows, cols, dev, kind=None):
-    """(pointer, dtype code, row stride) of t [rows, cols] on dev."""
+    """(pointer, dtype code, row stride) of t [rows, cols] on GPU dev; kind None: fp32 or bf16, else that type."""
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    code = _type(name, t, kind)
+    if t.get_device() != dev:
+        raise _where_error(name, t, dev)
+    code = _DT.get(t.dtype)
+    if (code != kind) if kind is not None else (code != F32 and code != BF16):
+        raise _type_error(name, t)
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
         raise ValueError(f"the elements of a row of {name} are not contiguous")
@@ -317,41 +320,46 @@ def _mat(name, t, rows, cols, dev, kind=None):
 
 
 def _first(name, t, kind=None):
-    """(device, rows, columns, pointer, dtype code, row stride) of the matrix whose shape the others follow."""
-    if _DT is None:
-        _setup()
+    """(GPU, rows, columns, pointer, dtype code, row stride) of the matrix whose shape the others follow."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} is on {t.device}: a GPU is needed")
     if t.dim() != 2:
         raise ValueError(f"{name} has {t.dim()} dimensions, expected 2")
+    if _DT is None:
+        _setup()
     rows, cols = t.shape
-    code = _type(name, t, kind)
-    s0, s1 = t.stride()
-    if s1 != 1 and cols > 1:
-        raise ValueError(f"the elements of a row of {name} are not contiguous")
-    return t.device, rows, cols, t.data_ptr(), code, (s0 if rows > 1 else cols)
+    return (dev, rows, cols) + _mat(name, t, rows, cols, dev, kind)
 
 
 def _vec(name, t, n, dev, kind=None):
-    """(pointer, dtype code) of the n contiguous elements of t on dev (n in all, whatever the shape)."""
+    """(pointer, dtype code) of the n contiguous elements of t on GPU dev (n in all, whatever the shape)."""
     if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != dev:
+        raise _where_error(name, t, dev)
+    code = _DT.get(t.dtype)
+    if (code != kind) if kind is not None else (code != F32 and code != BF16):
+        raise _type_error(name, t)
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
-    return t.data_ptr(), _type(name, t, kind)
+    return t.data_ptr(), code
 
 
-def _on(dev, stream, name, *args):
-    """Call the entry point on dev's current stream (or `stream`), with dev current."""
-    if dev.type != "cuda":
-        raise ValueError(f"the tensors are on {dev}: a GPU is needed")
-    s = _raw_stream(dev.index) if stream is None else stream.cuda_stream
-    if _device() == dev.index:
-        rc = getattr(_lib or lib(), name)(*args, s)
+def _on(dev, stream, fn, *args):
+    """Call fn on GPU dev's current stream (or `stream`, one of that GPU's), with dev current."""
+    if stream is None:
+        s = _raw_stream(dev)
+    else:
+        if stream.device_index != dev:
+            raise ValueError(f"the stream belongs to GPU {stream.device_index}, the tensors are on GPU {dev}")
+        s = stream.cuda_stream
+    if _device() == dev:
+        rc = fn(*args, s)
     else:
         import torch
         with torch.cuda.device(dev):
-            rc = getattr(_lib or lib(), name)(*args, s)
+            rc = fn(*args, s)
     if rc:
         _check(rc)
 
@@ -365,7 +373,7 @@ def route_score_topk(logits, k: int, topk_ids, topk_w, score: int = SCORE_SOFTMA
     bp = None if bias is None else _vec("bias", bias, E, dev, F32)[0]
     ip = _vec("topk_ids", topk_ids, T * k, dev, "int32")[0]
     wp = _vec("topk_w", topk_w, T * k, dev, F32)[0]
-    _on(dev, stream, "moe_route_score_topk", lp, ldt, ld, bp, T, E, k, score, n_group, topk_group, group_rank, renorm,
+    _on(dev, stream, _lib.moe_route_score_topk, lp, ldt, ld, bp, T, E, k, score, n_group, topk_group, group_rank, renorm,
         scale, ip, wp)
 
 
@@ -384,7 +392,7 @@ def norm_in(h, w, eps: float, x=None, xq=None, xq_scale=None, w_offset: float = 
     as int8 codes xq with one fp32 scale per row (xq_scale [T]), or both."""
     dev, T, H, hp, hdt, ldh = _first("h", h)
     wp, wdt = (None, F32) if w is None else _vec("w", w, H, dev)
-    _on(dev, stream, "moe_norm_in", hp, hdt, ldh, T, H, wp, wdt, w_offset, eps,
+    _on(dev, stream, _lib.moe_norm_in, hp, hdt, ldh, T, H, wp, wdt, w_offset, eps,
         *_norm_outputs(T, H, dev, x, xq, xq_scale))
 
 
@@ -392,7 +400,7 @@ def quantize_tokens(x, xq, xq_scale, stream=None):
     """int8 codes and the scale of each row of x [T, K]: codes rint(x / s), s = max |x| / 127."""
     dev, T, K, xp, xdt, ldx = _first("x", x)
     qp, _, ldq = _mat("xq", xq, T, K, dev, "int8")
-    _on(dev, stream, "moe_quantize_tokens", xp, xdt, ldx, T, K, qp, ldq, _vec("xq_scale", xq_scale, T, dev, F32)[0])
+    _on(dev, stream, _lib.moe_quantize_tokens, xp, xdt, ldx, T, K, qp, ldq, _vec("xq_scale", xq_scale, T, dev, F32)[0])
 
 
 def norm_out(h, h_out, w_post, eps: float, out_routes=None, topk_w=None, route_pos=None, y=None, gate=None,
@@ -428,18 +436,27 @@ def norm_out(h, h_out, w_post, eps: float, out_routes=None, topk_w=None, route_p
         wdt = ndt
     gp, gdt, gst, gsh = None, F32, 0, 0
     if gate is not None:
-        g = gate.expand(T, H)
-        if g.device != dev:
-            raise ValueError(f"gate is on {g.device}, expected {dev}")
-        gdt = _type("gate", g, None)
-        gst, gsh = g.stride()
-        gst = gst if T > 1 else 0
-        gp = g.data_ptr()
+        # broadcast by hand: gate.expand() alone takes 2 us
+        nd = gate.dim()
+        gr, gc = (1,) * (2 - nd) + tuple(gate.shape) if nd <= 2 else (0, 0)
+        if (gr != 1 and gr != T) or (gc != 1 and gc != H):
+            raise ValueError(f"gate has shape {tuple(gate.shape)}, which does not broadcast to {(T, H)}")
+        if gate.get_device() != dev:
+            raise _where_error("gate", gate, dev)
+        gdt = _DT.get(gate.dtype)
+        if gdt != F32 and gdt != BF16:
+            raise _type_error("gate", gate)
+        st = gate.stride()
+        if gr > 1:
+            gst = st[0]
+        if gc > 1:
+            gsh = st[-1]
+        gp = gate.data_ptr()
     outs = _norm_outputs(T, H, dev, x, xq, xq_scale)
     nxt = int(x is not None or xq is not None)
     if w_next is not None and not nxt:
         raise ValueError("w_next is given, but neither x nor xq to write the next norm into")
-    _on(dev, stream, "moe_norm_out", rp, rdt, wp, pp, k, yp, ydt, ldy, T, H, pw, wdt, w_offset, eps, gp, gdt, gst, gsh,
+    _on(dev, stream, _lib.moe_norm_out, rp, rdt, wp, pp, k, yp, ydt, ldy, T, H, pw, wdt, w_offset, eps, gp, gdt, gst, gsh,
         block_scale, res_scale, hp, hdt, ldh, op, ldo, nxt, nw, *outs)
 
 
@@ -450,7 +467,7 @@ def matmul_i8(xq, x_scale, wq, w_scale, out, bias=None, stream=None):
     N = wq.shape[0]
     wp, _, ldw = _mat("wq", wq, N, K, dev, "int8")
     op, odt, ldo = _mat("out", out, T, N, dev)
-    _on(dev, stream, "moe_matmul_i8", xp, ldx, _vec("x_scale", x_scale, T, dev, F32)[0], wp, ldw,
+    _on(dev, stream, _lib.moe_matmul_i8, xp, ldx, _vec("x_scale", x_scale, T, dev, F32)[0], wp, ldw,
         _vec("w_scale", w_scale, N, dev, F32)[0], None if bias is None else _vec("bias", bias, N, dev, F32)[0], T, N, K,
         op, odt, ldo)
 
@@ -464,5 +481,5 @@ def gated_matmul_i8(xq, x_scale, wq, w_scale, act: int, out, stream=None):
         raise ValueError(f"wq has {N2} rows: gate and up rows come in pairs")
     wp, _, ldw = _mat("wq", wq, N2, K, dev, "int8")
     op, odt, ldo = _mat("out", out, T, N2 // 2, dev)
-    _on(dev, stream, "moe_gated_matmul_i8", xp, ldx, _vec("x_scale", x_scale, T, dev, F32)[0], wp, ldw,
+    _on(dev, stream, _lib.moe_gated_matmul_i8, xp, ldx, _vec("x_scale", x_scale, T, dev, F32)[0], wp, ldw,
         _vec("w_scale", w_scale, N2, dev, F32)[0], T, N2 // 2, K, act, op, odt, ldo)

@@ -40,7 +40,10 @@ def route_score(logits, k, sigmoid, bias=None, n_group=1, topk_group=1, top2=Fal
                 if m == -np.inf or np.isnan(m):
                     e = np.zeros(E)
                 s = e / e.sum() if e.sum() > 0 else e
-            c = s + (0.0 if bias is None else np.asarray(bias, np.float64))
+            if bias is None and not (top2 and topk_group < n_group):
+                c = row                      # the order is that of the logits
+            else:
+                c = s + (0.0 if bias is None else np.asarray(bias, np.float64))
             c = np.where(nan, np.nan, c)
             # order: numbers by value, NaN after them, equal ones by id
             def order(v, idx):

@@ -123,6 +123,30 @@ def test_route_score_ties_and_specials(L):
     assert ids[0].tolist() == [1, 3, 4, 5]
 
 
+@pytest.mark.parametrize("sigmoid", [0, 1])
+def test_route_score_close_scores(L, sigmoid):
+    """Scores whose differences with the bias lie below 32-bit rounding: the choice is the 64-bit one."""
+    g = gen(77)
+    T, E = 257, 128
+    for top2, G, keep in ((0, 1, 1), (0, 8, 3), (1, 8, 3)):
+        base = normal(g, T, 1)
+        logits = base + 2e-7 * torch.randint(-40, 41, (T, E), generator=g, device="cuda").float()
+        b = (0.5 + 1e-8 * torch.randint(0, 16, (E,), generator=g, device="cuda").float())
+        b[::9] -= 0.25
+        ids, w = run_route(L, logits, 8, bias=b, score=sigmoid, n_group=G, topk_group=keep, group_rank=top2)
+        want_ids, want_w = ref.route_score(f64(logits), 8, sigmoid, f64(b), G, keep, top2)
+        # 64-bit scores that agree to 1e-15 may order either way between two programs
+        same = ids == want_ids
+        if not same.all():
+            l = f64(logits)
+            s = 1 / (1 + np.exp(-l)) if sigmoid else np.exp(l - l.max(1, keepdims=True))
+            s = s if sigmoid else s / s.sum(1, keepdims=True)
+            c = s + f64(b)
+            d = np.abs(np.take_along_axis(c, ids, 1) - np.take_along_axis(c, want_ids, 1))
+            assert (d[~same] <= 1e-15).all(), (top2, G, d.max())
+        assert same.mean() > 0.95
+
+
 def test_route_score_strided_rows(L):
     g = gen(3)
     for dt in (F32, BF16):
