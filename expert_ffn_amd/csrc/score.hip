@@ -1,4 +1,4 @@
-// Router top-k over scores (moe_route_score_topk), one wavefront per token.
+// Router top-k over scores (moe_route_score_topk).
 //
 //   s = softmax(l) or 1 / (1 + exp(-l));  c = s + bias;  the topk_group best of
 //   the n_group groups by their largest c or the sum of their two largest; the k
@@ -8,14 +8,14 @@
 // The choice is that of 64-bit scores: 32-bit rounding loses differences that
 // decide, and two programs that round differently choose different experts.  But
 // 64-bit exponentials and keys of every expert cost three times the instructions,
-// and a wave is bound by instructions here (T = 16383, E = 160: 30 us, 6 MB).  So:
+// and a wave is bound by instructions here (T = 16383, E = 160, 6 MB of logits: 30 us
+// in 64 bits, 10 as below).  So:
 //   - without a bias the scores order like the logits, and the logits are compared;
 //   - else the scores are taken in 32 bits with a bound on their error.  Where
 //     every gap that decides (between groups, between consecutive choices and the
 //     first one left out) exceeds twice the bound, the 64-bit choice is the same;
 //   - where one does not, the token is chosen again in 64 bits.
 // The weights of the k chosen are 64-bit always.
-// Lane l holds experts l + 64 s (s < NPL).
 #include "block.h"
 #include "common.h"
 #include "route.h"
@@ -115,13 +115,51 @@ __device__ __forceinline__ uint64_t best_groups(const K* key, int G, int keep) {
 // an integer, far more than its rounding
 __device__ __forceinline__ int group_of(int e, float inv) { return static_cast<int>((static_cast<float>(e) + 0.5f) * inv); }
 
+// LDS of one wave
 template <int NPL>
-__global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
-    __shared__ double cs[4][64 * NPL];   // c of the token (fp32 or fp64)
-    __shared__ uint64_t gk[4][SCORE_MAX_GROUPS];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int t = blockIdx.x * 4 + wave;
-    if (t >= p.T) return;   // wave-uniform; the kernel has no workgroup barrier
+struct ScoreLds {
+    double c[64 * NPL];                // c of the token (fp32 or fp64)
+    uint64_t g[SCORE_MAX_GROUPS];      // group ranks
+};
+
+__device__ __forceinline__ float ord_value(uint32_t o) {   // the number of an order image of a number
+    return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+// Errors of the 32-bit scores, U = 2^-24.  An exponential e^-x has its argument off
+// by x U (the product with log2 e; a softmax's v - m by x U more) and errs by 2 U
+// itself.  Sigmoid s = 1 / (1 + e): s (1 - s) (x + 2) U <= 0.75 U, the sum and the
+// division U each: below 3 U.  Softmax e / sum: with the mean of x under the
+// weights at most ln 512, the sum errs by (2 * 6.3 + 2 + 14 additions) U of itself,
+// the division and product by 3 U more, and s x <= 0.4: below (1 + 34 s) U.  A sum
+// with a bias rounds by U of the result.
+constexpr float SU = 5.9604645e-8f;
+__device__ __forceinline__ float score_err(int sigmoid, float smax) { return sigmoid ? 3.0f * SU : (1.0f + 34.0f * smax) * SU; }
+// Whether a > b in 32 bits settles the order in 64, each off by at most err and U of
+// its size.  False for NaN.
+__device__ __forceinline__ bool settled(float a, float b, float err) {
+    return a - b > 2.01f * (err + SU * fmaxf(fabsf(a), fabsf(b)));
+}
+// |c| of a finite c (an infinite one is exact)
+__device__ __forceinline__ float finite_size(float c) { return fabsf(c) < __builtin_inff() ? fabsf(c) : 0.0f; }
+// the scores order like the logits, and nothing adds them up
+__device__ __forceinline__ bool by_logits(const ScoreRouteParams& p) {
+    return p.bias == nullptr && !(p.topk_group < p.n_group && p.top2);
+}
+__device__ __forceinline__ float load_logit(const ScoreRouteParams& p, int t, int e) {
+    const int64_t i = static_cast<int64_t>(t) * p.ld + e;
+    return p.logits_dt == F32 ? static_cast<const float*>(p.logits)[i]
+                              : bf16_to_f32(static_cast<const uint16_t*>(p.logits)[i]);
+}
+// score in 32 bits before a softmax's division; NaN scores 0
+__device__ __forceinline__ float score32(float v, float m, int sigmoid) {
+    const float s = sigmoid ? 1.0f / (1.0f + __expf(-v)) : (v == m ? 1.0f : __expf(v - m));
+    return v == v && !(m == -__builtin_inff()) ? s : 0.0f;
+}
+
+// One token on one wave; lane l holds experts l + 64 s (s < NPL).
+template <int NPL>
+__device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, ScoreLds<NPL>& L) {
+    const int lane = threadIdx.x & 63;
     const int E = p.E, G = p.n_group, size = E / G;
     const bool grouped = p.topk_group < G;
     const float inv_size = 1.0f / static_cast<float>(size);
@@ -129,12 +167,10 @@ __global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
 #pragma unroll
     for (int s = 0; s < NPL; ++s) {
         const int e = lane + 64 * s;
-        const int64_t i = static_cast<int64_t>(t) * p.ld + e;
         val[s] = __builtin_nanf("");
         bias[s] = 0.0f;
         if (e < E) {
-            val[s] = p.logits_dt == F32 ? static_cast<const float*>(p.logits)[i]
-                                        : bf16_to_f32(static_cast<const uint16_t*>(p.logits)[i]);
+            val[s] = load_logit(p, t, e);
             if (p.bias != nullptr) bias[s] = p.bias[e];
         }
     }
@@ -145,17 +181,14 @@ __global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
 #pragma unroll
         for (int s = 0; s < NPL; ++s) top = max(top, logit_ord(val[s]));
         top = __builtin_amdgcn_readfirstlane(wave_max_u32(top));
-        m = top <= 1u ? __builtin_nanf("") : __uint_as_float((top & 0x80000000u) ? (top & 0x7FFFFFFFu) : ~top);
+        m = top <= 1u ? __builtin_nanf("") : ord_value(top);
     }
-    const bool by_logit = p.bias == nullptr && !(grouped && p.top2);
-    float* cf = reinterpret_cast<float*>(cs[wave]);
-    uint32_t* gu = reinterpret_cast<uint32_t*>(gk[wave]);
+    const bool by_logit = by_logits(p);
+    float* cf = reinterpret_cast<float*>(L.c);
+    uint32_t* gu = reinterpret_cast<uint32_t*>(L.g);
 
-    // --- 32 bits.  U = 2^-24.  A score errs by less than 32 U: an exponential by
-    // the rounding of its argument (|x| U, times e^-|x| at most 0.4 U) and 3 U, a
-    // softmax sum of up to 512 terms by (8 + 6 additions) U more, the division by
-    // 2 U; the sum with the bias rounds once more, by U of the result.
-    float c[NPL];
+    // --- 32 bits
+    float c[NPL], err = 0.0f;
     if (by_logit) {
 #pragma unroll
         for (int s = 0; s < NPL; ++s) c[s] = val[s];
@@ -163,22 +196,20 @@ __global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
         float sum = 0.0f;
 #pragma unroll
         for (int s = 0; s < NPL; ++s) {
-            const float v = val[s];
-            c[s] = p.sigmoid ? 1.0f / (1.0f + __expf(-v)) : (v == m ? 1.0f : __expf(v - m));
-            if (!(v == v) || m == -__builtin_inff()) c[s] = 0.0f;
+            c[s] = score32(val[s], m, p.sigmoid);
             sum += c[s];
         }
         if (!p.sigmoid) {
             sum = wave_sum_f32(sum);
-            sum = sum > 0.0f ? 1.0f / sum : 0.0f;
+            sum = sum > 0.0f ? 1.0f / sum : 0.0f;   // the largest score too
         }
+        err = score_err(p.sigmoid, sum);
 #pragma unroll
         for (int s = 0; s < NPL; ++s) {
             c[s] = (p.sigmoid ? c[s] : c[s] * sum) + bias[s];
             if (!(val[s] == val[s])) c[s] = __builtin_nanf("");
         }
     }
-    constexpr float U = 5.9604645e-8f;
     bool sure = true;
     uint32_t key[NPL];
 #pragma unroll
@@ -187,7 +218,7 @@ __global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
 #pragma unroll
         for (int s = 0; s < NPL; ++s) cf[lane + 64 * s] = c[s] == c[s] ? c[s] : -__builtin_inff();
         lds_wave_sync();
-        float* gf = reinterpret_cast<float*>(gk[wave]) + SCORE_MAX_GROUPS;
+        float* gf = reinterpret_cast<float*>(L.g) + SCORE_MAX_GROUPS;
         group_top2<float>(cf, G, size, -__builtin_inff(), gf, p.top2);
         lds_wave_sync();
         const float mine = gf[lane < G ? lane : 0];
@@ -199,9 +230,14 @@ __global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
             // lowest kept and highest dropped rank, as order images
             const uint32_t im = logit_ord(mine);
             const uint32_t lo = ~wave_max_u32(in ? ~im : 0u), hi = wave_max_u32(out ? im : 0u);
-            const float fl = __uint_as_float((lo & 0x80000000u) ? (lo & 0x7FFFFFFFu) : ~lo);
-            const float fh = __uint_as_float((hi & 0x80000000u) ? (hi & 0x7FFFFFFFu) : ~hi);
-            sure = fl - fh > 2.0f * (66.0f * U + 4.0f * U * fmaxf(fabsf(fl), fabsf(fh)));   // two scores each; false for NaN
+            float two = err;   // of a group's rank: one c, or two and their sum
+            if (p.top2) {
+                float cmax = 0.0f;
+#pragma unroll
+                for (int s = 0; s < NPL; ++s) cmax = fmaxf(cmax, finite_size(c[s]));
+                two = 2.0f * err + 4.0f * SU * __uint_as_float(wave_max_u32(__float_as_uint(cmax)));
+            }
+            sure = settled(ord_value(lo), ord_value(hi), two);
         }
 #pragma unroll
         for (int s = 0; s < NPL; ++s)
@@ -239,9 +275,7 @@ __global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
     if (!by_logit) {
         // lane j < k: the gap to the next one (lane k holds the first left out)
         const uint32_t next = __shfl_down(my_key, 1, 64);
-        const float a = __uint_as_float((my_key & 0x80000000u) ? (my_key & 0x7FFFFFFFu) : ~my_key);
-        const float b = __uint_as_float((next & 0x80000000u) ? (next & 0x7FFFFFFFu) : ~next);
-        const bool ok = lane >= p.k || next == 0u || a - b > 2.0f * (32.0f * U + 2.0f * U * fmaxf(fabsf(a), fabsf(b)));
+        const bool ok = lane >= p.k || next == 0u || settled(ord_value(my_key), ord_value(next), err);
         sure = sure && __ballot(!ok) == 0ull;
     }
 
@@ -259,7 +293,7 @@ __global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
     if (!sure) {
         // --- 64 bits
         uint64_t key64[NPL];
-        double* cd = cs[wave];
+        double* cd = L.c;
         lds_wave_sync();   // the 32-bit values have been read
 #pragma unroll
         for (int s = 0; s < NPL; ++s) {
@@ -272,14 +306,14 @@ __global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
         }
         if (grouped) {
             lds_wave_sync();
-            double* gd = reinterpret_cast<double*>(gk[wave]);
+            double* gd = reinterpret_cast<double*>(L.g);
             group_top2<double>(cd, G, size, -__builtin_inf(), gd, p.top2);
             lds_wave_sync();
             const double mine = gd[lane < G ? lane : 0];
             lds_wave_sync();
-            if (lane < G) gk[wave][lane] = score_key(mine);
+            if (lane < G) L.g[lane] = score_key(mine);
             lds_wave_sync();
-            const uint64_t kept = best_groups(gk[wave], G, p.topk_group);
+            const uint64_t kept = best_groups(L.g, G, p.topk_group);
 #pragma unroll
             for (int s = 0; s < NPL; ++s)
                 if (!((kept >> (group_of(lane + 64 * s, inv_size) & 63)) & 1ull)) key64[s] = 0ull;
@@ -323,8 +357,213 @@ __global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
     }
 }
 
+template <int NPL>
+__global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
+    __shared__ ScoreLds<NPL> lds[4];
+    const int wave = threadIdx.x >> 6, t = blockIdx.x * 4 + wave;
+    if (t >= p.T) return;   // wave-uniform; the kernel has no workgroup barrier
+    score_token<NPL>(p, t, lds[wave]);
+}
+
+// Reductions over the 16 lanes of a row (every lane gets the result).
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    v = max(v, dpp_u32<DPP_QUAD_1032>(v));
+    v = max(v, dpp_u32<DPP_QUAD_2301>(v));
+    v = max(v, dpp_u32<DPP_ROW_HALF_MIRROR>(v));
+    return max(v, dpp_u32<DPP_ROW_MIRROR>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+    v += __uint_as_float(dpp_u32<DPP_QUAD_1032>(__float_as_uint(v)));
+    v += __uint_as_float(dpp_u32<DPP_QUAD_2301>(__float_as_uint(v)));
+    v += __uint_as_float(dpp_u32<DPP_ROW_HALF_MIRROR>(__float_as_uint(v)));
+    return v + __uint_as_float(dpp_u32<DPP_ROW_MIRROR>(__float_as_uint(v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+    return __longlong_as_double(static_cast<long long>(dpp_u64<CTRL>(static_cast<uint64_t>(__double_as_longlong(v)))));
+}
+__device__ __forceinline__ double row_sum(double v) {
+    v += dpp_f64<DPP_QUAD_1032>(v);
+    v += dpp_f64<DPP_QUAD_2301>(v);
+    v += dpp_f64<DPP_ROW_HALF_MIRROR>(v);
+    return v + dpp_f64<DPP_ROW_MIRROR>(v);
+}
+
+// Many tokens: four to a wave, 16 lanes each, lane r with experts r + 16 s.  The
+// same steps on rows; one instruction serves four tokens, at the price of longer
+// rounds (a lane looks through 4 times the experts), so it is for launches that
+// fill the chip: by logits from 4096 tokens on (E = 128, k = 8: 4096 tokens 6.3 us
+// either way, 8192 8.2 -> 6.3, 65536 43.9 -> 22.5), with 32-bit scores from 12288
+// on (E = 128: 8192 10.8 against 11.8, 16384 17.4 -> 14.4, 65536 53.9 -> 33.1).
+// A token that is not settled in 32 bits is left to score_token.
+// E <= 256, at most 16 groups, k <= 15.
+template <int VPL>
+struct RowLds {
+    float c[4][16 * VPL];
+    uint32_t g[4][16];
+    float f[4][16];
+};
+constexpr int ROW_T_LOGITS = 4096, ROW_T_SCORES = 12288;
+constexpr int ROW_E_MAX = 256, ROW_G_MAX = 16, ROW_K_MAX = 15;
+
+template <int VPL>
+__global__ __launch_bounds__(256) void route_score_row_kernel(ScoreRouteParams p) {
+    constexpr int NPL = (VPL + 3) / 4;
+    __shared__ union Lds {
+        RowLds<VPL> row;
+        ScoreLds<NPL> one;
+    } lds[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane >> 4, r = lane & 15;
+    const int t0 = (blockIdx.x * 4 + wave) * 4;
+    if (t0 >= p.T) return;   // wave-uniform; the kernel has no workgroup barrier
+    const bool live = t0 + row < p.T;
+    const int t = live ? t0 + row : p.T - 1;
+    const int E = p.E, G = p.n_group, size = E / G, k = p.k;
+    const bool grouped = p.topk_group < G, by_logit = by_logits(p);
+    const float inv_size = 1.0f / static_cast<float>(size);
+    RowLds<VPL>& L = lds[wave].row;
+    float val[VPL], c[VPL], err = 0.0f;
+#pragma unroll
+    for (int s = 0; s < VPL; ++s) val[s] = r + 16 * s < E ? load_logit(p, t, r + 16 * s) : __builtin_nanf("");
+    float m = 0.0f;
+    if (!p.sigmoid) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int s = 0; s < VPL; ++s) top = max(top, logit_ord(val[s]));
+        top = row_max(top);
+        m = top <= 1u ? __builtin_nanf("") : ord_value(top);
+    }
+    if (by_logit) {
+#pragma unroll
+        for (int s = 0; s < VPL; ++s) c[s] = val[s];
+    } else {
+        float sum = 0.0f;
+#pragma unroll
+        for (int s = 0; s < VPL; ++s) {
+            c[s] = score32(val[s], m, p.sigmoid);
+            sum += c[s];
+        }
+        sum = row_sum(sum);
+        const float inv = p.sigmoid ? 1.0f : (sum > 0.0f ? 1.0f / sum : 0.0f);
+        err = score_err(p.sigmoid, inv);
+#pragma unroll
+        for (int s = 0; s < VPL; ++s) {
+            c[s] *= inv;
+            if (p.bias != nullptr && r + 16 * s < E) c[s] += p.bias[r + 16 * s];
+            if (!(val[s] == val[s])) c[s] = __builtin_nanf("");
+        }
+    }
+    bool sure = true;
+    uint32_t key[VPL];
+#pragma unroll
+    for (int s = 0; s < VPL; ++s) key[s] = r + 16 * s < E ? logit_ord(c[s]) : 0u;
+    if (grouped) {
+#pragma unroll
+        for (int s = 0; s < VPL; ++s) L.c[row][r + 16 * s] = c[s] == c[s] ? c[s] : -__builtin_inff();
+        lds_wave_sync();
+        int lg = 0;   // log2 of the lanes per group
+        while ((2 << lg) * G <= 16) ++lg;
+        const int P = 1 << lg, g = r >> lg, sub = r & (P - 1);
+        float m1 = -__builtin_inff(), m2 = -__builtin_inff();
+        if (g < G)
+            for (int i = sub; i < size; i += P) {
+                const float v = L.c[row][g * size + i];
+                m2 = fmaxf(m2, fminf(m1, v));
+                m1 = fmaxf(m1, v);
+            }
+        for (int d = 1; d < P; d <<= 1) {
+            const float o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
+            m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+            m1 = fmaxf(m1, o1);
+        }
+        if (g < G && sub == 0) L.g[row][g] = logit_ord(p.top2 && size > 1 ? m1 + m2 : m1);
+        lds_wave_sync();
+        const uint32_t mine = L.g[row][r < G ? r : 0];
+        int before = 0;
+        for (int q = 0; q < G; ++q) {
+            const uint32_t o = L.g[row][q];
+            before += (o > mine || (o == mine && q < r)) ? 1 : 0;
+        }
+        const bool in = r < G && before < p.topk_group;
+        const uint32_t kept = static_cast<uint32_t>(__ballot(in) >> (16 * row)) & 0xFFFFu;
+        if (!by_logit) {
+            const uint32_t lo = ~row_max(in ? ~mine : 0u), hi = row_max(r < G && !in ? mine : 0u);
+            float two = err;
+            if (p.top2) {
+                float cmax = 0.0f;
+#pragma unroll
+                for (int s = 0; s < VPL; ++s) cmax = fmaxf(cmax, finite_size(c[s]));
+                two = 2.0f * err + 4.0f * SU * __uint_as_float(row_max(__float_as_uint(cmax)));
+            }
+            sure = settled(ord_value(lo), ord_value(hi), two);
+        }
+#pragma unroll
+        for (int s = 0; s < VPL; ++s)
+            if (!((kept >> (group_of(r + 16 * s, inv_size) & 31)) & 1u)) key[s] = 0u;
+    }
+    int my_id = 0;
+    uint32_t my_key = 0;
+    const int rounds = by_logit ? k : k + 1;
+    for (int j = 0; j < rounds; ++j) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int s = 1; s < VPL; ++s) best = max(best, key[s]);
+        best = row_max(best);
+        uint32_t e = 0xFFFFu;
+#pragma unroll
+        for (int s = VPL - 1; s >= 0; --s) e = key[s] == best ? static_cast<uint32_t>(r + 16 * s) : e;
+        e = ~row_max(~e);   // the lowest id of the row that holds the maximum
+        const int d = static_cast<int>(e) - r;
+#pragma unroll
+        for (int s = 0; s < VPL; ++s)
+            if (d == 16 * s) key[s] = 0u;
+        if (r == j) {
+            my_id = static_cast<int>(e);
+            my_key = best;
+        }
+    }
+    if (!by_logit) {
+        const uint32_t next = __shfl_down(my_key, 1, 64);
+        if (r < k && next != 0u) sure = sure && settled(ord_value(my_key), ord_value(next), err);
+    }
+    const uint64_t unsure = __ballot(live && !sure);
+    // weights, lane r < k
+    const float ml = r < k ? load_logit(p, t, my_id) : 0.0f;
+    double w = r < k ? score64(ml, m, p.sigmoid) : 0.0;
+    double sum = 1.0;
+    if (p.renorm) {
+        sum = row_sum(w);
+    } else if (!p.sigmoid) {
+        sum = 0.0;
+#pragma unroll
+        for (int s = 0; s < VPL; ++s) sum += score64(val[s], m, 0);
+        sum = row_sum(sum);
+    }
+    w = sum > 0.0 ? w / sum : 0.0;
+    if (live && r < k && ((unsure >> (16 * row)) & 0xFFFFull) == 0ull) {
+        p.ids[static_cast<int64_t>(t) * k + r] = my_id;
+        p.w[static_cast<int64_t>(t) * k + r] = static_cast<float>(w * static_cast<double>(p.scale));
+    }
+    for (int q = 0; q < 4; ++q) {
+        if (((unsure >> (16 * q)) & 0xFFFFull) == 0ull) continue;   // wave-uniform
+        lds_wave_sync();
+        score_token<NPL>(p, t0 + q, lds[wave].one);
+    }
+}
+
 hipError_t launch_route_score(const ScoreRouteParams& p, hipStream_t s) {
-    const dim3 grid((p.T + 3) / 4), block(256);
+    const dim3 block(256);
+    const bool by_logit = p.bias == nullptr && !(p.topk_group < p.n_group && p.top2);
+    if (p.T >= (by_logit ? ROW_T_LOGITS : ROW_T_SCORES) && p.E <= ROW_E_MAX && p.n_group <= ROW_G_MAX && p.k <= ROW_K_MAX) {
+        const dim3 grid((p.T + 15) / 16);
+        auto kn = p.E <= 64 ? route_score_row_kernel<4>
+                            : p.E <= 128 ? route_score_row_kernel<8>
+                                         : p.E <= 160 ? route_score_row_kernel<10>
+                                                      : p.E <= 192 ? route_score_row_kernel<12> : route_score_row_kernel<16>;
+        hipLaunchKernelGGL(kn, grid, block, 0, s, p);
+        return hipGetLastError();
+    }
+    const dim3 grid((p.T + 3) / 4);
     auto kn = p.E <= 64 ? route_score_kernel<1>
                         : p.E <= 128 ? route_score_kernel<2>
                                      : p.E <= 192 ? route_score_kernel<3>

@@ -23,44 +23,47 @@ def half_step(dtype):
 
 # ------------------------------------------------------------- routing ----
 def route_score(logits, k, sigmoid, bias=None, n_group=1, topk_group=1, top2=False, renorm=True, scale=1.0):
-    """ids [T, k] and weights (64 bits) of moe_route_score_topk, one row at a time."""
+    """ids [T, k] and weights (64 bits) of moe_route_score_topk."""
     l = np.asarray(logits, np.float64)
     T, E = l.shape
     size = E // n_group
-    ids = np.zeros((T, k), np.int32)
-    w = np.zeros((T, k))
+    nan = np.isnan(l)
+    low = np.where(nan, -np.inf, l)
     with np.errstate(all="ignore"):
-        for t in range(T):
-            row, nan = l[t], np.isnan(l[t])
-            if sigmoid:
-                s = np.where(nan, 0.0, 1.0 / (1.0 + np.exp(-row)))
-            else:
-                m = np.max(row[~nan]) if (~nan).any() else np.nan
-                e = np.where(nan, 0.0, np.where(row == m, 1.0, np.exp(row - m)))
-                if m == -np.inf or np.isnan(m):
-                    e = np.zeros(E)
-                s = e / e.sum() if e.sum() > 0 else e
-            if bias is None and not (top2 and topk_group < n_group):
-                c = row                      # the order is that of the logits
-            else:
-                c = s + (0.0 if bias is None else np.asarray(bias, np.float64))
-            c = np.where(nan, np.nan, c)
-            # order: numbers by value, NaN after them, equal ones by id
-            def order(v, idx):
-                return sorted(idx, key=lambda i: (np.isnan(v[i]), -v[i] if not np.isnan(v[i]) else 0.0, i))
-            keep = list(range(E))
-            if topk_group < n_group:
-                g = np.where(np.isnan(c), -np.inf, c).reshape(n_group, size)
-                g = -np.sort(-g, axis=1)
-                rank = g[:, 0] + g[:, 1] if top2 and size > 1 else g[:, 0]
-                best = order(rank, range(n_group))[:topk_group]
-                keep = [e for b in sorted(best) for e in range(b * size, (b + 1) * size)]
-            chosen = order(c, keep)[:k]
-            ws = s[chosen]
-            if renorm:
-                ws = ws / ws.sum() if ws.sum() > 0 else np.zeros(k)
-            ids[t], w[t] = chosen, ws * np.float64(np.float32(scale))
-    return ids, w
+        if sigmoid:
+            s = np.where(nan, 0.0, 1.0 / (1.0 + np.exp(-l)))
+        else:
+            m = low.max(axis=1, keepdims=True)
+            e = np.where(nan | (m == -np.inf), 0.0, np.where(l == m, 1.0, np.exp(l - m)))
+            tot = e.sum(axis=1, keepdims=True)
+            s = np.where(tot > 0, e / tot, 0.0)
+        if bias is None and not (top2 and topk_group < n_group):
+            c = l.copy()                     # the order is that of the logits
+        else:
+            c = s + (0.0 if bias is None else np.asarray(bias, np.float64)[None, :])
+        c[nan] = np.nan
+
+        def order(v, out=None):
+            """Numbers by value, NaN after them, equal ones by index; what is out last."""
+            idx = np.broadcast_to(np.arange(v.shape[1]), v.shape)
+            return np.lexsort((idx, -np.nan_to_num(v, nan=0.0, posinf=np.inf, neginf=-np.inf), np.isnan(v),
+                               np.zeros(v.shape, bool) if out is None else out), axis=1)
+
+        out = np.zeros((T, E), bool)
+        if topk_group < n_group:
+            g = np.where(np.isnan(c), -np.inf, c).reshape(T, n_group, size)
+            g = -np.sort(-g, axis=2)
+            rank = g[:, :, 0] + g[:, :, 1] if top2 and size > 1 else g[:, :, 0]
+            gone = order(rank)[:, topk_group:]
+            drop = np.zeros((T, n_group), bool)
+            np.put_along_axis(drop, gone, True, axis=1)
+            out = np.repeat(drop, size, axis=1)
+        ids = order(c, out)[:, :k]
+        w = np.take_along_axis(s, ids, axis=1)
+        if renorm:
+            tot = w.sum(axis=1, keepdims=True)
+            w = np.where(tot > 0, w / tot, 0.0)
+    return ids.astype(np.int32), w * np.float64(np.float32(scale))
 
 
 # --------------------------------------------------------------- norms ----

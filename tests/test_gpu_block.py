@@ -77,6 +77,16 @@ def run_route(L, logits, k, bias=None, **kw):
     (130, 100, 4, 1, 1, 0, 1, False, F32, 1.0, 1),
     (37, 384, 8, 1, 1, 0, 1, True, BF16, 1.0, 1),
     (17, 257, 9, 1, 1, 0, 0, True, F32, 1.0, 1),
+    # four tokens to a wave: every width, ragged token counts, the largest k and group count it takes
+    (4099, 160, 6, 8, 3, 0, 0, False, BF16, 1.0, 1),
+    (4097, 61, 15, 1, 1, 0, 1, False, F32, 1.0, 0),
+    (4096, 128, 8, 16, 5, 0, 0, False, F32, 2.5, 0),
+    (12289, 256, 8, 8, 4, 1, 1, True, F32, 2.5, 1),
+    (12290, 192, 12, 3, 2, 1, 0, True, BF16, 1.0, 1),
+    (12291, 48, 3, 16, 7, 1, 0, True, F32, 1.0, 0),
+    (12292, 100, 15, 1, 1, 0, 1, True, F32, 1.0, 1),
+    (12300, 256, 8, 32, 4, 0, 1, True, F32, 1.0, 1),     # more groups than it takes: one token to a wave
+    (12300, 64, 16, 1, 1, 0, 0, True, F32, 1.0, 1),      # k too large for it
 ])
 def test_route_score(L, T, E, k, G, keep, rank, sigmoid, bias, dt, scale, renorm):
     g = gen(T * 1000 + E)
@@ -91,7 +101,8 @@ def test_route_score(L, T, E, k, G, keep, rank, sigmoid, bias, dt, scale, renorm
     close(w, want_w, U * (1 + 1e-6) * np.abs(want_w) + 1e-45, "weights")
 
 
-def test_route_score_ties_and_specials(L):
+@pytest.mark.parametrize("repeat", [1, 410, 1229])   # 10 rows, and enough for four tokens to a wave
+def test_route_score_ties_and_specials(L, repeat):
     inf, nan = float("inf"), float("nan")
     low = torch.finfo(F32).min
     E = 70
@@ -106,6 +117,7 @@ def test_route_score_ties_and_specials(L):
     rows[7, 5:60] = low
     rows[8] = torch.linspace(-90, 90, E)
     rows[9, 64:] = 1.0
+    rows = rows.repeat(repeat, 1)
     for sigmoid in (0, 1):
         for G, keep, rank in ((1, 1, 0), (7, 2, 0), (7, 2, 1)):
             for bias in (None, torch.linspace(0.3, -0.3, E)):
@@ -124,10 +136,11 @@ def test_route_score_ties_and_specials(L):
 
 
 @pytest.mark.parametrize("sigmoid", [0, 1])
-def test_route_score_close_scores(L, sigmoid):
+@pytest.mark.parametrize("T", [257, 12289])
+def test_route_score_close_scores(L, sigmoid, T):
     """Scores whose differences with the bias lie below 32-bit rounding: the choice is the 64-bit one."""
     g = gen(77)
-    T, E = 257, 128
+    E = 128
     for top2, G, keep in ((0, 1, 1), (0, 8, 3), (1, 8, 3)):
         base = normal(g, T, 1)
         logits = base + 2e-7 * torch.randint(-40, 41, (T, E), generator=g, device="cuda").float()
