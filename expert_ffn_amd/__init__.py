@@ -69,13 +69,14 @@ def lib():
         L.moe_slot_admit.argtypes = [P, i32, P, i32, i32]
         f32, i64 = ctypes.c_float, ctypes.c_int64
         L.moe_route_score_topk.argtypes = [P, i32, i64, P, i32, i32, i32, i32, i32, i32, i32, i32, f32, P, P, P]
+        L.moe_router_score_topk.argtypes = [P, i32, i32, i32, P, i32, i32, P, i32, i32, i32, i32, i32, f32, P, P, sz, P, P, P]
         L.moe_norm_in.argtypes = [P, i32, i64, i32, i32, P, i32, f32, f32, P, i32, i64, P, i64, P, P]
         L.moe_norm_out.argtypes = [P, i32, P, P, i32, P, i32, i64, i32, i32, P, i32, f32, f32, P, i32, i64, i64, f32, f32,
                                    P, i32, i64, P, i64, i32, P, P, i32, i64, P, i64, P, P]
         L.moe_quantize_tokens.argtypes = [P, i32, i64, i32, i32, P, i64, P, P]
         L.moe_matmul_i8.argtypes = [P, i64, P, P, i64, P, P, i32, i32, i32, P, i32, i64, P]
         L.moe_gated_matmul_i8.argtypes = [P, i64, P, P, i64, P, i32, i32, i32, i32, P, i32, i64, P]
-        for name in ("moe_route_score_topk", "moe_norm_in", "moe_norm_out", "moe_quantize_tokens", "moe_matmul_i8",
+        for name in ("moe_route_score_topk", "moe_router_score_topk", "moe_norm_in", "moe_norm_out", "moe_quantize_tokens", "moe_matmul_i8",
                      "moe_gated_matmul_i8"):
             getattr(L, name).restype = ctypes.c_int
         for name in ("moe_blob_layout", "moe_route_topk", "moe_permute", "moe_route_permute", "moe_expert_ffn",
@@ -375,6 +376,28 @@ def route_score_topk(logits, k: int, topk_ids, topk_w, score: int = SCORE_SOFTMA
     wp = _vec("topk_w", topk_w, T * k, dev, F32)[0]
     _on(dev, stream, _lib.moe_route_score_topk, lp, ldt, ld, bp, T, E, k, score, n_group, topk_group, group_rank, renorm,
         scale, ip, wp)
+
+
+def router_score_topk(x, w_router, k: int, logits, ws, topk_ids, topk_w, score: int = SCORE_SOFTMAX, bias=None,
+                      n_group: int = 1, topk_group: int = 1, group_rank: int = GROUP_MAX, renorm: int = 1,
+                      scale: float = 1.0, stream=None):
+    """fp32 router product of x [T, H] with w_router [E, H] (logits [T, E] out, ws as for router_topk), then
+    route_score_topk on the logits."""
+    dev, T, H, xp, xdt, ldx = _first("x", x)
+    if ldx != H and T > 1:
+        raise ValueError("x is not contiguous")
+    E = w_router.shape[0]
+    wp = _vec("w_router", w_router, E * H, dev, F32)[0]
+    lp = _vec("logits", logits, T * E, dev, F32)[0]
+    bp = None if bias is None else _vec("bias", bias, E, dev, F32)[0]
+    ip = _vec("topk_ids", topk_ids, T * k, dev, "int32")[0]
+    op = _vec("topk_w", topk_w, T * k, dev, F32)[0]
+    if ws.get_device() != dev:
+        raise _where_error("ws", ws, dev)
+    if not ws.is_contiguous():
+        raise ValueError("ws is not contiguous")
+    _on(dev, stream, _lib.moe_router_score_topk, xp, xdt, T, H, wp, E, k, bp, score, n_group, topk_group, group_rank, renorm,
+        scale, lp, ws.data_ptr(), ws.numel() * ws.element_size(), ip, op)
 
 
 def _norm_outputs(T, H, dev, x, xq, xq_scale):

@@ -2,6 +2,7 @@
 // and after the block, and the 8-bit integer products.  Argument checks on the
 // host, then one launch on the caller's stream.
 #include "block.h"
+#include "kernels.h"
 #include "status.h"
 
 using moe::aligned;
@@ -80,14 +81,9 @@ moe_status check_apart(const char* fn, const Span* in, int n_in, const Span* out
 
 extern "C" {
 
-moe_status moe_route_score_topk(const void* logits, int32_t logits_dtype, int64_t ld_logits, const float* bias, int32_t T,
-                                int32_t E, int32_t k, int32_t score, int32_t n_group, int32_t topk_group,
-                                int32_t group_rank, int32_t renorm, float scale, int32_t* topk_ids, float* topk_w,
-                                void* stream) {
-    const char* fn = "moe_route_score_topk";
+static moe_status check_score(const char* fn, int32_t T, int32_t E, int32_t k, int32_t score, int32_t n_group,
+                              int32_t topk_group, int32_t group_rank, float scale) {
     if (T < 0) return fail(MOE_E_SHAPE, fn, "T=%d < 0", T);
-    if (T > 0 && (!logits || !topk_ids || !topk_w)) return fail(MOE_E_ARG, fn, "null pointer argument");
-    if (!dt_ok(logits_dtype)) return fail(MOE_E_ARG, fn, "unknown dtype %d", logits_dtype);
     if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return fail(MOE_E_ARG, fn, "unknown score %d", score);
     if (group_rank != MOE_GROUP_MAX && group_rank != MOE_GROUP_TOP2)
         return fail(MOE_E_ARG, fn, "unknown group rank %d", group_rank);
@@ -97,21 +93,17 @@ moe_status moe_route_score_topk(const void* logits, int32_t logits_dtype, int64_
     if (topk_group < 1 || topk_group > n_group)
         return fail(MOE_E_SHAPE, fn, "topk_group=%d outside [1, n_group=%d]", topk_group, n_group);
     const int32_t open = E / n_group * topk_group;
-    if (k < 1 || k > 32 || k > open) return fail(MOE_E_SHAPE, fn, "k=%d outside [1, min(%d experts of the kept groups, 32)]", k, open);
-    if (ld_logits < E || ld_logits >= (1ll << 40))
-        return fail(MOE_E_SHAPE, fn, "row stride %lld of logits is below E=%d or too large", static_cast<long long>(ld_logits), E);
-    if (static_cast<int64_t>(T) * k > (1ll << 30)) return fail(MOE_E_SHAPE, fn, "T*k too large");
+    if (k < 1 || k > 32 || k > open)
+        return fail(MOE_E_SHAPE, fn, "k=%d outside [1, min(%d experts of the kept groups, 32)]", k, open);
+    if (T > (1 << 24) || static_cast<int64_t>(T) * k > (1ll << 30)) return fail(MOE_E_SHAPE, fn, "T=%d or T*k too large", T);
     if (!(scale - scale == 0.0f)) return fail(MOE_E_ARG, fn, "scale is not finite");
-    if (!aligned(logits, esize(logits_dtype)) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
-        return fail(MOE_E_ARG, fn, "a pointer is not aligned to its elements");
-    const Span in[2] = {span(logits, T, ld_logits, E, esize(logits_dtype)), span(bias, 1, E, E, 4)};
-    const Span out[2] = {span(topk_ids, T, k, k, 4), span(topk_w, T, k, k, 4)};
-    const moe_status st = check_apart(fn, in, 2, out, 2);
-    if (st != MOE_OK || T == 0) return st;
+    return MOE_OK;
+}
+
+static moe::ScoreRouteParams score_params(const float* bias, int32_t T, int32_t E, int32_t k, int32_t score, int32_t n_group,
+                                          int32_t topk_group, int32_t group_rank, int32_t renorm, float scale,
+                                          int32_t* topk_ids, float* topk_w) {
     moe::ScoreRouteParams p{};
-    p.logits = logits;
-    p.logits_dt = logits_dtype;
-    p.ld = ld_logits;
     p.bias = bias;
     p.T = T; p.E = E; p.k = k;
     p.sigmoid = score == MOE_SCORE_SIGMOID;
@@ -122,7 +114,61 @@ moe_status moe_route_score_topk(const void* logits, int32_t logits_dtype, int64_
     p.scale = scale;
     p.ids = topk_ids;
     p.w = topk_w;
+    return p;
+}
+
+moe_status moe_route_score_topk(const void* logits, int32_t logits_dtype, int64_t ld_logits, const float* bias, int32_t T,
+                                int32_t E, int32_t k, int32_t score, int32_t n_group, int32_t topk_group,
+                                int32_t group_rank, int32_t renorm, float scale, int32_t* topk_ids, float* topk_w,
+                                void* stream) {
+    const char* fn = "moe_route_score_topk";
+    moe_status st = check_score(fn, T, E, k, score, n_group, topk_group, group_rank, scale);
+    if (st != MOE_OK) return st;
+    if (T > 0 && (!logits || !topk_ids || !topk_w)) return fail(MOE_E_ARG, fn, "null pointer argument");
+    if (!dt_ok(logits_dtype)) return fail(MOE_E_ARG, fn, "unknown dtype %d", logits_dtype);
+    if (ld_logits < E || ld_logits >= (1ll << 40))
+        return fail(MOE_E_SHAPE, fn, "row stride %lld of logits is below E=%d or too large", static_cast<long long>(ld_logits), E);
+    if (!aligned(logits, esize(logits_dtype)) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+        return fail(MOE_E_ARG, fn, "a pointer is not aligned to its elements");
+    const Span in[2] = {span(logits, T, ld_logits, E, esize(logits_dtype)), span(bias, 1, E, E, 4)};
+    const Span out[2] = {span(topk_ids, T, k, k, 4), span(topk_w, T, k, k, 4)};
+    st = check_apart(fn, in, 2, out, 2);
+    if (st != MOE_OK || T == 0) return st;
+    moe::ScoreRouteParams p = score_params(bias, T, E, k, score, n_group, topk_group, group_rank, renorm, scale, topk_ids, topk_w);
+    p.logits = logits;
+    p.logits_dt = logits_dtype;
+    p.ld = ld_logits;
     return hip_status(fn, moe::launch_route_score(p, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_router_score_topk(const void* x, int32_t x_dtype, int32_t T, int32_t H, const float* w_router, int32_t E,
+                                 int32_t k, const float* bias, int32_t score, int32_t n_group, int32_t topk_group,
+                                 int32_t group_rank, int32_t renorm, float scale, float* logits, void* ws, size_t ws_bytes,
+                                 int32_t* topk_ids, float* topk_w, void* stream) {
+    const char* fn = "moe_router_score_topk";
+    moe_status st = check_score(fn, T, E, k, score, n_group, topk_group, group_rank, scale);
+    if (st != MOE_OK) return st;
+    if (T > 0 && (!x || !w_router || !logits || !ws || !topk_ids || !topk_w))
+        return fail(MOE_E_ARG, fn, "null pointer argument");
+    if (!dt_ok(x_dtype)) return fail(MOE_E_ARG, fn, "unknown dtype %d", x_dtype);
+    if (H < 64 || H % 64) return fail(MOE_E_SHAPE, fn, "H=%d is not a positive multiple of 64", H);
+    if (static_cast<int64_t>(T) * H >= (1ll << 31) || moe::router_part_floats(T, H, E) >= (1ll << 31))
+        return fail(MOE_E_SHAPE, fn, "T=%d too large", T);
+    if (T == 0) return MOE_OK;
+    if (ws_bytes < moe_router_ws_bytes(T, H, E))
+        return fail(MOE_E_WORKSPACE, fn, "ws_bytes=%zu < %zu", ws_bytes, moe_router_ws_bytes(T, H, E));
+    if (!aligned(x, 16) || !aligned(w_router, 16) || !aligned(ws, 16))
+        return fail(MOE_E_ARG, fn, "x, w_router and ws must be 16-byte aligned");
+    if (!aligned(bias, 4) || !aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+        return fail(MOE_E_ARG, fn, "a pointer is not aligned to its elements");
+    const Span in[3] = {span(x, T, H, H, esize(x_dtype)), span(w_router, E, H, H, 4), span(bias, 1, E, E, 4)};
+    const Span out[4] = {span(topk_ids, T, k, k, 4), span(topk_w, T, k, k, 4), span(logits, T, E, E, 4),
+                         span(ws, 1, 1, static_cast<int64_t>(moe_router_ws_bytes(T, H, E)), 1)};
+    if ((st = check_apart(fn, in, 3, out, 4)) != MOE_OK) return st;
+    const moe::ScoreRouteParams p =
+        score_params(bias, T, E, k, score, n_group, topk_group, group_rank, renorm, scale, topk_ids, topk_w);
+    return hip_status(fn, moe::launch_router_score(x, x_dtype == MOE_F32, w_router, H, logits, static_cast<float*>(ws), p,
+                                                   static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_norm_in(const void* h, int32_t h_dtype, int64_t ldh, int32_t T, int32_t H, const void* w, int32_t w_dtype,

@@ -19,6 +19,12 @@ struct ScoreRouteParams {
     float* w;               // [T, k]
 };
 hipError_t launch_route_score(const ScoreRouteParams& p, hipStream_t s);
+// the router's product in slices of H: part fp32 [*HS][T][E] (router_part_floats in all), summed in slice order by the reader
+hipError_t launch_router_part(const void* x, bool xf32, const float* wr, int T, int H, int E, float* part, int* HS,
+                              hipStream_t s);
+// the product, then the scored top-k of p (its logits, logits_dt and ld are not read); logits fp32 [T, E] out
+hipError_t launch_router_score(const void* x, bool xf32, const float* wr, int H, float* logits, float* part,
+                               const ScoreRouteParams& p, hipStream_t s);
 
 // ---------------------------------------------------------------- norms --
 // One row's outputs of a norm: x (null: none), 8-bit codes and their scale

@@ -111,16 +111,19 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
     // nothing is read for them, and the count of copies in flight stays uniform.
     auto copy = [&](int c, uint8_t* st, int i) {
         const int k = BK * (c * KG + kg);
+        // the scalar offset stays inside the resource: the range check subtracts it
+        // from the resource's size
+        const uint32_t so = k < p.K ? k : 0;
         if (i < DA) {
             const uint32_t o = k + chunk(i) < p.K ? ao[i] : NO_LANE;
             uint8_t* dst = st + RPC * (wave + NW * i) * BK;
             if (is_up(RPC * (wave + NW * i)))
-                lds_copy16(wr1, dst, o, k);
+                lds_copy16(wr1, dst, o, so);
             else
-                lds_copy16(wr0, dst, o, k);
+                lds_copy16(wr0, dst, o, so);
         } else {
             const int j = i - DA;
-            lds_copy16(xr, st + (BN + RPC * (wave + NW * j)) * BK, k + chunk(j) < p.K ? bo[j] : NO_LANE, k);
+            lds_copy16(xr, st + (BN + RPC * (wave + NW * j)) * BK, k + chunk(j) < p.K ? bo[j] : NO_LANE, so);
         }
     };
     // fragments: row l & 31 of a 32-row block (blocks start at multiples of 32), chunk 2 s + (l >> 5)

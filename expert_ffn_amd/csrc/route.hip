@@ -6,6 +6,7 @@
 // (ballots), which is the tie rule of rlx_runtime/expert_pool.rs
 // (target_gpu_from_counts).  k rounds give the ids in rank order; lanes j < k
 // then compute the softmax weights (prain README, "Trading quality for speed").
+#include "block.h"
 #include "common.h"
 #include "kernels.h"
 #include "route.h"
@@ -279,8 +280,8 @@ int64_t router_part_floats(int T, int H, int E) {
     return static_cast<int64_t>((H + hl - 1) / hl) * T * E;
 }
 
-hipError_t launch_router_topk(const void* x, bool xf32, const float* wr, int T, int H, int E, int k, int renorm,
-                              float* logits, float* part, int* ids, float* w, hipStream_t s) {
+hipError_t launch_router_part(const void* x, bool xf32, const float* wr, int T, int H, int E, float* part, int* HS_out,
+                              hipStream_t s) {
     const dim3 block(256);
     int HS;
     if (router_large(T)) {
@@ -294,6 +295,16 @@ hipError_t launch_router_topk(const void* x, bool xf32, const float* wr, int T, 
         auto pk = xf32 ? router_part_kernel<true> : router_part_kernel<false>;
         hipLaunchKernelGGL(pk, grid, block, 0, s, x, wr, T, H, E, part);
     }
+    *HS_out = HS;
+    return hipGetLastError();
+}
+
+hipError_t launch_router_topk(const void* x, bool xf32, const float* wr, int T, int H, int E, int k, int renorm,
+                              float* logits, float* part, int* ids, float* w, hipStream_t s) {
+    const dim3 block(256);
+    int HS = 0;
+    const hipError_t e = launch_router_part(x, xf32, wr, T, H, E, part, &HS, s);
+    if (e != hipSuccess) return e;
     const dim3 g2((T + 3) / 4);   // the slice sums run in slice order either way
     auto tk = E <= 64 ? router_topk_part_kernel<1>
                       : E <= 128 ? router_topk_part_kernel<2>

@@ -156,24 +156,17 @@ __device__ __forceinline__ float score32(float v, float m, int sigmoid) {
     return v == v && !(m == -__builtin_inff()) ? s : 0.0f;
 }
 
-// One token on one wave; lane l holds experts l + 64 s (s < NPL).
+// One token on one wave; lane l holds experts l + 64 s (s < NPL), val their logits
+// (NaN past E).
 template <int NPL>
-__device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, ScoreLds<NPL>& L) {
+__device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, const float (&val)[NPL], ScoreLds<NPL>& L) {
     const int lane = threadIdx.x & 63;
     const int E = p.E, G = p.n_group, size = E / G;
     const bool grouped = p.topk_group < G;
     const float inv_size = 1.0f / static_cast<float>(size);
-    float val[NPL], bias[NPL];
+    float bias[NPL];
 #pragma unroll
-    for (int s = 0; s < NPL; ++s) {
-        const int e = lane + 64 * s;
-        val[s] = __builtin_nanf("");
-        bias[s] = 0.0f;
-        if (e < E) {
-            val[s] = load_logit(p, t, e);
-            if (p.bias != nullptr) bias[s] = p.bias[e];
-        }
-    }
+    for (int s = 0; s < NPL; ++s) bias[s] = p.bias != nullptr && lane + 64 * s < E ? p.bias[lane + 64 * s] : 0.0f;
     // the largest logit (NaN when there is none): equal ones score alike also when infinite
     float m = 0.0f;
     if (!p.sigmoid) {
@@ -358,11 +351,51 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, Sc
 }
 
 template <int NPL>
+__device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, ScoreLds<NPL>& L) {
+    const int lane = threadIdx.x & 63;
+    float val[NPL];
+#pragma unroll
+    for (int s = 0; s < NPL; ++s) val[s] = lane + 64 * s < p.E ? load_logit(p, t, lane + 64 * s) : __builtin_nanf("");
+    score_token<NPL>(p, t, val, L);
+}
+
+template <int NPL>
 __global__ __launch_bounds__(256) void route_score_kernel(ScoreRouteParams p) {
     __shared__ ScoreLds<NPL> lds[4];
     const int wave = threadIdx.x >> 6, t = blockIdx.x * 4 + wave;
     if (t >= p.T) return;   // wave-uniform; the kernel has no workgroup barrier
     score_token<NPL>(p, t, lds[wave]);
+}
+
+// The same behind the router's product: the logits are the sums of its HS slices
+// (part [HS][T][E]) in slice order, and are written (p.logits [T, E]).
+template <int NPL>
+__global__ __launch_bounds__(256) void route_score_part_kernel(ScoreRouteParams p, const float* __restrict__ part, int HS,
+                                                               float* __restrict__ logits) {
+    __shared__ ScoreLds<NPL> lds[4];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, t = blockIdx.x * 4 + wave;
+    if (t >= p.T) return;
+    const int64_t stride = static_cast<int64_t>(p.T) * p.E;
+    float val[NPL];
+#pragma unroll
+    for (int s = 0; s < NPL; ++s) {
+        const int e = lane + 64 * s;
+        val[s] = __builtin_nanf("");
+        if (e >= p.E) continue;
+        const float* q = part + static_cast<int64_t>(t) * p.E + e;
+        float v = 0.0f;
+        for (int s0 = 0; s0 < HS; s0 += 8) {   // eight slices' loads in flight at a time
+            float b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[j] = s0 + j < HS ? q[(s0 + j) * stride] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (s0 + j < HS) v = s0 + j == 0 ? b[j] : v + b[j];
+        }
+        logits[static_cast<int64_t>(t) * p.E + e] = v;
+        val[s] = v;
+    }
+    score_token<NPL>(p, t, val, lds[wave]);
 }
 
 // Reductions over the 16 lanes of a row (every lane gets the result).
@@ -569,6 +602,19 @@ hipError_t launch_route_score(const ScoreRouteParams& p, hipStream_t s) {
                                      : p.E <= 192 ? route_score_kernel<3>
                                                   : p.E <= 256 ? route_score_kernel<4> : route_score_kernel<8>;
     hipLaunchKernelGGL(kn, grid, block, 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_router_score(const void* x, bool xf32, const float* wr, int H, float* logits, float* part,
+                               const ScoreRouteParams& p, hipStream_t s) {
+    int HS = 0;
+    const hipError_t e = launch_router_part(x, xf32, wr, p.T, H, p.E, part, &HS, s);
+    if (e != hipSuccess) return e;
+    auto kn = p.E <= 64 ? route_score_part_kernel<1>
+                        : p.E <= 128 ? route_score_part_kernel<2>
+                                     : p.E <= 192 ? route_score_part_kernel<3>
+                                                  : p.E <= 256 ? route_score_part_kernel<4> : route_score_part_kernel<8>;
+    hipLaunchKernelGGL(kn, dim3((p.T + 3) / 4), dim3(256), 0, s, p, part, HS, logits);
     return hipGetLastError();
 }
 

@@ -7,8 +7,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (ACT_GELU_TANH, F32, combine, expert_ffn, ffn_down, ffn_gate_up, min_weight, permute,
-               route_topk, workspace_bytes)
+from . import (ACT_GELU_TANH, F32, GROUP_MAX, SCORE_SOFTMAX, W_INT8_ROW, blob_layout, combine,
+               expert_ffn, ffn_down, ffn_gate_up, gated_matmul_i8, matmul_i8, min_weight, norm_in, norm_out, permute,
+               quantize_tokens, route_topk, router_score_topk, router_ws_bytes, workspace_bytes)
 
 
 class MoeLayer:
@@ -89,4 +90,89 @@ class MoeLayer:
         return self.y[:T]
 
 
-__all__ = ["MoeLayer", "F32"]
+class DenseExpert:
+    """A dense (shared) expert beside the routed ones, in 8-bit integers: an int8 blob (pack_expert with
+    W_INT8_ROW) whose codes the 8-bit products read in place."""
+
+    def __init__(self, blob, H, FF, act=ACT_GELU_TANH):
+        o13, s13, o2, s2, size = blob_layout(W_INT8_ROW, H, FF)
+        if blob.dtype != torch.uint8 or not blob.is_contiguous() or blob.numel() < size:
+            raise ValueError(f"blob must be {size} contiguous bytes")
+        b = blob.view(-1)
+        self.H, self.FF, self.act, self.blob = H, FF, act, blob
+        self.w13 = b[o13:o13 + 2 * FF * H].view(torch.int8).view(2 * FF, H)
+        self.s13 = b[s13:s13 + 8 * FF].view(torch.float32)
+        self.w2 = b[o2:o2 + H * FF].view(torch.int8).view(H, FF)
+        self.s2 = b[s2:s2 + 4 * H].view(torch.float32)
+
+
+class MoeBlock:
+    """The MoE half of a transformer block around a MoeLayer, over buffers torch allocates once:
+
+        x      = norm(h; w_in)              bf16, and 8-bit codes when there is a dense expert
+        routes = scored top-k of x . w_router^T, grouped by expert
+        h_out  = res_scale h + block_scale gate norm(combine(routes) + dense(x); w_post)
+
+    run() returns h_out [T, H] and, with w_next, the next block's normed rows.  h is fp32 or bf16; h_out
+    may be h.  w_post, gate, bias, dense and w_next may be None.  The buffers hold up to the layer's T_max
+    tokens and are reused by the next run: calls on one block are ordered by the caller."""
+
+    def __init__(self, layer, w_in, w_router, w_post=None, eps=1e-6, w_offset=0.0, dense=None, gate=None,
+                 block_scale=1.0, res_scale=1.0, w_next=None, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1,
+                 group_rank=GROUP_MAX, route_scale=1.0):
+        T, H, d = layer.T_max, layer.H, layer.y.device
+        if dense is not None and dense.H != H:
+            raise ValueError(f"the dense expert has H={dense.H}, the layer {H}")
+        self.layer, self.dense, self.gate, self.eps, self.w_offset = layer, dense, gate, eps, w_offset
+        self.w_in, self.w_router, self.w_post, self.w_next = w_in, w_router, w_post, w_next
+        self.block_scale, self.res_scale = block_scale, res_scale
+        self.routing = dict(score=score, bias=bias, n_group=n_group, topk_group=topk_group, group_rank=group_rank,
+                            renorm=layer.renorm, scale=route_scale)
+        bf16, f32 = torch.bfloat16, torch.float32
+        self.x = torch.empty((T, H), dtype=bf16, device=d)
+        self.logits = torch.empty((T, layer.E), dtype=f32, device=d)
+        # the sizes of the workspace do not grow with T alone: few tokens take wider slices of H
+        nbytes = max(router_ws_bytes(t, H, layer.E) for t in {min(T, 64), T})
+        self.router_ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=d)
+        self.x_next = torch.empty((T, H), dtype=bf16, device=d) if w_next is not None else None
+        if dense is not None:
+            self.xq = torch.empty((T, H), dtype=torch.int8, device=d)
+            self.hid = torch.empty((T, dense.FF), dtype=bf16, device=d)
+            self.hq = torch.empty((T, dense.FF), dtype=torch.int8, device=d)
+            self.xs, self.hs = (torch.empty(T, dtype=f32, device=d) for _ in range(2))
+            self.yd = torch.empty((T, H), dtype=bf16, device=d)
+
+    def run_dense(self, T, stream=None):
+        """The dense expert on the codes of the last norm: its rows in yd."""
+        e = self.dense
+        gated_matmul_i8(self.xq[:T], self.xs[:T], e.w13, e.s13, e.act, self.hid[:T], stream)
+        quantize_tokens(self.hid[:T], self.hq[:T], self.hs[:T], stream)
+        matmul_i8(self.hq[:T], self.hs[:T], e.w2, e.s2, self.yd[:T], stream=stream)
+        return self.yd[:T]
+
+    def run(self, h, h_out, stream=None):
+        if h.shape[0] > self.layer.T_max:
+            raise ValueError(f"T={h.shape[0]} exceeds the layer's T_max={self.layer.T_max}")
+        if h.shape[0] == 0:
+            return h_out, self.x_next[:0] if self.x_next is not None else None
+        with torch.cuda.device(self.x.device):   # the layer's calls go to the current device
+            return self._run(h, h_out, stream)
+
+    def _run(self, h, h_out, stream):
+        T, L = h.shape[0], self.layer
+        codes = dict(xq=self.xq[:T], xq_scale=self.xs[:T]) if self.dense is not None else {}
+        norm_in(h, self.w_in, self.eps, x=self.x[:T], w_offset=self.w_offset, stream=stream, **codes)
+        router_score_topk(self.x[:T], self.w_router, L.k, self.logits[:T], self.router_ws, L.topk_ids[:T], L.topk_w[:T],
+                          stream=stream, **self.routing)
+        L.group(T, stream)
+        L.ffn(self.x[:T], stream)
+        y = self.run_dense(T, stream) if self.dense is not None else None
+        gate = self.gate[:T] if self.gate is not None and self.gate.dim() == 2 and self.gate.shape[0] > 1 else self.gate
+        nxt = self.x_next[:T] if self.x_next is not None else None
+        norm_out(h, h_out, self.w_post, self.eps, out_routes=L.out_routes[:T * L.k], topk_w=L.topk_w[:T],
+                 route_pos=L.route_pos[:T * L.k], y=y, gate=gate, block_scale=self.block_scale,
+                 res_scale=self.res_scale, w_next=self.w_next, x=nxt, w_offset=self.w_offset, stream=stream)
+        return h_out, nxt
+
+
+__all__ = ["MoeLayer", "MoeBlock", "DenseExpert", "F32"]

@@ -444,12 +444,22 @@ typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_rank;
  * c; infinite logits take the limits (softmax: the experts at +inf share the
  * weight; a row of -inf alone scores 0 everywhere).
  * 1 <= k <= min(32, topk_group * E / n_group), E <= 512, n_group a divisor of E,
- * at most 64; scale finite.  T = 0 enqueues nothing.
+ * at most 64; scale finite; T <= 2^24, T*k <= 2^30.  T = 0 enqueues nothing.
  */
 moe_status moe_route_score_topk(const void* logits, int32_t logits_dtype, int64_t ld_logits, const float* bias, int32_t T,
                                 int32_t E, int32_t k, int32_t score, int32_t n_group, int32_t topk_group,
                                 int32_t group_rank, int32_t renorm, float scale, int32_t* topk_ids, float* topk_w,
                                 void* stream);
+
+/*
+ * The router's product (logits = x . w_router^T in fp32, as moe_router_topk: same
+ * operands, workspace and sums), then moe_route_score_topk on those logits, with
+ * the logits written: two launches.  H a multiple of 64.
+ */
+moe_status moe_router_score_topk(const void* x, int32_t x_dtype, int32_t T, int32_t H, const float* w_router, int32_t E,
+                                 int32_t k, const float* bias, int32_t score, int32_t n_group, int32_t topk_group,
+                                 int32_t group_rank, int32_t renorm, float scale, float* logits, void* ws, size_t ws_bytes,
+                                 int32_t* topk_ids, float* topk_w, void* stream);
 
 /*
  * RMS norm before a block: for each row of h (device [T, H], fp32 or bf16)

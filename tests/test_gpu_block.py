@@ -443,3 +443,75 @@ def test_matmul_i8_non_finite_scales(L):
         keep = [0] + list(range(3, T))
         want, bound = ref.matmul_i8(xq.cpu().numpy()[keep], np.ones(len(keep)), wq.cpu().numpy(), np.ones(40))
         close(f64(out)[keep], want, bound, "out")
+
+
+def test_binding_refusals_on_gpu_tensors(L):
+    """Wrong shapes, types and layouts are refused before anything is enqueued."""
+    z = lambda *s, dt=F32: torch.zeros(*s, dtype=dt, device="cuda")
+    i8, i32 = torch.int8, torch.int32
+    h, x, w = z(4, 64, dt=BF16), z(4, 64, dt=BF16), z(64)
+    ids, tw = z(4, 2, dt=i32), z(4, 2)
+    for err, call in [
+        (ValueError, lambda: L.route_score_topk(z(8), 2, ids, tw)),
+        (ValueError, lambda: L.route_score_topk(z(4, 8), 3, ids, tw)),
+        (TypeError, lambda: L.route_score_topk(z(4, 8, dt=torch.float16), 2, ids, tw)),
+        (TypeError, lambda: L.route_score_topk(z(4, 8), 2, ids.long(), tw)),
+        (ValueError, lambda: L.route_score_topk(z(8, 4).t(), 2, ids, tw)),
+        (ValueError, lambda: L.route_score_topk(z(4, 8), 2, ids, tw, bias=z(9))),
+        (ValueError, lambda: L.route_score_topk(z(4, 8), 2, ids, tw, bias=torch.zeros(8))),
+        (L.MoeError, lambda: L.route_score_topk(z(4, 8), 2, ids, tw, n_group=3)),
+        (ValueError, lambda: L.norm_in(h, z(65), EPS, x=x)),
+        (ValueError, lambda: L.norm_in(h, w, EPS, x=z(4, 72, dt=BF16))),
+        (ValueError, lambda: L.norm_in(h, w, EPS, xq=z(4, 64, dt=i8))),
+        (TypeError, lambda: L.norm_in(h, w, EPS, xq=z(4, 64, dt=torch.uint8), xq_scale=z(4))),
+        (L.MoeError, lambda: L.norm_in(h, w, EPS)),
+        (L.MoeError, lambda: L.norm_in(h, w, 0.0, x=x)),
+        (L.MoeError, lambda: L.norm_in(h, w, EPS, x=h)),
+        (L.MoeError, lambda: L.norm_in(z(4, 60), None, EPS, x=z(4, 60))),
+        (L.MoeError, lambda: L.norm_in(z(4, 66)[:, 1:65], None, EPS, x=x)),
+        (L.MoeError, lambda: L.norm_in(z(1, 64).expand(4, 64), None, EPS, x=x)),
+        (TypeError, lambda: L.norm_out(h, z(4, 64), None, EPS, y=x)),
+        (ValueError, lambda: L.norm_out(h, x, None, EPS, y=z(3, 64))),
+        (ValueError, lambda: L.norm_out(h, x, None, EPS, out_routes=z(8, 64))),
+        (ValueError, lambda: L.norm_out(h, x, None, EPS, out_routes=z(8, 64), topk_w=z(4, 2), route_pos=z(7, dt=i32))),
+        (ValueError, lambda: L.norm_out(h, x, None, EPS, y=z(4, 64), gate=z(3, 64))),
+        (ValueError, lambda: L.norm_out(h, x, None, EPS, y=z(4, 64), gate=z(2, 4, 64))),
+        (ValueError, lambda: L.norm_out(h, x, None, EPS, y=z(4, 64), w_next=w)),
+        (TypeError, lambda: L.norm_out(h, x, w, EPS, y=z(4, 64), w_next=w.bfloat16(), x=z(4, 64))),
+        (L.MoeError, lambda: L.norm_out(h, x, None, EPS)),
+        (L.MoeError, lambda: L.norm_out(h, x, None, EPS, y=z(4, 64), gate=z(64, 4).t())),
+        (ValueError, lambda: L.matmul_i8(z(4, 64, dt=i8), z(4), z(8, 48, dt=i8), z(8), z(4, 8))),
+        (ValueError, lambda: L.matmul_i8(z(4, 64, dt=i8), z(3), z(8, 64, dt=i8), z(8), z(4, 8))),
+        (TypeError, lambda: L.matmul_i8(z(4, 64), z(4), z(8, 64, dt=i8), z(8), z(4, 8))),
+        (TypeError, lambda: L.matmul_i8(z(4, 64, dt=i8), z(4), z(8, 64, dt=i8), z(8), z(4, 8, dt=torch.float16))),
+        (L.MoeError, lambda: L.matmul_i8(z(4, 72, dt=i8), z(4), z(8, 72, dt=i8), z(8), z(4, 8))),
+        (ValueError, lambda: L.gated_matmul_i8(z(4, 64, dt=i8), z(4), z(7, 64, dt=i8), z(7), 0, z(4, 3))),
+        (L.MoeError, lambda: L.gated_matmul_i8(z(4, 64, dt=i8), z(4), z(8, 64, dt=i8), z(8), 9, z(4, 4))),
+    ]:
+        with pytest.raises(err):
+            call()
+
+
+def test_empty_batches(L):
+    """T = 0: nothing is written, nothing refused."""
+    z = lambda *s, dt=F32: torch.zeros(*s, dtype=dt, device="cuda")
+    i8 = torch.int8
+    L.route_score_topk(z(0, 8), 2, z(0, 2, dt=torch.int32), z(0, 2))
+    L.norm_in(z(0, 64), z(64), EPS, x=z(0, 64), xq=z(0, 64, dt=i8), xq_scale=z(0))
+    L.norm_out(z(0, 64), z(0, 64), z(64), EPS, y=z(0, 64))
+    L.quantize_tokens(z(0, 64), z(0, 64, dt=i8), z(0))
+    L.matmul_i8(z(0, 64, dt=i8), z(0), z(8, 64, dt=i8), z(8), z(0, 8))
+    L.gated_matmul_i8(z(0, 64, dt=i8), z(0), z(8, 64, dt=i8), z(8), 0, z(0, 4))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("shape", [(64,), (1, 64), (5, 1), (5, 64), (1,), (1, 1), ()])
+def test_norm_out_gate_broadcasts(L, shape):
+    g = gen(4)
+    h, y = normal(g, 5, 64), normal(g, 5, 64)
+    gate = normal(g, *shape) if shape else normal(g, 1).reshape(())
+    a, b = torch.empty_like(h), torch.empty_like(h)
+    L.norm_out(h, a, None, EPS, y=y, gate=gate)
+    L.norm_out(h, b, None, EPS, y=y, gate=gate.expand(5, 64).contiguous())
+    assert torch.equal(a, b)
+    close(f64(a), f64(h) + f64(y) * f64(gate), 3 * U * (np.abs(f64(h)) + np.abs(f64(y) * f64(gate))) + 1e-37, "h_out")
