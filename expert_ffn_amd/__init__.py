@@ -1,6 +1,7 @@
 """Python binding of libexpert_ffn.so (the C ABI in include/expert_ffn.h).
 
-Argument marshalling only: every function passes torch tensors' device
+Argument marshalling only (ctypes here, a compiled module for the operators
+around the expert FFN): every function passes torch tensors' device
 pointers, sizes and torch's current HIP stream to the C entry point of the same
 name and raises MoeError on a non-OK status.  There is no fallback: without the
 built library, importing the first entry point raises.
@@ -280,229 +281,22 @@ def budget_from_memory(free_bytes: int, reserve_bytes: int, expert_bytes: int, l
 
 
 # --------------------------------------------- around the expert FFN --
-# These calls check shapes, types and devices here, take rows at any stride
-# (elements of a row contiguous), and run on the tensors' device: on its
+# These are functions of the compiled module _binding (csrc/binding.cpp), loaded
+# with torch on first use.  They check shapes, types and devices, take rows at any
+# stride (elements of a row contiguous), and run on the tensors' GPU: on its
 # current stream when none is given.
-_DT = None
-_raw_stream = _device = None
+_BOUND = ("route_score_topk", "router_score_topk", "norm_in", "norm_out", "quantize_tokens", "matmul_i8",
+          "gated_matmul_i8")
 
 
-def _setup():
-    """torch's type codes and its queries of the current device and its raw stream (torch is imported on
-    first use only).  The public current_stream() and current_device() cost 2 us of a call that takes 6."""
-    global _DT, _raw_stream, _device
-    import torch
+def __getattr__(name):
+    if name not in _BOUND:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import torch  # noqa: F401  (its libraries come first)
     lib()
-    _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: "int8", torch.int32: "int32"}
-
-
-def _type_error(name, t):
-    return TypeError(f"unsupported dtype {t.dtype} of {name}")
-
-
-def _where_error(name, t, dev):
-    return ValueError(f"{name} is on {t.device}, expected GPU {dev}")
-
-
-def _mat(name, t, rows, cols, dev, kind=None):
-    """(pointer, dtype code, row stride) of t [rows, cols] on GPU dev; kind None: fp32 or bf16, else that type."""
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if t.get_device() != dev:
-        raise _where_error(name, t, dev)
-    code = _DT.get(t.dtype)
-    if (code != kind) if kind is not None else (code != F32 and code != BF16):
-        raise _type_error(name, t)
-    s0, s1 = t.stride()
-    if s1 != 1 and cols > 1:
-        raise ValueError(f"the elements of a row of {name} are not contiguous")
-    return t.data_ptr(), code, (s0 if rows > 1 else cols)
-
-
-def _first(name, t, kind=None):
-    """(GPU, rows, columns, pointer, dtype code, row stride) of the matrix whose shape the others follow."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} is on {t.device}: a GPU is needed")
-    if t.dim() != 2:
-        raise ValueError(f"{name} has {t.dim()} dimensions, expected 2")
-    if _DT is None:
-        _setup()
-    rows, cols = t.shape
-    return (dev, rows, cols) + _mat(name, t, rows, cols, dev, kind)
-
-
-def _vec(name, t, n, dev, kind=None):
-    """(pointer, dtype code) of the n contiguous elements of t on GPU dev (n in all, whatever the shape)."""
-    if t.numel() != n:
-        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
-    if t.get_device() != dev:
-        raise _where_error(name, t, dev)
-    code = _DT.get(t.dtype)
-    if (code != kind) if kind is not None else (code != F32 and code != BF16):
-        raise _type_error(name, t)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
-    return t.data_ptr(), code
-
-
-def _on(dev, stream, fn, *args):
-    """Call fn on GPU dev's current stream (or `stream`, one of that GPU's), with dev current."""
-    if stream is None:
-        s = _raw_stream(dev)
-    else:
-        if stream.device_index != dev:
-            raise ValueError(f"the stream belongs to GPU {stream.device_index}, the tensors are on GPU {dev}")
-        s = stream.cuda_stream
-    if _device() == dev:
-        rc = fn(*args, s)
-    else:
-        import torch
-        with torch.cuda.device(dev):
-            rc = fn(*args, s)
-    if rc:
-        _check(rc)
-
-
-def route_score_topk(logits, k: int, topk_ids, topk_w, score: int = SCORE_SOFTMAX, bias=None, n_group: int = 1,
-                     topk_group: int = 1, group_rank: int = GROUP_MAX, renorm: int = 1, scale: float = 1.0,
-                     stream=None):
-    """Top-k of softmax or sigmoid scores of logits [T, E] plus a bias [E] that counts for the choice
-    only, inside the topk_group best of n_group expert groups; ids int32 and weights fp32 [T, k]."""
-    dev, T, E, lp, ldt, ld = _first("logits", logits)
-    bp = None if bias is None else _vec("bias", bias, E, dev, F32)[0]
-    ip = _vec("topk_ids", topk_ids, T * k, dev, "int32")[0]
-    wp = _vec("topk_w", topk_w, T * k, dev, F32)[0]
-    _on(dev, stream, _lib.moe_route_score_topk, lp, ldt, ld, bp, T, E, k, score, n_group, topk_group, group_rank, renorm,
-        scale, ip, wp)
-
-
-def router_score_topk(x, w_router, k: int, logits, ws, topk_ids, topk_w, score: int = SCORE_SOFTMAX, bias=None,
-                      n_group: int = 1, topk_group: int = 1, group_rank: int = GROUP_MAX, renorm: int = 1,
-                      scale: float = 1.0, stream=None):
-    """fp32 router product of x [T, H] with w_router [E, H] (logits [T, E] out, ws as for router_topk), then
-    route_score_topk on the logits."""
-    dev, T, H, xp, xdt, ldx = _first("x", x)
-    if ldx != H and T > 1:
-        raise ValueError("x is not contiguous")
-    E = w_router.shape[0]
-    wp = _vec("w_router", w_router, E * H, dev, F32)[0]
-    lp = _vec("logits", logits, T * E, dev, F32)[0]
-    bp = None if bias is None else _vec("bias", bias, E, dev, F32)[0]
-    ip = _vec("topk_ids", topk_ids, T * k, dev, "int32")[0]
-    op = _vec("topk_w", topk_w, T * k, dev, F32)[0]
-    if ws.get_device() != dev:
-        raise _where_error("ws", ws, dev)
-    if not ws.is_contiguous():
-        raise ValueError("ws is not contiguous")
-    _on(dev, stream, _lib.moe_router_score_topk, xp, xdt, T, H, wp, E, k, bp, score, n_group, topk_group, group_rank, renorm,
-        scale, lp, ws.data_ptr(), ws.numel() * ws.element_size(), ip, op)
-
-
-def _norm_outputs(T, H, dev, x, xq, xq_scale):
-    xp, xdt, ldx = (None, F32, 0) if x is None else _mat("x", x, T, H, dev)
-    if (xq is None) != (xq_scale is None):
-        raise ValueError("xq and xq_scale go together")
-    if xq is None:
-        return xp, xdt, ldx, None, 0, None
-    qp, _, ldq = _mat("xq", xq, T, H, dev, "int8")
-    return xp, xdt, ldx, qp, ldq, _vec("xq_scale", xq_scale, T, dev, F32)[0]
-
-
-def norm_in(h, w, eps: float, x=None, xq=None, xq_scale=None, w_offset: float = 0.0, stream=None):
-    """RMS norm of the rows of h [T, H] with weight w_offset + w [H] (w None: 1), into x (fp32 or bf16),
-    as int8 codes xq with one fp32 scale per row (xq_scale [T]), or both."""
-    dev, T, H, hp, hdt, ldh = _first("h", h)
-    wp, wdt = (None, F32) if w is None else _vec("w", w, H, dev)
-    _on(dev, stream, _lib.moe_norm_in, hp, hdt, ldh, T, H, wp, wdt, w_offset, eps,
-        *_norm_outputs(T, H, dev, x, xq, xq_scale))
-
-
-def quantize_tokens(x, xq, xq_scale, stream=None):
-    """int8 codes and the scale of each row of x [T, K]: codes rint(x / s), s = max |x| / 127."""
-    dev, T, K, xp, xdt, ldx = _first("x", x)
-    qp, _, ldq = _mat("xq", xq, T, K, dev, "int8")
-    _on(dev, stream, _lib.moe_quantize_tokens, xp, xdt, ldx, T, K, qp, ldq, _vec("xq_scale", xq_scale, T, dev, F32)[0])
-
-
-def norm_out(h, h_out, w_post, eps: float, out_routes=None, topk_w=None, route_pos=None, y=None, gate=None,
-             block_scale: float = 1.0, res_scale: float = 1.0, w_next=None, x=None, xq=None, xq_scale=None,
-             w_offset: float = 0.0, stream=None):
-    """End of a block: h_out = res_scale * h + block_scale * gate * norm(b; w_post), where b is the weighted
-    combine of out_routes (topk_w, route_pos [T, k] as for combine) plus y [T, H]; then, when x or xq is
-    given, the next block's norm of h_out (w_next) into them.  w_post None: b is not normed.  gate
-    broadcasts to [T, H].  h_out may be h."""
-    dev, T, H, hp, hdt, ldh = _first("h", h)
-    op, _, ldo = _mat("h_out", h_out, T, H, dev, hdt)
-    rp = wp = pp = None
-    rdt, k = F32, 0
-    if out_routes is not None:
-        if topk_w is None or route_pos is None:
-            raise ValueError("out_routes needs topk_w and route_pos")
-        R = route_pos.numel()
-        k = R // T if T else 0
-        if k * T != R:
-            raise ValueError(f"route_pos has {R} elements, not a multiple of T={T}")
-        if not out_routes.is_contiguous():
-            raise ValueError("out_routes is not contiguous")
-        rp, rdt, _ = _mat("out_routes", out_routes, R, H, dev)
-        wp = _vec("topk_w", topk_w, R, dev, F32)[0]
-        pp = _vec("route_pos", route_pos, R, dev, "int32")[0]
-    yp, ydt, ldy = (None, F32, 0) if y is None else _mat("y", y, T, H, dev)
-    pw, wdt = (None, F32) if w_post is None else _vec("w_post", w_post, H, dev)
-    nw = None
-    if w_next is not None:
-        nw, ndt = _vec("w_next", w_next, H, dev)
-        if w_post is not None and ndt != wdt:
-            raise TypeError("w_post and w_next have different dtypes")
-        wdt = ndt
-    gp, gdt, gst, gsh = None, F32, 0, 0
-    if gate is not None:
-        # broadcast by hand: gate.expand() alone takes 2 us
-        nd = gate.dim()
-        gr, gc = (1,) * (2 - nd) + tuple(gate.shape) if nd <= 2 else (0, 0)
-        if (gr != 1 and gr != T) or (gc != 1 and gc != H):
-            raise ValueError(f"gate has shape {tuple(gate.shape)}, which does not broadcast to {(T, H)}")
-        if gate.get_device() != dev:
-            raise _where_error("gate", gate, dev)
-        gdt = _DT.get(gate.dtype)
-        if gdt != F32 and gdt != BF16:
-            raise _type_error("gate", gate)
-        st = gate.stride()
-        if gr > 1:
-            gst = st[0]
-        if gc > 1:
-            gsh = st[-1]
-        gp = gate.data_ptr()
-    outs = _norm_outputs(T, H, dev, x, xq, xq_scale)
-    nxt = int(x is not None or xq is not None)
-    if w_next is not None and not nxt:
-        raise ValueError("w_next is given, but neither x nor xq to write the next norm into")
-    _on(dev, stream, _lib.moe_norm_out, rp, rdt, wp, pp, k, yp, ydt, ldy, T, H, pw, wdt, w_offset, eps, gp, gdt, gst, gsh,
-        block_scale, res_scale, hp, hdt, ldh, op, ldo, nxt, nw, *outs)
-
-
-def matmul_i8(xq, x_scale, wq, w_scale, out, bias=None, stream=None):
-    """out [T, N] = (xq [T, K] . wq [N, K]) * x_scale [T] * w_scale [N] (+ bias [N] fp32): int8 codes, exact
-    int32 sums, out fp32 or bf16."""
-    dev, T, K, xp, _, ldx = _first("xq", xq, "int8")
-    N = wq.shape[0]
-    wp, _, ldw = _mat("wq", wq, N, K, dev, "int8")
-    op, odt, ldo = _mat("out", out, T, N, dev)
-    _on(dev, stream, _lib.moe_matmul_i8, xp, ldx, _vec("x_scale", x_scale, T, dev, F32)[0], wp, ldw,
-        _vec("w_scale", w_scale, N, dev, F32)[0], None if bias is None else _vec("bias", bias, N, dev, F32)[0], T, N, K,
-        op, odt, ldo)
-
-
-def gated_matmul_i8(xq, x_scale, wq, w_scale, act: int, out, stream=None):
-    """out [T, F] = act(gate) * up of the int8 product of xq [T, K] with wq [2F, K] (gate rows, then up rows,
-    as an expert's w13)."""
-    dev, T, K, xp, _, ldx = _first("xq", xq, "int8")
-    N2 = wq.shape[0]
-    if N2 % 2:
-        raise ValueError(f"wq has {N2} rows: gate and up rows come in pairs")
-    wp, _, ldw = _mat("wq", wq, N2, K, dev, "int8")
-    op, odt, ldo = _mat("out", out, T, N2 // 2, dev)
-    _on(dev, stream, _lib.moe_gated_matmul_i8, xp, ldx, _vec("x_scale", x_scale, T, dev, F32)[0], wp, ldw,
-        _vec("w_scale", w_scale, N2, dev, F32)[0], T, N2 // 2, K, act, op, odt, ldo)
+    if not os.path.exists(os.path.join(HERE, "_binding.so")):
+        raise ImportError(f"{os.path.join(HERE, '_binding.so')} is missing: build it with __graft_entry__.build()")
+    from . import _binding
+    for n in _BOUND:
+        globals()[n] = getattr(_binding, n)
+    return globals()[name]

@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 from concurrent.futures import ThreadPoolExecutor
@@ -13,6 +14,9 @@ LIB = os.path.join(HERE, "libexpert_ffn.so")
 # measurement kernels of the benchmark (achieved peaks): a library of their own
 PEAKS_SRC = os.path.join(HERE, "measure", "peaks.hip")
 PEAKS_LIB = os.path.join(HERE, "libpeaks.so")
+# Python binding of the operators around the expert FFN
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = os.environ.get("EXPERT_FFN_ARCH", "gfx950")
 
 HIPCC = "/opt/rocm/bin/hipcc" if os.path.exists("/opt/rocm/bin/hipcc") else "hipcc"
@@ -49,14 +53,35 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(compile_one, srcs))
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
+    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libexpert_ffn.so", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
     del deps
     build_peaks()
+    build_binding()
     return LIB
+
+
+def build_binding() -> str:
+    """The compiled Python binding of the operators around the expert FFN (host code, against torch's headers
+    and this library)."""
+    import sysconfig
+    spec = importlib.util.find_spec("torch")
+    torch_dir = os.path.dirname(spec.origin)
+    inc, libs = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", "-I/opt/rocm/include",
+           f"-I{sysconfig.get_paths()['include']}", BINDING_SRC, "-o", tmp,
+           LIB, "-Wl,-rpath,$ORIGIN", f"-L{libs}", f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build_peaks() -> str:

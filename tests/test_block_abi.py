@@ -248,3 +248,29 @@ def test_dense_expert_blob_size(L):
     assert d.w13.shape == (128, 128) and d.w2.shape == (128, 64) and d.s13.shape == (128,) and d.s2.shape == (128,)
     with pytest.raises(ValueError, match="blob"):
         DenseExpert(torch.zeros(n - 1, dtype=torch.uint8), 128, 64)
+
+
+def test_bound_functions():
+    """The compiled binding: names and signatures as documented, and its own argument errors (no GPU needed)."""
+    import inspect
+
+    import expert_ffn_amd as lib
+    want = {"route_score_topk": 12, "router_score_topk": 15, "norm_in": 8, "quantize_tokens": 4, "norm_out": 17, "matmul_i8": 7,
+            "gated_matmul_i8": 7}
+    for name, n in want.items():
+        assert len(inspect.signature(getattr(lib, name)).parameters) == n
+    with pytest.raises(AttributeError):
+        lib.no_such_function
+    h = torch.zeros(2, 64)
+    with pytest.raises(ValueError, match="a GPU is needed"):
+        lib.norm_in(h, None, 1e-6, x=h)
+    with pytest.raises(TypeError, match="missing its argument 'eps'"):
+        lib.norm_in(h, None)
+    with pytest.raises(TypeError, match="unexpected keyword argument 'y'"):
+        lib.norm_in(h, None, 1e-6, y=h)
+    with pytest.raises(TypeError, match="multiple values for argument 'w'"):
+        lib.norm_in(h, None, 1e-6, w=None)
+    with pytest.raises(TypeError, match="takes 4 arguments"):
+        lib.quantize_tokens(h, h, h, None, None)
+    with pytest.raises(TypeError, match="h is not a tensor"):
+        lib.norm_in(None, None, 1e-6)
