@@ -190,7 +190,11 @@ static int row_threads(int nchunk, int cap, int* C) {
     *C = c;
     return ((nchunk + c - 1) / c + 63) / 64 * 64;
 }
-constexpr int NORM_MANY_ROWS = 2048;
+// Many rows: at most 256 threads to a row, so that a CU holds several rows and one's
+// reads run behind another's reductions (8191 bf16 rows of 2816 17.3 us, with up to
+// 1024 threads 20.2; of 8192 48.3 and 52.3).  Few rows: a thread has one chunk if it
+// can (256 rows of 8192 3.8 us, in 256 threads 4.3).
+constexpr int NORM_MANY_ROWS = 1024;
 
 template <int HT, bool NORM>
 static hipError_t norm_in_by_chunks(const void* h, int64_t ldh, int T, int H, const NormOut& o, hipStream_t s) {
@@ -219,74 +223,102 @@ hipError_t launch_quantize_tokens(const void* x, int x_dt, int64_t ldx, int T, i
 }
 
 // After the block.  The routes of a row are requested four at a time, all loads
-// before the first addition; the sums run in ascending j, then y, fp32.  (Eight at
-// a time take 32 registers more: 26.9 us for 1024 rows of 2816 with 8 fp32 routes,
-// four 24.1; requesting the weights and the gate with them, 29.9.)
-constexpr int NO_CH = 4;
-
-__device__ __forceinline__ void gate8(const NormOutParams& p, int t, int c, float (&g)[8]) {
-    const int64_t g0 = static_cast<int64_t>(t) * p.gate_st;
-    if (p.gate_sh != 0) {
-        widen8(load_raw8(p.gate, p.gate_dt, g0 + 8 * c), p.gate_dt, g);
-        return;
-    }
-    const float v = p.gate_dt == F32 ? static_cast<const float*>(p.gate)[g0]
-                                     : bf16_to_f32(static_cast<const uint16_t*>(p.gate)[g0]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = v;
+// before the first addition; the sums run in ascending j, then y, fp32.  (Eight at a
+// time, with the weights and the gate requested at the start, took 3 to 9 % less for
+// 16 to 256 rows of 2816 and 5 to 18 % more for rows of 7168 and for many rows.)
+//
+// The loads go through buffer resources of one row each, sized 0 where there is
+// nothing to read (no y, an absent route, the upper half of a bf16 chunk, chunks past
+// H): such a load gives zeros without a branch.  With branches the compiler waits for
+// every load in flight before the next one (16 rows of 2816 with 8 fp32 routes: 6.0 us,
+// without 5.2; 1024 rows 25.0 and 23.4, 113 MB).
+struct RowSrc {
+    rsrc_t a, b;   // elements 0-3 (fp32) or 0-7 (bf16) of a chunk, elements 4-7
+    uint32_t es;
+};
+__device__ __forceinline__ RowSrc row_src(const void* p, int dt, int64_t i, int H, bool on) {
+    RowSrc r;
+    r.es = dt == F32 ? 4 : 2;
+    const uint8_t* q = static_cast<const uint8_t*>(p) + (on ? i * r.es : 0);
+    const uint32_t n = on ? H * r.es : 0;
+    r.a = make_rsrc(q, n);
+    r.b = make_rsrc(q, dt == F32 ? n : 0);
+    return r;
+}
+__device__ __forceinline__ Raw8 load_src(const RowSrc& r, int c) {
+    const uint32_t o = static_cast<uint32_t>(c) * 8 * r.es;
+    return Raw8{bload16(r.a, o), bload16(r.b, o + 16)};
 }
 
 template <int OT, int C>
 __global__ __launch_bounds__(1024) void norm_out_kernel(NormOutParams p) {
+    constexpr int CH = C == 4 ? 2 : 4;   // (within 128 registers)
     __shared__ RowStat red[2][MAX_WAVES];
     const int t = blockIdx.x, nt = blockDim.x, H = p.H, nchunk = H >> 3;
     const bool codes = p.next && p.n.xq != nullptr;
-    float b[C][8];
-    Raw8 hr[C];
-    auto weight = [&](const void* w, int c, float (&v)[8]) {
-        weight8(w != nullptr ? load_raw8(w, p.w_dt, 8 * c) : Raw8{}, w, p.w_dt, p.w_offset, v);
+    const RowSrc hs = row_src(p.h, p.h_dt, t * p.ldh, H, true), ys = row_src(p.y, p.y_dt, t * p.ldy, H, p.y != nullptr);
+    const RowSrc wps = row_src(p.w_post, p.w_dt, 0, H, p.w_post != nullptr);
+    const RowSrc wns = row_src(p.n.w, p.w_dt, 0, H, p.next && p.n.w != nullptr);
+    // the gate's row, or its one element
+    const RowSrc gs = row_src(p.gate, p.gate_dt, t * p.gate_st, H, p.gate != nullptr && p.gate_sh != 0);
+    const RowSrc g1 = row_src(p.gate, p.gate_dt, t * p.gate_st, 1, p.gate != nullptr && p.gate_sh == 0);
+    auto load_gate = [&](int c) {
+        Raw8 r = load_src(gs, c);
+        // (g1.b has size 0 for bf16)
+        const uint32_t e = __builtin_amdgcn_raw_buffer_load_b32(g1.b, 0, 0, 0), h = bload_u16(g1.a, 0, 0) << 16;
+        if (p.gate_sh == 0) r.a[0] = p.gate_dt == F32 ? e : h;
+        return r;
     };
+    auto gate8 = [&](const Raw8& r, float (&g)[8]) {
+        if (p.gate_sh != 0) {
+            widen8(r, p.gate_dt, g);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = __uint_as_float(r.a[0]);
+    };
+    float b[C][8];
+    Raw8 hr[C], yr[C];
     RowStat st = {0.0f, 0u};
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int c = threadIdx.x + i * nt;
+        hr[i] = load_src(hs, c);
+        yr[i] = load_src(ys, c);
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[i][j] = 0.0f;
-        if (c >= nchunk) continue;
-        hr[i] = load_raw8(p.h, p.h_dt, static_cast<int64_t>(t) * p.ldh + 8 * c);
-        Raw8 yr;
-        if (p.y != nullptr) yr = load_raw8(p.y, p.y_dt, static_cast<int64_t>(t) * p.ldy + 8 * c);
-        for (int j0 = 0; j0 < p.k; j0 += NO_CH) {
-            int pj[NO_CH];
-            float wj[NO_CH];
-            Raw8 rows[NO_CH];
+        for (int j0 = 0; j0 < p.k; j0 += CH) {
+            int pj[CH];
+            float wj[CH];
+            Raw8 rows[CH];
 #pragma unroll
-            for (int q = 0; q < NO_CH; ++q) {
+            for (int q = 0; q < CH; ++q) {
                 const int64_t j = static_cast<int64_t>(t) * p.k + min(j0 + q, p.k - 1);
-                pj[q] = j0 + q < p.k ? p.route_pos[j] : -1;
-                if (pj[q] >= p.T * p.k) pj[q] = -1;
+                pj[q] = p.route_pos[j];
                 wj[q] = p.topk_w[j];
             }
+            __builtin_amdgcn_sched_barrier(0);   // all of them before the first wait
 #pragma unroll
-            for (int q = 0; q < NO_CH; ++q)
-                if (pj[q] >= 0) rows[q] = load_raw8(p.out_routes, OT, static_cast<int64_t>(pj[q]) * H + 8 * c);
+            for (int q = 0; q < CH; ++q) {
+                const bool on = j0 + q < p.k && pj[q] >= 0 && pj[q] < p.T * p.k;
+                wj[q] = on ? wj[q] : 0.0f;
+                rows[q] = load_src(row_src(p.out_routes, OT, static_cast<int64_t>(pj[q]) * H, H, on), c);
+            }
 #pragma unroll
-            for (int q = 0; q < NO_CH; ++q) {
-                if (pj[q] < 0) continue;
+            for (int q = 0; q < CH; ++q) {
                 float v[8];
                 widen8(rows[q], OT, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) b[i][j] = fmaf(wj[q], v[j], b[i][j]);
             }
         }
-        if (p.y != nullptr) {
-            float v[8];
-            widen8(yr, p.y_dt, v);
+        float v[8];
+        widen8(yr[i], p.y_dt, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) b[i][j] += v[j];
+        for (int j = 0; j < 8; ++j) {
+            b[i][j] += v[j];
+            st.sum = fmaf(b[i][j], b[i][j], st.sum);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) st.sum = fmaf(b[i][j], b[i][j], st.sum);
     }
     float r = 1.0f;
     if (p.w_post != nullptr) {
@@ -300,12 +332,12 @@ __global__ __launch_bounds__(1024) void norm_out_kernel(NormOutParams p) {
         if (c >= nchunk) continue;
         float v[8], g[8];
         if (p.w_post != nullptr) {
-            weight(p.w_post, c, v);
+            weight8(load_src(wps, c), p.w_post, p.w_dt, p.w_offset, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) b[i][j] = b[i][j] * r * v[j];
         }
         if (p.gate != nullptr) {
-            gate8(p, t, c, g);
+            gate8(load_gate(c), g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) b[i][j] = b[i][j] * g[j];
         }
@@ -322,7 +354,7 @@ __global__ __launch_bounds__(1024) void norm_out_kernel(NormOutParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) st.sum = fmaf(v[j], v[j], st.sum);
         if (codes) {
-            weight(p.n.w, c, g);
+            weight8(load_src(wns, c), p.n.w, p.w_dt, p.w_offset, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) st.top = max(st.top, abs_bits(v[j] * g[j]));
         }
@@ -339,7 +371,7 @@ __global__ __launch_bounds__(1024) void norm_out_kernel(NormOutParams p) {
         const int c = threadIdx.x + i * nt;
         if (c >= nchunk) continue;
         float w[8], x[8];
-        weight(p.n.w, c, w);
+        weight8(load_src(wns, c), p.n.w, p.w_dt, p.w_offset, w);
         if (p.n.x != nullptr) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = b[i][j] * r * w[j];
@@ -357,8 +389,7 @@ template <int OT>
 static hipError_t norm_out_by_chunks(const NormOutParams& p, hipStream_t s) {
     int C;
     const int nt = row_threads(p.H / 8, 1024, &C);
-    auto kn = C == 1 ? norm_out_kernel<OT, 1>
-                     : C == 2 ? norm_out_kernel<OT, 2> : norm_out_kernel<OT, 4>;
+    auto kn = C == 1 ? norm_out_kernel<OT, 1> : C == 2 ? norm_out_kernel<OT, 2> : norm_out_kernel<OT, 4>;
     hipLaunchKernelGGL(kn, dim3(p.T), dim3(nt), 0, s, p);
     return hipGetLastError();
 }

@@ -54,18 +54,37 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
     v = max(v, dpp_u64<DPP_ROW_MIRROR>(v));
     return swap32_max(swap16_max(v));
 }
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+    return __longlong_as_double(static_cast<long long>(dpp_u64<CTRL>(static_cast<uint64_t>(__double_as_longlong(v)))));
+}
+// sum over the 16 lanes of a row (every lane gets it)
+__device__ __forceinline__ double row_sum(double v) {
+    v += dpp_f64<DPP_QUAD_1032>(v);
+    v += dpp_f64<DPP_QUAD_2301>(v);
+    v += dpp_f64<DPP_ROW_HALF_MIRROR>(v);
+    return v + dpp_f64<DPP_ROW_MIRROR>(v);
+}
+__device__ __forceinline__ double two_halves(uint32_t lo0, uint32_t hi0, uint32_t lo1, uint32_t hi1) {
+    return __hiloint2double(static_cast<int>(hi0), static_cast<int>(lo0)) +
+           __hiloint2double(static_cast<int>(hi1), static_cast<int>(lo1));
+}
 __device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
-    return v;
+    v = row_sum(v);
+    uint32_t l = static_cast<uint32_t>(__double2loint(v)), h = static_cast<uint32_t>(__double2hiint(v));
+    const auto l16 = __builtin_amdgcn_permlane16_swap(l, l, false, false);
+    const auto h16 = __builtin_amdgcn_permlane16_swap(h, h, false, false);
+    v = two_halves(l16[0], h16[0], l16[1], h16[1]);
+    l = static_cast<uint32_t>(__double2loint(v)), h = static_cast<uint32_t>(__double2hiint(v));
+    const auto l32 = __builtin_amdgcn_permlane32_swap(l, l, false, false);
+    const auto h32 = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+    return two_halves(l32[0], h32[0], l32[1], h32[1]);
 }
 // LDS written by some lanes of the wave and read by others of the same wave
 __device__ __forceinline__ void lds_wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
-
-constexpr int SCORE_MAX_GROUPS = 64;
 
 // score of one logit in 64 bits (softmax: before the division); NaN scores 0
 __device__ __forceinline__ double score64(float v, float m, int sigmoid) {
@@ -75,10 +94,10 @@ __device__ __forceinline__ double score64(float v, float m, int sigmoid) {
     return v == m ? 1.0 : exp(static_cast<double>(v) - static_cast<double>(m));
 }
 
-// Ranks of the groups: lane g < G gets group g's first and second largest value
-// (m1, m2) of c [E] in LDS, scanned by P lanes per group (a power of two).
+// The rank of group g in lane g < G: the largest value of c [E] in LDS in the group,
+// or the sum of its two largest.  P lanes scan a group (a power of two).
 template <typename F>
-__device__ __forceinline__ void group_top2(const F* c, int G, int size, F lowest, F* rank, bool top2) {
+__device__ __forceinline__ F group_rank(const F* c, int G, int size, F lowest, bool top2) {
     const int lane = threadIdx.x & 63;
     int lg = 0;   // log2 P
     while ((2 << lg) * G <= 64) ++lg;
@@ -95,18 +114,21 @@ __device__ __forceinline__ void group_top2(const F* c, int G, int size, F lowest
         m2 = max(min(m1, o1), max(m2, o2));
         m1 = max(m1, o1);
     }
-    if (g < G && sub == 0) rank[g] = top2 && size > 1 ? m1 + m2 : m1;
+    return __shfl(top2 && size > 1 ? m1 + m2 : m1, (lane << lg) & 63, 64);
 }
 
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int l) {
+    return (static_cast<uint64_t>(lane_value(static_cast<uint32_t>(v >> 32), l)) << 32) | lane_value(static_cast<uint32_t>(v), l);
+}
 // Bit g: group g (rank key in lane g) is among the keep best, equal keys by the lower group.
 template <typename K>
-__device__ __forceinline__ uint64_t best_groups(const K* key, int G, int keep) {
+__device__ __forceinline__ uint64_t best_groups(K key, int G, int keep) {
     const int lane = threadIdx.x & 63;
-    const K mine = key[lane < G ? lane : 0];
     int before = 0;
     for (int q = 0; q < G; ++q) {
-        const K o = key[q];
-        before += (o > mine || (o == mine && q < lane)) ? 1 : 0;
+        const K o = lane_value(key, q);
+        before += (o > key || (o == key && q < lane)) ? 1 : 0;
     }
     return __ballot(lane < G && before < keep);
 }
@@ -118,8 +140,8 @@ __device__ __forceinline__ int group_of(int e, float inv) { return static_cast<i
 // LDS of one wave
 template <int NPL>
 struct ScoreLds {
-    double c[64 * NPL];                // c of the token (fp32 or fp64)
-    uint64_t g[SCORE_MAX_GROUPS];      // group ranks
+    double c[64 * NPL];   // c of the token (fp32 or fp64)
+    float v[64 * NPL];    // logits
 };
 
 __device__ __forceinline__ float ord_value(uint32_t o) {   // the number of an order image of a number
@@ -178,7 +200,6 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, co
     }
     const bool by_logit = by_logits(p);
     float* cf = reinterpret_cast<float*>(L.c);
-    uint32_t* gu = reinterpret_cast<uint32_t*>(L.g);
 
     // --- 32 bits
     float c[NPL], err = 0.0f;
@@ -211,17 +232,12 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, co
 #pragma unroll
         for (int s = 0; s < NPL; ++s) cf[lane + 64 * s] = c[s] == c[s] ? c[s] : -__builtin_inff();
         lds_wave_sync();
-        float* gf = reinterpret_cast<float*>(L.g) + SCORE_MAX_GROUPS;
-        group_top2<float>(cf, G, size, -__builtin_inff(), gf, p.top2);
-        lds_wave_sync();
-        const float mine = gf[lane < G ? lane : 0];
-        if (lane < G) gu[lane] = logit_ord(mine);
-        lds_wave_sync();
-        const uint64_t kept = best_groups(gu, G, p.topk_group);
+        // of a lane past the groups: never looked at
+        const uint32_t im = logit_ord(group_rank<float>(cf, G, size, -__builtin_inff(), p.top2));
+        const uint64_t kept = best_groups(im, G, p.topk_group);
         if (!by_logit) {
             const bool in = lane < G && ((kept >> lane) & 1ull), out = lane < G && !((kept >> lane) & 1ull);
             // lowest kept and highest dropped rank, as order images
-            const uint32_t im = logit_ord(mine);
             const uint32_t lo = ~wave_max_u32(in ? ~im : 0u), hi = wave_max_u32(out ? im : 0u);
             float two = err;   // of a group's rank: one c, or two and their sum
             if (p.top2) {
@@ -236,8 +252,9 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, co
         for (int s = 0; s < NPL; ++s)
             if (!((kept >> (group_of(lane + 64 * s, inv_size) & 63)) & 1ull)) key[s] = 0u;
     }
+#pragma unroll
+    for (int s = 0; s < NPL; ++s) L.v[lane + 64 * s] = val[s];
     int my_id = 0;
-    float my_logit = 0.0f;
     uint32_t my_key = 0;
     const int rounds = by_logit ? p.k : p.k + 1;   // one more: the first one left out (key 0 if there is none)
     for (int j = 0; j < rounds; ++j) {
@@ -246,22 +263,16 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, co
         for (int s = 1; s < NPL; ++s) best = max(best, key[s]);
         best = __builtin_amdgcn_readfirstlane(wave_max_u32(best));
         int e = 0;
-        float ve = 0.0f;
 #pragma unroll
         for (int s = NPL - 1; s >= 0; --s) {   // ends at the lowest s holding the maximum
             const uint64_t b = __ballot(key[s] == best);
-            if (b != 0ull) {
-                const int ln = __ffsll(static_cast<unsigned long long>(b)) - 1;
-                e = ln + 64 * s;
-                ve = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(val[s]), ln));
-            }
+            e = b != 0ull ? __builtin_ctzll(b) + 64 * s : e;
         }
 #pragma unroll
         for (int s = 0; s < NPL; ++s)
             if (lane + 64 * s == e) key[s] = 0u;
         if (lane == j) {
             my_id = e;
-            my_logit = ve;
             my_key = best;
         }
     }
@@ -299,14 +310,8 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, co
         }
         if (grouped) {
             lds_wave_sync();
-            double* gd = reinterpret_cast<double*>(L.g);
-            group_top2<double>(cd, G, size, -__builtin_inf(), gd, p.top2);
-            lds_wave_sync();
-            const double mine = gd[lane < G ? lane : 0];
-            lds_wave_sync();
-            if (lane < G) L.g[lane] = score_key(mine);
-            lds_wave_sync();
-            const uint64_t kept = best_groups(L.g, G, p.topk_group);
+            const uint64_t kept =
+                best_groups(score_key(group_rank<double>(cd, G, size, -__builtin_inf(), p.top2)), G, p.topk_group);
 #pragma unroll
             for (int s = 0; s < NPL; ++s)
                 if (!((kept >> (group_of(lane + 64 * s, inv_size) & 63)) & 1ull)) key64[s] = 0ull;
@@ -317,27 +322,20 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, co
             for (int s = 1; s < NPL; ++s) best = max(best, key64[s]);
             best = wave_max_u64(best);
             int e = 0;
-            float ve = 0.0f;
 #pragma unroll
             for (int s = NPL - 1; s >= 0; --s) {
                 const uint64_t b = __ballot(key64[s] == best);
-                if (b != 0ull) {
-                    const int ln = __ffsll(static_cast<unsigned long long>(b)) - 1;
-                    e = ln + 64 * s;
-                    ve = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(val[s]), ln));
-                }
+                e = b != 0ull ? __builtin_ctzll(b) + 64 * s : e;
             }
 #pragma unroll
             for (int s = 0; s < NPL; ++s)
                 if (lane + 64 * s == e) key64[s] = 0ull;
-            if (lane == j) {
-                my_id = e;
-                my_logit = ve;
-            }
+            if (lane == j) my_id = e;
         }
     }
     // weights, lane j
-    double w = lane < p.k ? score64(my_logit, m, p.sigmoid) : 0.0;
+    lds_wave_sync();
+    double w = lane < p.k ? score64(L.v[my_id], m, p.sigmoid) : 0.0;
     if (p.renorm) {
         const double sum = wave_sum_f64(w);
         w = sum > 0.0 ? w / sum : 0.0;
@@ -410,16 +408,6 @@ __device__ __forceinline__ float row_sum(float v) {
     v += __uint_as_float(dpp_u32<DPP_QUAD_2301>(__float_as_uint(v)));
     v += __uint_as_float(dpp_u32<DPP_ROW_HALF_MIRROR>(__float_as_uint(v)));
     return v + __uint_as_float(dpp_u32<DPP_ROW_MIRROR>(__float_as_uint(v)));
-}
-template <int CTRL>
-__device__ __forceinline__ double dpp_f64(double v) {
-    return __longlong_as_double(static_cast<long long>(dpp_u64<CTRL>(static_cast<uint64_t>(__double_as_longlong(v)))));
-}
-__device__ __forceinline__ double row_sum(double v) {
-    v += dpp_f64<DPP_QUAD_1032>(v);
-    v += dpp_f64<DPP_QUAD_2301>(v);
-    v += dpp_f64<DPP_ROW_HALF_MIRROR>(v);
-    return v + dpp_f64<DPP_ROW_MIRROR>(v);
 }
 
 // Many tokens: four to a wave, 16 lanes each, lane r with experts r + 16 s.  The
