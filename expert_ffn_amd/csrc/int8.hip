@@ -305,6 +305,132 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
     }
 }
 
+// Few tokens (at most 16 TT): workgroups of 16 weight rows (gated: 8 gate rows and
+// their up rows), so that all CUs take part, and FEW_KG waves that take the 128-byte K
+// steps in turn.  Each wave has a ring of its own, so none waits for another before
+// the sums are added.  MFMA 16x16x64: lane l holds row l & 15, chunk 4 s + (l >> 4) of
+// both operands; swz16 spreads the rows that are read together over all banks.
+//
+// What is left are two round trips to memory and the launch (weights of 16 MB, N =
+// 5632, K = 2816, 16 tokens: 5.1 us, 3.1 TB/s; 6 MB 2.85 us).  Three stages took 0 to 8 %
+// longer, 8 waves 2 to 30 %: more LDS per workgroup leaves fewer of them on a CU.
+__device__ __forceinline__ int swz16(int r) { return (r & 15) >> 1; }
+
+constexpr int FEW_KG = 4, FEW_NSTG = 2;
+
+template <int TT, bool GATED, int OT>
+__global__ __launch_bounds__(64 * FEW_KG) void matmul_i8_few_kernel(MatI8Params p) {
+    constexpr int KG = FEW_KG, NSTG = FEW_NSTG, BK = 128, STAGE = (16 + 16 * TT) * BK, CH = GATED ? 8 : 16, CPS = 2 + 2 * TT;
+    static_assert(KG >= 4 && NSTG >= 2 && CPS * (NSTG - 1) <= 63, "256 threads for the results, copies in flight");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * NSTG * STAGE];
+    __shared__ __attribute__((aligned(16))) int part[KG][TT][256];
+    const int tid = threadIdx.x, lane = tid & 63, kg = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n0 = blockIdx.x * CH, nch = min(CH, p.N - n0);
+    const rsrc_t wr0 = rows_rsrc(p.w, p.ldw, n0, nch, p.K);
+    const rsrc_t wr1 = rows_rsrc(p.w, p.ldw, GATED ? p.N + n0 : n0, nch, p.K);
+    const rsrc_t xr = rows_rsrc(p.x, p.ldx, 0, p.T, p.K);
+    // this thread's results: channel ch of tokens tok, tok + 16 ..
+    const int tok = tid / CH, ch = tid % CH;
+    const bool mine = tid < 16 * CH && ch < nch;
+    float sx[TT] = {}, sg = 0.0f, su = 0.0f, bias = 0.0f;
+    if (mine) {
+#pragma unroll
+        for (int j = 0; j < TT; ++j) sx[j] = p.sx[min(tok + 16 * j, p.T - 1)];
+        sg = p.sw[n0 + ch];
+        if (GATED) su = p.sw[p.N + n0 + ch];
+        if (!GATED && p.bias != nullptr) bias = p.bias[n0 + ch];
+    }
+    // copies: 8 rows each, lane l row l / 8, chunk (l % 8) ^ swz16(row)
+    uint8_t* ring = lds + kg * NSTG * STAGE;
+    uint32_t chunk[2], wo[2], xo[2 * TT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = 8 * i + lane / 8, c = GATED ? row & 7 : row;
+        chunk[i] = ((lane % 8) ^ swz16(row)) * 16;
+        wo[i] = c < nch ? static_cast<uint32_t>(c * p.ldw + chunk[i]) : NO_LANE;
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * TT; ++i) {
+        const int row = 8 * i + lane / 8;
+        xo[i] = row < p.T ? static_cast<uint32_t>(row * p.ldx + chunk[i & 1]) : NO_LANE;
+    }
+    const int nk = ((p.K + BK - 1) / BK + KG - 1) / KG;
+    auto copy = [&](int c, uint8_t* st) {   // chunks past K are zeros
+        const uint32_t k = BK * (c * KG + kg);
+        const uint32_t so = k < static_cast<uint32_t>(p.K) ? k : 0;   // inside the resource
+#pragma unroll
+        for (int i = 0; i < CPS; ++i) {
+            const bool in = k + chunk[i & 1] < static_cast<uint32_t>(p.K);
+            if (i < 2)
+                lds_copy16(i == 0 ? wr0 : wr1, st + i * 8 * BK, in ? wo[i] : NO_LANE, so);
+            else
+                lds_copy16(xr, st + i * 8 * BK, in ? xo[i - 2] : NO_LANE, so);
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < NSTG; ++c) copy(c, ring + c * STAGE);
+    i32x4 acc[TT] = {};
+    const int row = lane & 15, q = lane >> 4;
+    for (int c = 0, buf = 0; c < nk; ++c) {
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(CPS * (NSTG - 1)));
+        asm volatile("" ::: "memory");
+        uint8_t* st = ring + buf * STAGE;
+        u32x4 a[2], b[2][TT];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int o = row * BK + (((4 * s + q) ^ swz16(row)) << 4);
+            a[s] = *reinterpret_cast<const u32x4*>(st + o);
+#pragma unroll
+            for (int j = 0; j < TT; ++j) b[s][j] = *reinterpret_cast<const u32x4*>(st + (16 + 16 * j) * BK + o);
+        }
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(63));   // read, so the buffer may be filled again
+        asm volatile("" ::: "memory");
+        copy(c + NSTG, st);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+                acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a[s]), __builtin_bit_cast(i32x4, b[s][j]),
+                                                               acc[j], 0, 0, 0);
+        buf = buf + 1 == NSTG ? 0 : buf + 1;
+    }
+    // lane l: token l & 15 of tile j, tile rows 4 (l >> 4) ..
+#pragma unroll
+    for (int j = 0; j < TT; ++j) *reinterpret_cast<i32x4*>(&part[kg][j][lane * 4]) = acc[j];
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(0));   // the zero stages past the last have landed too
+    __syncthreads();
+    if (!mine) return;
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        const int t = tok + 16 * j;
+        if (t >= p.T) return;
+        auto total = [&](int r) {
+            int s = 0;
+#pragma unroll
+            for (int g = 0; g < KG; ++g) s += part[g][j][(tok + 16 * (r >> 2)) * 4 + (r & 3)];
+            return static_cast<float>(s);
+        };
+        float v = total(ch) * sx[j] * sg;
+        if (GATED)
+            v = act_fn(p.act, v) * (total(8 + ch) * sx[j] * su);
+        else
+            v += bias;
+        const int64_t o = static_cast<int64_t>(t) * p.ldo + n0 + ch;
+        if (OT == F32)
+            static_cast<float*>(p.out)[o] = v;
+        else
+            static_cast<uint16_t*>(p.out)[o] = static_cast<uint16_t>(pack_bf16x2(v, v));
+    }
+}
+
+template <int TT, bool GATED>
+static hipError_t few(const MatI8Params& p, hipStream_t s) {
+    constexpr int CH = GATED ? 8 : 16;
+    auto kn = p.out_dt == F32 ? matmul_i8_few_kernel<TT, GATED, F32> : matmul_i8_few_kernel<TT, GATED, BF16>;
+    hipLaunchKernelGGL(kn, dim3((p.N + CH - 1) / CH), dim3(64 * FEW_KG), 0, s, p);
+    return hipGetLastError();
+}
+
 template <int BN, int BT, int WN, int WT, int NSTG, int KG, bool GATED>
 static hipError_t tile(const MatI8Params& p, hipStream_t s) {
     constexpr int CH = GATED ? BN / 2 : BN;
@@ -323,7 +449,7 @@ static hipError_t tile(const MatI8Params& p, hipStream_t s) {
 // that of a CU with work in reserve.  The figures (us) are fitted to times of every
 // tile at 96 shapes (T 1 to 4096, N 704 to 8192, K 704 to 8192, both kinds); the
 // choice is then within 1 % of the best tile on average, 6 % at worst.  The ends of
-// the range: T = 16, N = 5632, K = 2816: 32 x 32 6.5 us, 64 x 64 8.3; T = 4096, N =
+// the range: T = 64, N = 2819, K = 1424: 32 x 32 5.0 us, 64 x 64 6.6; T = 4096, N =
 // 8192, K = 4096: 32 x 32 over 400 us, 256 x 128 143, 256 x 256 123.
 struct Tile {
     int bn, bt;
@@ -351,9 +477,17 @@ static int pick_tile(int64_t T, int64_t rows, int K) {
     return best;
 }
 
+// Up to 16 tokens the kernel for few (210 shapes, T 1 to 16, N 704 to 8192, K 704 to
+// 8192: 1.37 times as fast as the best tile on average, T = 16, N = 2112, K = 2816 2.85
+// and 4.9 us, 8 of them slower, N = 8192, K = 4096 10.5 and 8.8).  Up to 32 as long as
+// every workgroup has a CU of its own: 1.36 times as fast (N = 2112, K = 2816 3.9 and
+// 5.0 us); with more, 5 % slower on average.
 template <bool GATED>
 static hipError_t dispatch(const MatI8Params& p, hipStream_t s) {
-    switch (pick_tile(p.T, static_cast<int64_t>(p.N) * (GATED ? 2 : 1), p.K)) {
+    const int64_t rows = static_cast<int64_t>(p.N) * (GATED ? 2 : 1);
+    if (p.T <= 16) return few<1, GATED>(p, s);
+    if (p.T <= 32 && rows <= 256 * 16) return few<2, GATED>(p, s);
+    switch (pick_tile(p.T, rows, p.K)) {
         case 0: return tile<32, 32, 1, 1, 3, 4, GATED>(p, s);
         case 1: return tile<32, 64, 1, 2, 3, 4, GATED>(p, s);
         case 2: return tile<64, 64, 2, 2, 4, 2, GATED>(p, s);

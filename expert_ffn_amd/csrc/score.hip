@@ -413,9 +413,9 @@ __device__ __forceinline__ float row_sum(float v) {
 // Many tokens: four to a wave, 16 lanes each, lane r with experts r + 16 s.  The
 // same steps on rows; one instruction serves four tokens, at the price of longer
 // rounds (a lane looks through 4 times the experts), so it is for launches that
-// fill the chip: by logits from 4096 tokens on (E = 128, k = 8: 4096 tokens 6.3 us
-// either way, 8192 8.2 -> 6.3, 65536 43.9 -> 22.5), with 32-bit scores from 12288
-// on (E = 128: 8192 10.8 against 11.8, 16384 17.4 -> 14.4, 65536 53.9 -> 33.1).
+// fill the chip: by logits from 4096 tokens on (E = 128, k = 8: 4096 tokens 5.1 us
+// either way, 8192 7.4 -> 5.7, 65536 39.4 -> 22.0), with 32-bit scores from 12288
+// on (E = 128: 8192 9.1 against 11.3, 16384 15.3 -> 13.2, 65536 49.1 -> 31.5).
 // A token that is not settled in 32 bits is left to score_token.
 // E <= 256, at most 16 groups, k <= 15.
 template <int VPL>

@@ -429,6 +429,24 @@ def test_gated_matmul_i8(L, T, F, K, ot, act):
     close(f64(out), want, bound + half_step(ot) * (np.abs(want) + bound), "out")
 
 
+# either side of the token and row counts where few tokens go over to tiles
+@pytest.mark.parametrize("T,N,K,ot,bias", [
+    (1, 15, 16, BF16, True), (2, 4099, 144, F32, True), (16, 8192, 4096, BF16, False), (16, 16, 112, F32, False),
+    (17, 4096, 400, BF16, True), (17, 4097, 400, BF16, True), (18, 48, 131056, F32, False), (32, 1000, 1424, F32, True),
+    (32, 4200, 704, BF16, False), (33, 1000, 1424, F32, True),
+])
+def test_matmul_i8_few_tokens(L, T, N, K, ot, bias):
+    test_matmul_i8(L, T, N, K, ot, bias)
+
+
+@pytest.mark.parametrize("T,F,K,ot,act", [
+    (1, 7, 16, F32, 0), (5, 2049, 528, BF16, 1), (16, 9, 1424, BF16, 0), (17, 2048, 400, F32, 0), (17, 2049, 400, F32, 1),
+    (32, 300, 2816, BF16, 0), (32, 2100, 272, BF16, 1),
+])
+def test_gated_matmul_i8_few_tokens(L, T, F, K, ot, act):
+    test_gated_matmul_i8(L, T, F, K, ot, act)
+
+
 def test_matmul_i8_non_finite_scales(L):
     """A token whose scale is NaN or infinite gives NaN there and leaves the others alone."""
     g = gen(2)
