@@ -70,7 +70,7 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
     constexpr int RING = NSTG * STAGE, NTH = 64 * NW * KG;
     static_assert(DA * RPC * NW == BN && DB * RPC * NW == BT && BN % 32 == 0, "tile shape");
     static_assert(NSTG >= 2 && CPS * (NSTG - 1) <= 63, "copies in flight");
-    static_assert((KG - 1) * BN * BT * 4 <= KG * RING && 32 * CW * 4 * NW <= KG * RING, "epilogue regions");
+    static_assert((KG - 1) * BN * BT * 4 <= KG * RING, "epilogue regions");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * RING];
     __shared__ float sws[BN], sxs[BT], bs[BN];
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -238,10 +238,13 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
     // groups, the partial sums may lie where another wave of group 0 still reads:
     // the waves' regions start behind them.
     constexpr int PART = KG > 1 ? (KG - 1) * BN * BT * 4 : 0;
-    static_assert(PART + 32 * CW * 4 * NW <= KG * RING, "epilogue regions");
-    uint8_t* my = lds + PART + wave * 32 * CW * 4;
     constexpr bool f32 = OT == F32;
-    constexpr int es = f32 ? 4 : 2, cpr = CW * es / 16;   // 16-byte chunks per row (a power of two)
+    constexpr int es = f32 ? 4 : 2, cpr = CW * es / 16;   // 16-byte chunks per row
+    constexpr bool p2 = (cpr & (cpr - 1)) == 0;           // else the rows are 16 bytes apart instead
+    constexpr int RS = CW * es + (p2 ? 0 : 16);
+    static_assert(PART + 32 * RS * NW <= KG * RING, "epilogue regions");
+    uint8_t* my = lds + PART + wave * 32 * RS;
+    auto at = [&](int tok, int c) { return my + tok * RS + ((p2 ? c ^ (tok & (cpr - 1)) : c) << 4); };
     const bool vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo * es % 16 == 0;
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb) {
@@ -263,10 +266,9 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
                         v[j] += bs[rw + j];
                 }
                 if (f32) {
-                    *reinterpret_cast<f32x4*>(my + l32 * CW * 4 + (((cl >> 2) ^ (l32 & (cpr - 1))) << 4)) =
-                        f32x4{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<f32x4*>(at(l32, cl >> 2)) = f32x4{v[0], v[1], v[2], v[3]};
                 } else {
-                    *reinterpret_cast<u32x2*>(my + l32 * CW * 2 + (((cl >> 3) ^ (l32 & (cpr - 1))) << 4) + 8 * hh) =
+                    *reinterpret_cast<u32x2*>(at(l32, cl >> 3) + 8 * hh) =
                         u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                 }
             }
@@ -275,8 +277,8 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
 #pragma unroll 4
         for (int i0 = 0; i0 < 32 * cpr; i0 += 64) {
             const int it = i0 + lane;
-            const int tok = it / cpr, c = it & (cpr - 1);
-            const u32x4 v = *reinterpret_cast<const u32x4*>(my + tok * CW * es + ((c ^ (tok & (cpr - 1))) << 4));
+            const int tok = it / cpr, c = it % cpr;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(at(tok, c));
             const int t = tl + tok, ch = wn * CW + c * (16 / es);
             if (t >= ntok || ch >= nch) continue;
             const int64_t o = static_cast<int64_t>(t0 + t) * p.ldo + n0 + ch;
@@ -444,20 +446,24 @@ static hipError_t tile(const MatI8Params& p, hipStream_t s) {
 
 // Which tile: the one with the smallest estimated time.  A launch of W workgroups
 // over 256 CUs takes ceil(W / 256) of them after each other, so with `steps`
-// 128-byte K steps about steps * max(alone, ceil(W / 256) * full) + fixed: `alone` is
-// the time of a step when a CU has one workgroup and waits for its copies, `full`
-// that of a CU with work in reserve.  The figures (us) are fitted to times of every
-// tile at 96 shapes (T 1 to 4096, N 704 to 8192, K 704 to 8192, both kinds); the
-// choice is then within 1 % of the best tile on average, 6 % at worst.  The ends of
-// the range: T = 64, N = 2819, K = 1424: 32 x 32 5.0 us, 64 x 64 6.6; T = 4096, N =
-// 8192, K = 4096: 32 x 32 over 400 us, 256 x 128 143, 256 x 256 123.
+// 128-byte K steps about steps * max(alone, ceil(W / 256) * full) + fixed: `full` is
+// the time of a step, `alone` that of a workgroup that has its CU for itself where it
+// is longer (several of the 64 x 64 ones fit on a CU).  The figures (us) are fitted to
+// times of every tile at 199 shapes (T 20 to 16384, N 704 to 16384, K 704 to 8192, both
+// kinds); the choice is then within 0.3 % of the best tile on average, 9 % at worst.
+// The ends of the range: T = 64, N = 2819, K = 1424: 32 x 32 5.0 us, 64 x 64 6.6; T =
+// 4096, N = 8192, K = 4096: 32 x 32 over 400 us, 256 x 128 143, 256 x 256 123.  The one
+// that is no power of two fills the CUs where its neighbours leave half of them idle
+// or need a second round (T = 1024, gated, N = 2112, K = 2816: 17.7 us, 256 x 128 20.1,
+// 128 x 128 26.3); without it the choice is 1.2 % slower on average, 17 % at worst.
 struct Tile {
     int bn, bt;
     float alone, full, fixed;
 };
 constexpr Tile TILES[] = {
-    {32, 32, 0.09f, 0.11f, 1.4f},  {32, 64, 0.11f, 0.12f, 1.5f},   {64, 64, 0.14f, 0.17f, 2.5f},  {64, 64, 0.31f, 0.18f, 0.0f},
-    {128, 64, 0.19f, 0.33f, 0.2f}, {128, 128, 0.43f, 0.49f, 0.2f}, {256, 128, 0.50f, 0.75f, 0.5f}, {256, 256, 1.06f, 1.15f, 0.9f},
+    {32, 32, 0.12f, 0.12f, 1.3f},   {32, 64, 0.13f, 0.13f, 1.9f},   {64, 64, 0.18f, 0.18f, 1.9f},
+    {64, 64, 0.31f, 0.21f, 0.1f},   {128, 64, 0.34f, 0.34f, 0.2f},  {128, 128, 0.54f, 0.54f, 0.1f},
+    {192, 128, 0.66f, 0.66f, 0.8f}, {256, 128, 0.75f, 0.75f, 1.3f}, {256, 256, 1.32f, 1.32f, 0.3f},
 };
 constexpr int N_TILES = sizeof(TILES) / sizeof(TILES[0]);
 
@@ -494,7 +500,8 @@ static hipError_t dispatch(const MatI8Params& p, hipStream_t s) {
         case 3: return tile<64, 64, 2, 2, 3, 1, GATED>(p, s);
         case 4: return tile<128, 64, 2, 2, 3, 1, GATED>(p, s);
         case 5: return tile<128, 128, 2, 4, 4, 1, GATED>(p, s);
-        case 6: return tile<256, 128, 4, 2, 3, 1, GATED>(p, s);
+        case 6: return tile<192, 128, 2, 4, 3, 1, GATED>(p, s);
+        case 7: return tile<256, 128, 4, 2, 3, 1, GATED>(p, s);
         default: return tile<256, 256, 4, 2, 2, 1, GATED>(p, s);
     }
 }
