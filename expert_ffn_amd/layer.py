@@ -7,9 +7,10 @@ from __future__ import annotations
 
 import torch
 
-from . import (ACT_GELU_TANH, F32, GROUP_MAX, SCORE_SOFTMAX, W_INT8_ROW, blob_layout, combine,
-               expert_ffn, ffn_down, ffn_gate_up, gated_matmul_i8, matmul_i8, min_weight, norm_in, norm_out, permute,
-               quantize_tokens, route_topk, router_score_topk, router_ws_bytes, workspace_bytes)
+import expert_ffn_amd as ops
+
+from . import (ACT_GELU_TANH, F32, GROUP_MAX, SCORE_SOFTMAX, W_INT8_ROW, blob_layout, combine, expert_ffn, ffn_down,
+               ffn_gate_up, min_weight, permute, route_topk, router_ws_bytes, workspace_bytes)
 
 
 class MoeLayer:
@@ -145,9 +146,9 @@ class MoeBlock:
     def run_dense(self, T, stream=None):
         """The dense expert on the codes of the last norm: its rows in yd."""
         e = self.dense
-        gated_matmul_i8(self.xq[:T], self.xs[:T], e.w13, e.s13, e.act, self.hid[:T], stream)
-        quantize_tokens(self.hid[:T], self.hq[:T], self.hs[:T], stream)
-        matmul_i8(self.hq[:T], self.hs[:T], e.w2, e.s2, self.yd[:T], stream=stream)
+        ops.gated_matmul_i8(self.xq[:T], self.xs[:T], e.w13, e.s13, e.act, self.hid[:T], stream)
+        ops.quantize_tokens(self.hid[:T], self.hq[:T], self.hs[:T], stream)
+        ops.matmul_i8(self.hq[:T], self.hs[:T], e.w2, e.s2, self.yd[:T], stream=stream)
         return self.yd[:T]
 
     def run(self, h, h_out, stream=None):
@@ -161,17 +162,17 @@ class MoeBlock:
     def _run(self, h, h_out, stream):
         T, L = h.shape[0], self.layer
         codes = dict(xq=self.xq[:T], xq_scale=self.xs[:T]) if self.dense is not None else {}
-        norm_in(h, self.w_in, self.eps, x=self.x[:T], w_offset=self.w_offset, stream=stream, **codes)
-        router_score_topk(self.x[:T], self.w_router, L.k, self.logits[:T], self.router_ws, L.topk_ids[:T], L.topk_w[:T],
-                          stream=stream, **self.routing)
+        ops.norm_in(h, self.w_in, self.eps, x=self.x[:T], w_offset=self.w_offset, stream=stream, **codes)
+        ops.router_score_topk(self.x[:T], self.w_router, L.k, self.logits[:T], self.router_ws, L.topk_ids[:T],
+                              L.topk_w[:T], stream=stream, **self.routing)
         L.group(T, stream)
         L.ffn(self.x[:T], stream)
         y = self.run_dense(T, stream) if self.dense is not None else None
         gate = self.gate[:T] if self.gate is not None and self.gate.dim() == 2 and self.gate.shape[0] > 1 else self.gate
         nxt = self.x_next[:T] if self.x_next is not None else None
-        norm_out(h, h_out, self.w_post, self.eps, out_routes=L.out_routes[:T * L.k], topk_w=L.topk_w[:T],
-                 route_pos=L.route_pos[:T * L.k], y=y, gate=gate, block_scale=self.block_scale,
-                 res_scale=self.res_scale, w_next=self.w_next, x=nxt, w_offset=self.w_offset, stream=stream)
+        ops.norm_out(h, h_out, self.w_post, self.eps, out_routes=L.out_routes[:T * L.k], topk_w=L.topk_w[:T],
+                     route_pos=L.route_pos[:T * L.k], y=y, gate=gate, block_scale=self.block_scale,
+                     res_scale=self.res_scale, w_next=self.w_next, x=nxt, w_offset=self.w_offset, stream=stream)
         return h_out, nxt
 
 

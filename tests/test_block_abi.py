@@ -274,3 +274,16 @@ def test_bound_functions():
         lib.quantize_tokens(h, h, h, None, None)
     with pytest.raises(TypeError, match="h is not a tensor"):
         lib.norm_in(None, None, 1e-6)
+
+
+def test_layer_imports_without_the_library(tmp_path):
+    """Nothing of the package is loaded before the first call; then a missing build raises."""
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import expert_ffn_amd as lib\n"
+            f"lib.LIB_PATH = {str(tmp_path / 'none.so')!r}\n"
+            "import expert_ffn_amd.layer\n"
+            "try:\n    lib.norm_in\nexcept ImportError as e:\n    print('refused:', e)\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120, cwd=root)
+    assert r.returncode == 0 and "refused:" in r.stdout and "is missing" in r.stdout, r.stdout + r.stderr
