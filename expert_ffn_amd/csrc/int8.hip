@@ -69,7 +69,7 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
     constexpr int CW = CH / WN;               // of a wave
     constexpr int RING = NSTG * STAGE, NTH = 64 * NW * KG;
     static_assert(DA * RPC * NW == BN && DB * RPC * NW == BT && BN % 32 == 0, "tile shape");
-    static_assert(NSTG >= 2 && CPS * (NSTG - 1) <= 63, "copies in flight");
+    static_assert(NSTG >= 2 && NSTG <= 4 && CPS * (NSTG - 1) <= 63, "copies in flight");
     static_assert((KG - 1) * BN * BT * 4 <= KG * RING, "epilogue regions");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * RING];
     __shared__ float sws[BN], sxs[BT], bs[BN];
@@ -105,10 +105,13 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
         const int row = crow(i);
         bo[i] = row < ntok ? static_cast<uint32_t>(row * p.ldx + chunk(i)) : NO_LANE;
     }
-    const int nk = ((p.K + BK - 1) / BK + KG - 1) / KG;   // steps of each group (past K: zeros)
+    const int nk = ((p.K + BK - 1) / BK + KG - 1) / KG;   // steps of each group, the same for all
     // copy i of stage c: weight rows (RPC of them lie on one side of a gated
-    // block), then tokens.  Chunks past K, and whole stages past the last, are zeros:
-    // nothing is read for them, and the count of copies in flight stays uniform.
+    // block), then tokens.  Chunks past K are zeros: nothing is read for them.
+    // Stages past the last are not requested either, by a copy of the loop's body
+    // without copies (32 to 128 tokens: 3 to 4 % less time).  The largest tile requests them as zeros: its body is 10 KB, and
+    // twice that took 1 to 7 % longer.
+    constexpr bool TAIL = NSTG > 2;
     auto copy = [&](int c, uint8_t* st, int i) {
         const int k = BK * (c * KG + kg);
         // the scalar offset stays inside the resource: the range check subtracts it
@@ -172,9 +175,11 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
         }
     };
 #pragma unroll
-    for (int c = 0; c < NSTG; ++c)
+    for (int c = 0; c < NSTG; ++c) {
+        if (TAIL && c >= nk) break;
 #pragma unroll
         for (int q = 0; q < CPS; ++q) copy(c, ring + c * STAGE, q);
+    }
     // per-row factors, behind the first copies
     for (int i = tid; i < BN; i += NTH) {
         const int c = channel(i);
@@ -187,10 +192,15 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
     __syncthreads();
     read(ring, 0, 0);
     most(ring, -1, ring);
-    for (int c = 0, buf = 0; c + 1 < nk; ++c) {
-        // stages up to c + NSTG - 1 have been requested: all but the last NSTG - 2
-        // of them must have landed, and the operands of step c's last round too
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(CPS * (NSTG - 2)));
+    int buf = 0;
+    // from step c to step c + 1: `left` of the stages behind that one may still be on their way
+    auto step = [&](int left, int next) {
+        if (NSTG > 3 && left >= 2)
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(CPS * 2));
+        else if (NSTG > 2 && left >= 1)
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(CPS));
+        else
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(0));
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
@@ -199,11 +209,15 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
         const uint8_t* st = ring + buf * STAGE;
         read(st, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
-        round(S - 1, c + NSTG, done);
-        most(st, c + NSTG, done);
-    }
+        round(S - 1, next, done);
+        most(st, next, done);
+    };
+    int c = 0;
+    for (; c + (TAIL ? NSTG : 1) < nk; ++c) step(NSTG - 2, c + NSTG);
+    if (TAIL)
+        for (; c + 1 < nk; ++c) step(nk - 2 - c, -1);
     round(S - 1, -1, ring);
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(0));   // the zero stages past the last have landed too
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(0));   // zero stages have landed too
     __syncthreads();   // the rings are free
     if (KG > 1) {
         int* part = reinterpret_cast<int*>(lds);
@@ -314,7 +328,7 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
 // both operands; swz16 spreads the rows that are read together over all banks.
 //
 // What is left are two round trips to memory and the launch (weights of 16 MB, N =
-// 5632, K = 2816, 16 tokens: 5.1 us, 3.1 TB/s; 6 MB 2.85 us).  Three stages took 0 to 8 %
+// 5632, K = 2816, 16 tokens: 5.0 us, 3.2 TB/s; 6 MB 2.8 us).  Three stages took 0 to 8 %
 // longer, 8 waves 2 to 30 %: more LDS per workgroup leaves fewer of them on a CU.
 __device__ __forceinline__ int swz16(int r) { return (r & 15) >> 1; }
 
@@ -323,7 +337,7 @@ constexpr int FEW_KG = 4, FEW_NSTG = 2;
 template <int TT, bool GATED, int OT>
 __global__ __launch_bounds__(64 * FEW_KG) void matmul_i8_few_kernel(MatI8Params p) {
     constexpr int KG = FEW_KG, NSTG = FEW_NSTG, BK = 128, STAGE = (16 + 16 * TT) * BK, CH = GATED ? 8 : 16, CPS = 2 + 2 * TT;
-    static_assert(KG >= 4 && NSTG >= 2 && CPS * (NSTG - 1) <= 63, "256 threads for the results, copies in flight");
+    static_assert(KG >= 4 && NSTG == 2 && CPS <= 63, "256 threads for the results, copies in flight");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * NSTG * STAGE];
     __shared__ __attribute__((aligned(16))) int part[KG][TT][256];
     const int tid = threadIdx.x, lane = tid & 63, kg = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -357,7 +371,9 @@ __global__ __launch_bounds__(64 * FEW_KG) void matmul_i8_few_kernel(MatI8Params 
         xo[i] = row < p.T ? static_cast<uint32_t>(row * p.ldx + chunk[i & 1]) : NO_LANE;
     }
     const int nk = ((p.K + BK - 1) / BK + KG - 1) / KG;
-    auto copy = [&](int c, uint8_t* st) {   // chunks past K are zeros
+    // chunks past K are zeros; stages past the last are not requested (T = 16, N = 5632,
+    // K = 704: 3.0 -> 2.7 us)
+    auto copy = [&](int c, uint8_t* st) {
         const uint32_t k = BK * (c * KG + kg);
         const uint32_t so = k < static_cast<uint32_t>(p.K) ? k : 0;   // inside the resource
 #pragma unroll
@@ -370,11 +386,15 @@ __global__ __launch_bounds__(64 * FEW_KG) void matmul_i8_few_kernel(MatI8Params 
         }
     };
 #pragma unroll
-    for (int c = 0; c < NSTG; ++c) copy(c, ring + c * STAGE);
+    for (int c = 0; c < NSTG; ++c)
+        if (c < nk) copy(c, ring + c * STAGE);
     i32x4 acc[TT] = {};
     const int row = lane & 15, q = lane >> 4;
     for (int c = 0, buf = 0; c < nk; ++c) {
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(CPS * (NSTG - 1)));
+        if (c + 1 < nk)
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(CPS));   // the next stage may still be on its way
+        else
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
         asm volatile("" ::: "memory");
         uint8_t* st = ring + buf * STAGE;
         u32x4 a[2], b[2][TT];
@@ -387,7 +407,7 @@ __global__ __launch_bounds__(64 * FEW_KG) void matmul_i8_few_kernel(MatI8Params 
         }
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(63));   // read, so the buffer may be filled again
         asm volatile("" ::: "memory");
-        copy(c + NSTG, st);
+        if (c + NSTG < nk) copy(c + NSTG, st);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -399,7 +419,6 @@ __global__ __launch_bounds__(64 * FEW_KG) void matmul_i8_few_kernel(MatI8Params 
     // lane l: token l & 15 of tile j, tile rows 4 (l >> 4) ..
 #pragma unroll
     for (int j = 0; j < TT; ++j) *reinterpret_cast<i32x4*>(&part[kg][j][lane * 4]) = acc[j];
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(0));   // the zero stages past the last have landed too
     __syncthreads();
     if (!mine) return;
 #pragma unroll
