@@ -468,21 +468,22 @@ static hipError_t tile(const MatI8Params& p, hipStream_t s) {
 // 128-byte K steps about steps * max(alone, ceil(W / 256) * full) + fixed: `full` is
 // the time of a step, `alone` that of a workgroup that has its CU for itself where it
 // is longer (several of the 64 x 64 ones fit on a CU).  The figures (us) are fitted to
-// times of every tile at 199 shapes (T 20 to 16384, N 704 to 16384, K 704 to 8192, both
-// kinds); the choice is then within 0.3 % of the best tile on average, 9 % at worst.
+// times of every tile at 274 shapes (T 20 to 16384, N 704 to 16384, K 704 to 8192, both
+// kinds); the choice is then within 0.2 % of the best tile on average, 11 % at worst.
 // The ends of the range: T = 64, N = 2819, K = 1424: 32 x 32 5.0 us, 64 x 64 6.6; T =
-// 4096, N = 8192, K = 4096: 32 x 32 over 400 us, 256 x 128 143, 256 x 256 123.  The one
-// that is no power of two fills the CUs where its neighbours leave half of them idle
-// or need a second round (T = 1024, gated, N = 2112, K = 2816: 17.7 us, 256 x 128 20.1,
-// 128 x 128 26.3); without it the choice is 1.2 % slower on average, 17 % at worst.
+// 4096, N = 8192, K = 4096: 32 x 32 over 400 us, 256 x 128 143, 256 x 256 123.  The two
+// that are no powers of two fill the CUs where their neighbours leave many of them idle
+// or need a second round (T = 1024, gated, N = 2112, K = 2816: 192 x 128 17.7 us, 256 x
+// 128 20.1, 128 x 128 26.3; T = 2048: 256 x 192 31.0 us, 256 x 256 36.3, 256 x 128 41.1);
+// without them the choice is 2 % slower on average, 18 % at worst.
 struct Tile {
     int bn, bt;
     float alone, full, fixed;
 };
 constexpr Tile TILES[] = {
-    {32, 32, 0.12f, 0.12f, 1.3f},   {32, 64, 0.13f, 0.13f, 1.9f},   {64, 64, 0.18f, 0.18f, 1.9f},
-    {64, 64, 0.31f, 0.21f, 0.1f},   {128, 64, 0.34f, 0.34f, 0.2f},  {128, 128, 0.54f, 0.54f, 0.1f},
-    {192, 128, 0.66f, 0.66f, 0.8f}, {256, 128, 0.75f, 0.75f, 1.3f}, {256, 256, 1.32f, 1.32f, 0.3f},
+    {32, 32, 0.12f, 0.12f, 1.3f},   {32, 64, 0.14f, 0.14f, 1.7f},   {64, 64, 0.18f, 0.18f, 1.9f},   {64, 64, 0.32f, 0.20f, 0.2f},
+    {128, 64, 0.32f, 0.32f, 1.2f},  {128, 128, 0.52f, 0.52f, 0.4f}, {192, 128, 0.66f, 0.66f, 0.7f}, {256, 128, 0.79f, 0.79f, 1.1f},
+    {256, 192, 1.08f, 1.08f, 1.1f}, {256, 256, 1.32f, 1.32f, 0.3f},
 };
 constexpr int N_TILES = sizeof(TILES) / sizeof(TILES[0]);
 
@@ -521,6 +522,7 @@ static hipError_t dispatch(const MatI8Params& p, hipStream_t s) {
         case 5: return tile<128, 128, 2, 4, 4, 1, GATED>(p, s);
         case 6: return tile<192, 128, 2, 4, 3, 1, GATED>(p, s);
         case 7: return tile<256, 128, 4, 2, 3, 1, GATED>(p, s);
+        case 8: return tile<256, 192, 4, 2, 2, 1, GATED>(p, s);
         default: return tile<256, 256, 4, 2, 2, 1, GATED>(p, s);
     }
 }

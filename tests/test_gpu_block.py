@@ -433,7 +433,8 @@ def test_gated_matmul_i8(L, T, F, K, ot, act):
 @pytest.mark.parametrize("T,N,K,ot,bias", [
     (50, 130, 1424, F32, True), (130, 2053, 1424, BF16, True), (77, 4101, 2816, F32, False), (77, 130, 400, BF16, True),
     (200, 4101, 272, F32, True), (200, 8200, 272, BF16, True), (1030, 4101, 272, F32, True), (1030, 4101, 272, BF16, False),
-    (3000, 2053, 400, F32, False), (1030, 8200, 272, BF16, True),
+    (3000, 2053, 400, F32, False), (1030, 8200, 272, BF16, True), (200, 4101, 2816, BF16, False), (1030, 8200, 400, F32, True),
+    (2100, 4101, 400, BF16, True),
 ])
 def test_matmul_i8_tiles(L, T, N, K, ot, bias):
     test_matmul_i8(L, T, N, K, ot, bias)
@@ -442,7 +443,8 @@ def test_matmul_i8_tiles(L, T, N, K, ot, bias):
 @pytest.mark.parametrize("T,F,K,ot,act", [
     (77, 130, 1424, BF16, 0), (200, 601, 1424, F32, 1), (200, 1100, 2816, BF16, 1), (77, 130, 272, F32, 0),
     (77, 4101, 272, BF16, 0), (200, 4101, 272, F32, 0), (1030, 2053, 272, BF16, 0), (1030, 2053, 272, F32, 1),
-    (3000, 1100, 400, BF16, 1), (1030, 4101, 272, F32, 0),
+    (3000, 1100, 400, BF16, 1), (1030, 4101, 272, F32, 0), (77, 4101, 2816, F32, 1), (1030, 4101, 400, BF16, 0),
+    (2100, 2053, 400, F32, 1),
 ])
 def test_gated_matmul_i8_tiles(L, T, F, K, ot, act):
     test_gated_matmul_i8(L, T, F, K, ot, act)
