@@ -327,8 +327,8 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
 // the sums are added.  MFMA 16x16x64: lane l holds row l & 15, chunk 4 s + (l >> 4) of
 // both operands; swz16 spreads the rows that are read together over all banks.
 //
-// What is left are two round trips to memory and the launch (weights of 16 MB, N =
-// 5632, K = 2816, 16 tokens: 5.0 us, 3.2 TB/s; 6 MB 2.8 us).  Three stages took 0 to 8 %
+// What is left are the launch, about 2 us of the kernel's time, and the memory's rate
+// (16 MB of weights, N = 5632, K = 2816, 16 tokens: 4.9 us; 6 MB: 2.9 us).  Three stages took 0 to 8 %
 // longer, 8 waves 2 to 30 %: more LDS per workgroup leaves fewer of them on a CU.
 __device__ __forceinline__ int swz16(int r) { return (r & 15) >> 1; }
 

@@ -10,7 +10,8 @@
 // 64-bit exponentials and keys of every expert cost three times the instructions,
 // and a wave is bound by instructions here (T = 16383, E = 160, 6 MB of logits: 30 us
 // in 64 bits, 10 as below).  So:
-//   - without a bias the scores order like the logits, and the logits are compared;
+//   - without a bias the scores order like the logits, and the logits are compared
+//     (all but sums of two scores that rank groups);
 //   - else the scores are taken in 32 bits with a bound on their error.  Where
 //     every gap that decides (between groups, between consecutive choices and the
 //     first one left out) exceeds twice the bound, the 64-bit choice is the same;
@@ -163,9 +164,10 @@ __device__ __forceinline__ bool settled(float a, float b, float err) {
 }
 // |c| of a finite c (an infinite one is exact)
 __device__ __forceinline__ float finite_size(float c) { return fabsf(c) < __builtin_inff() ? fabsf(c) : 0.0f; }
-// the scores order like the logits, and nothing adds them up
-__device__ __forceinline__ bool by_logits(const ScoreRouteParams& p) {
-    return p.bias == nullptr && !(p.topk_group < p.n_group && p.top2);
+// nothing adds scores up: without a bias they order like the logits, and groups need
+// them only for sums of two
+__host__ __device__ __forceinline__ bool by_logits(const ScoreRouteParams& p) {
+    return p.bias == nullptr && !(p.topk_group < p.n_group && p.top2 && p.n_group < p.E);
 }
 __device__ __forceinline__ float load_logit(const ScoreRouteParams& p, int t, int e) {
     const int64_t i = static_cast<int64_t>(t) * p.ld + e;
@@ -224,17 +226,46 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, co
             if (!(val[s] == val[s])) c[s] = __builtin_nanf("");
         }
     }
-    bool sure = true;
+    // --- 64 bits, where they are wanted: scores (softmax: before the division) and their sum
+    double sc[NPL], sum64 = 0.0;
+    auto scores64 = [&]() {
+#pragma unroll
+        for (int s = 0; s < NPL; ++s) {
+            sc[s] = score64(val[s], m, p.sigmoid);
+            sum64 += sc[s];
+        }
+        if (!p.sigmoid) sum64 = wave_sum_f64(sum64);
+    };
+    // sc becomes c (NaN where the logit is), returns the kept groups
+    auto kept64 = [&]() -> uint64_t {
+        double* cd = L.c;
+        lds_wave_sync();   // the 32-bit values have been read
+#pragma unroll
+        for (int s = 0; s < NPL; ++s) {
+            double x = sc[s];
+            if (!p.sigmoid) x = sum64 > 0.0 ? x / sum64 : 0.0;
+            x += static_cast<double>(bias[s]);
+            if (!(val[s] == val[s])) x = __builtin_nan("");
+            cd[lane + 64 * s] = x == x ? x : -__builtin_inf();
+            sc[s] = x;
+        }
+        if (!grouped) return ~0ull;
+        lds_wave_sync();
+        return best_groups(score_key(group_rank<double>(cd, G, size, -__builtin_inf(), p.top2)), G, p.topk_group);
+    };
+
+    bool sure = true, have64 = false;
+    const bool plain = p.bias == nullptr;
     uint32_t key[NPL];
 #pragma unroll
-    for (int s = 0; s < NPL; ++s) key[s] = lane + 64 * s < E ? logit_ord(c[s]) : 0u;
+    for (int s = 0; s < NPL; ++s) key[s] = lane + 64 * s < E ? logit_ord(plain ? val[s] : c[s]) : 0u;
     if (grouped) {
 #pragma unroll
         for (int s = 0; s < NPL; ++s) cf[lane + 64 * s] = c[s] == c[s] ? c[s] : -__builtin_inff();
         lds_wave_sync();
         // of a lane past the groups: never looked at
         const uint32_t im = logit_ord(group_rank<float>(cf, G, size, -__builtin_inff(), p.top2));
-        const uint64_t kept = best_groups(im, G, p.topk_group);
+        uint64_t kept = best_groups(im, G, p.topk_group);
         if (!by_logit) {
             const bool in = lane < G && ((kept >> lane) & 1ull), out = lane < G && !((kept >> lane) & 1ull);
             // lowest kept and highest dropped rank, as order images
@@ -247,6 +278,11 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, co
                 two = 2.0f * err + 4.0f * SU * __uint_as_float(wave_max_u32(__float_as_uint(cmax)));
             }
             sure = settled(ord_value(lo), ord_value(hi), two);
+            if (plain && !sure) {
+                scores64();
+                kept = kept64();
+                sure = have64 = true;
+            }
         }
 #pragma unroll
         for (int s = 0; s < NPL; ++s)
@@ -256,7 +292,7 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, co
     for (int s = 0; s < NPL; ++s) L.v[lane + 64 * s] = val[s];
     int my_id = 0;
     uint32_t my_key = 0;
-    const int rounds = by_logit ? p.k : p.k + 1;   // one more: the first one left out (key 0 if there is none)
+    const int rounds = plain ? p.k : p.k + 1;   // one more: the first one left out (key 0 if there is none)
     for (int j = 0; j < rounds; ++j) {
         uint32_t best = key[0];
 #pragma unroll
@@ -276,45 +312,21 @@ __device__ __forceinline__ void score_token(const ScoreRouteParams& p, int t, co
             my_key = best;
         }
     }
-    if (!by_logit) {
+    if (!plain) {
         // lane j < k: the gap to the next one (lane k holds the first left out)
         const uint32_t next = __shfl_down(my_key, 1, 64);
         const bool ok = lane >= p.k || next == 0u || settled(ord_value(my_key), ord_value(next), err);
         sure = sure && __ballot(!ok) == 0ull;
     }
 
-    double sum64 = 0.0;   // softmax: the 64-bit sum over all experts, where it is wanted
-    const bool full = !p.sigmoid && (!sure || !p.renorm);
-    double sc[NPL];
-    if (full || !sure) {
-#pragma unroll
-        for (int s = 0; s < NPL; ++s) {
-            sc[s] = score64(val[s], m, p.sigmoid);
-            sum64 += sc[s];
-        }
-        if (full) sum64 = wave_sum_f64(sum64);
-    }
+    if (!have64 && (!sure || (!p.sigmoid && !p.renorm))) scores64();
     if (!sure) {
-        // --- 64 bits
+        const uint64_t kept = kept64();
         uint64_t key64[NPL];
-        double* cd = L.c;
-        lds_wave_sync();   // the 32-bit values have been read
 #pragma unroll
         for (int s = 0; s < NPL; ++s) {
-            double x = sc[s];
-            if (!p.sigmoid) x = sum64 > 0.0 ? x / sum64 : 0.0;
-            x += static_cast<double>(bias[s]);
-            if (!(val[s] == val[s])) x = __builtin_nan("");
-            key64[s] = lane + 64 * s < E ? score_key(x) : 0ull;
-            cd[lane + 64 * s] = x == x ? x : -__builtin_inf();
-        }
-        if (grouped) {
-            lds_wave_sync();
-            const uint64_t kept =
-                best_groups(score_key(group_rank<double>(cd, G, size, -__builtin_inf(), p.top2)), G, p.topk_group);
-#pragma unroll
-            for (int s = 0; s < NPL; ++s)
-                if (!((kept >> (group_of(lane + 64 * s, inv_size) & 63)) & 1ull)) key64[s] = 0ull;
+            key64[s] = lane + 64 * s < E ? score_key(sc[s]) : 0ull;
+            if (grouped && !((kept >> (group_of(lane + 64 * s, inv_size) & 63)) & 1ull)) key64[s] = 0ull;
         }
         for (int j = 0; j < p.k; ++j) {
             uint64_t best = key64[0];
@@ -475,9 +487,10 @@ __global__ __launch_bounds__(256) void route_score_row_kernel(ScoreRouteParams p
         }
     }
     bool sure = true;
+    const bool plain = p.bias == nullptr;
     uint32_t key[VPL];
 #pragma unroll
-    for (int s = 0; s < VPL; ++s) key[s] = r + 16 * s < E ? logit_ord(c[s]) : 0u;
+    for (int s = 0; s < VPL; ++s) key[s] = r + 16 * s < E ? logit_ord(plain ? val[s] : c[s]) : 0u;
     if (grouped) {
 #pragma unroll
         for (int s = 0; s < VPL; ++s) L.c[row][r + 16 * s] = c[s] == c[s] ? c[s] : -__builtin_inff();
@@ -524,7 +537,7 @@ __global__ __launch_bounds__(256) void route_score_row_kernel(ScoreRouteParams p
     }
     int my_id = 0;
     uint32_t my_key = 0;
-    const int rounds = by_logit ? k : k + 1;
+    const int rounds = plain ? k : k + 1;
     for (int j = 0; j < rounds; ++j) {
         uint32_t best = key[0];
 #pragma unroll
@@ -543,7 +556,7 @@ __global__ __launch_bounds__(256) void route_score_row_kernel(ScoreRouteParams p
             my_key = best;
         }
     }
-    if (!by_logit) {
+    if (!plain) {
         const uint32_t next = __shfl_down(my_key, 1, 64);
         if (r < k && next != 0u) sure = sure && settled(ord_value(my_key), ord_value(next), err);
     }
@@ -574,8 +587,7 @@ __global__ __launch_bounds__(256) void route_score_row_kernel(ScoreRouteParams p
 
 hipError_t launch_route_score(const ScoreRouteParams& p, hipStream_t s) {
     const dim3 block(256);
-    const bool by_logit = p.bias == nullptr && !(p.topk_group < p.n_group && p.top2);
-    if (p.T >= (by_logit ? ROW_T_LOGITS : ROW_T_SCORES) && p.E <= ROW_E_MAX && p.n_group <= ROW_G_MAX && p.k <= ROW_K_MAX) {
+    if (p.T >= (by_logits(p) ? ROW_T_LOGITS : ROW_T_SCORES) && p.E <= ROW_E_MAX && p.n_group <= ROW_G_MAX && p.k <= ROW_K_MAX) {
         const dim3 grid((p.T + 15) / 16);
         auto kn = p.E <= 64 ? route_score_row_kernel<4>
                             : p.E <= 128 ? route_score_row_kernel<8>
@@ -588,7 +600,8 @@ hipError_t launch_route_score(const ScoreRouteParams& p, hipStream_t s) {
     auto kn = p.E <= 64 ? route_score_kernel<1>
                         : p.E <= 128 ? route_score_kernel<2>
                                      : p.E <= 192 ? route_score_kernel<3>
-                                                  : p.E <= 256 ? route_score_kernel<4> : route_score_kernel<8>;
+                                                  : p.E <= 256 ? route_score_kernel<4>
+                                                               : p.E <= 384 ? route_score_kernel<6> : route_score_kernel<8>;
     hipLaunchKernelGGL(kn, grid, block, 0, s, p);
     return hipGetLastError();
 }
@@ -601,7 +614,8 @@ hipError_t launch_router_score(const void* x, bool xf32, const float* wr, int H,
     auto kn = p.E <= 64 ? route_score_part_kernel<1>
                         : p.E <= 128 ? route_score_part_kernel<2>
                                      : p.E <= 192 ? route_score_part_kernel<3>
-                                                  : p.E <= 256 ? route_score_part_kernel<4> : route_score_part_kernel<8>;
+                                                  : p.E <= 256 ? route_score_part_kernel<4>
+                                                               : p.E <= 384 ? route_score_part_kernel<6> : route_score_part_kernel<8>;
     hipLaunchKernelGGL(kn, dim3((p.T + 3) / 4), dim3(256), 0, s, p, part, HS, logits);
     return hipGetLastError();
 }

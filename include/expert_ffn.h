@@ -439,9 +439,9 @@ typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_rank;
  *   renorm != 0 (0 where the sum is 0), times scale; computed in 64 bits and
  *   rounded once.
  * The choice is that of scores and c in 64 bits, so it does not depend on 32-bit
- * rounding; without a bias (and without MOE_GROUP_TOP2 groups to drop) the order is
- * that of the logits themselves.  A NaN logit scores 0 and ranks below every number, as does a NaN
- * c; infinite logits take the limits (softmax: the experts at +inf share the
+ * rounding.  Without a bias the scores order like the logits, and the logits are
+ * compared (sums of two scores for MOE_GROUP_TOP2 groups of more than one expert).
+ * A NaN logit scores 0 and ranks below every number, as does a NaN c; infinite logits take the limits (softmax: the experts at +inf share the
  * weight; a row of -inf alone scores 0 everywhere).
  * 1 <= k <= min(32, topk_group * E / n_group), E <= 512, n_group a divisor of E,
  * at most 64; scale finite; T <= 2^24, T*k <= 2^30.  T = 0 enqueues nothing.

@@ -37,11 +37,11 @@ def route_score(logits, k, sigmoid, bias=None, n_group=1, topk_group=1, top2=Fal
             e = np.where(nan | (m == -np.inf), 0.0, np.where(l == m, 1.0, np.exp(l - m)))
             tot = e.sum(axis=1, keepdims=True)
             s = np.where(tot > 0, e / tot, 0.0)
-        if bias is None and not (top2 and topk_group < n_group):
-            c = l.copy()                     # the order is that of the logits
-        else:
-            c = s + (0.0 if bias is None else np.asarray(bias, np.float64)[None, :])
+        # without a bias the experts' order is that of the logits
+        c = l.copy() if bias is None else s + np.asarray(bias, np.float64)[None, :]
         c[nan] = np.nan
+        sums = top2 and size > 1             # groups rank by sums of scores
+        r = np.where(nan, np.nan, s) if bias is None and sums else c
 
         def order(v, out=None):
             """Numbers by value, NaN after them, equal ones by index; what is out last."""
@@ -51,9 +51,9 @@ def route_score(logits, k, sigmoid, bias=None, n_group=1, topk_group=1, top2=Fal
 
         out = np.zeros((T, E), bool)
         if topk_group < n_group:
-            g = np.where(np.isnan(c), -np.inf, c).reshape(T, n_group, size)
+            g = np.where(np.isnan(r), -np.inf, r).reshape(T, n_group, size)
             g = -np.sort(-g, axis=2)
-            rank = g[:, :, 0] + g[:, :, 1] if top2 and size > 1 else g[:, :, 0]
+            rank = g[:, :, 0] + g[:, :, 1] if sums else g[:, :, 0]
             gone = order(rank)[:, topk_group:]
             drop = np.zeros((T, n_group), bool)
             np.put_along_axis(drop, gone, True, axis=1)

@@ -135,6 +135,31 @@ def test_route_score_ties_and_specials(L, repeat):
     assert ids[0].tolist() == [1, 3, 4, 5]
 
 
+@pytest.mark.parametrize("T", [40, 12289])
+def test_route_score_saturated(L, T):
+    """Without a bias the experts of the kept groups are ordered by their logits, also where the scores (and so the
+    sums that rank the groups) are equal in 64 bits; equal logits go to the lower id."""
+    g = gen(T)
+    for logits, sigmoid in ((torch.randint(40, 60, (T, 96), generator=g, device="cuda").float(), 1),
+                            (-1000.0 * torch.randint(1, 9, (T, 96), generator=g, device="cuda").float(), 0),
+                            (normal(g, T, 96, dtype=BF16, scale=0.05).float(), 0)):
+        for E, G, keep in ((96, 8, 3), (96, 48, 20), (64, 64, 20)):
+            l = logits[:, :E]
+            ids, w = run_route(L, l, 5, score=sigmoid, n_group=G, topk_group=keep, group_rank=1)
+            want_ids, want_w = ref.route_score(f64(l), 5, sigmoid, None, G, keep, True)
+            assert np.array_equal(ids, want_ids), (sigmoid, G)
+            close(w, want_w, U * (1 + 1e-6) * np.abs(want_w) + 1e-45, "weights")
+
+
+@pytest.mark.parametrize("T,E,k,G,keep,rank,sigmoid,bias,dt,scale,renorm", [
+    (65, 340, 8, 1, 1, 0, 0, True, BF16, 2.5, 1), (7, 384, 20, 6, 2, 1, 1, True, F32, 1.0, 1),
+    (13000, 260, 6, 26, 9, 1, 0, False, BF16, 1.0, 0), (33, 385, 5, 1, 1, 0, 0, True, F32, 1.0, 1),
+    (11573, 60, 4, 4, 1, 1, 0, False, BF16, 1.0, 1),
+])
+def test_route_score_widths(L, T, E, k, G, keep, rank, sigmoid, bias, dt, scale, renorm):
+    test_route_score(L, T, E, k, G, keep, rank, sigmoid, bias, dt, scale, renorm)
+
+
 @pytest.mark.parametrize("sigmoid", [0, 1])
 @pytest.mark.parametrize("T", [257, 12289])
 def test_route_score_close_scores(L, sigmoid, T):
