@@ -426,8 +426,10 @@ __device__ __forceinline__ float row_sum(float v) {
 // same steps on rows; one instruction serves four tokens, at the price of longer
 // rounds (a lane looks through 4 times the experts), so it is for launches that
 // fill the chip: by logits from 4096 tokens on (E = 128, k = 8: 4096 tokens 5.1 us
-// either way, 8192 7.4 -> 5.7, 65536 39.4 -> 22.0), with 32-bit scores from 12288
-// on (E = 128: 8192 9.1 against 11.3, 16384 15.3 -> 13.2, 65536 49.1 -> 31.5).
+// either way, 8192 7.4 -> 5.7, 65536 39.4 -> 22.0), with 32-bit scores from 6144
+// + 48 E on (E = 64: 8192 8.2 and 8.0, 12288 10.4 -> 8.4; E = 128: 8192 9.1 against
+// 11.3, 16384 15.3 -> 13.2, 65536 49.1 -> 31.5; E = 256: 16384 25.4 against 26.1,
+// 32768 44.1 -> 37.6).
 // A token that is not settled in 32 bits is left to score_token.
 // E <= 256, at most 16 groups, k <= 15.
 template <int VPL>
@@ -436,7 +438,7 @@ struct RowLds {
     uint32_t g[4][16];
     float f[4][16];
 };
-constexpr int ROW_T_LOGITS = 4096, ROW_T_SCORES = 12288;
+constexpr int ROW_T_LOGITS = 4096, ROW_T_SCORES = 6144, ROW_T_SCORES_E = 48;
 constexpr int ROW_E_MAX = 256, ROW_G_MAX = 16, ROW_K_MAX = 15;
 
 template <int VPL>
@@ -587,7 +589,7 @@ __global__ __launch_bounds__(256) void route_score_row_kernel(ScoreRouteParams p
 
 hipError_t launch_route_score(const ScoreRouteParams& p, hipStream_t s) {
     const dim3 block(256);
-    if (p.T >= (by_logits(p) ? ROW_T_LOGITS : ROW_T_SCORES) && p.E <= ROW_E_MAX && p.n_group <= ROW_G_MAX && p.k <= ROW_K_MAX) {
+    if (p.T >= (by_logits(p) ? ROW_T_LOGITS : ROW_T_SCORES + ROW_T_SCORES_E * p.E) && p.E <= ROW_E_MAX && p.n_group <= ROW_G_MAX && p.k <= ROW_K_MAX) {
         const dim3 grid((p.T + 15) / 16);
         auto kn = p.E <= 64 ? route_score_row_kernel<4>
                             : p.E <= 128 ? route_score_row_kernel<8>

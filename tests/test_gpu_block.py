@@ -154,7 +154,8 @@ def test_route_score_saturated(L, T):
 @pytest.mark.parametrize("T,E,k,G,keep,rank,sigmoid,bias,dt,scale,renorm", [
     (65, 340, 8, 1, 1, 0, 0, True, BF16, 2.5, 1), (7, 384, 20, 6, 2, 1, 1, True, F32, 1.0, 1),
     (13000, 260, 6, 26, 9, 1, 0, False, BF16, 1.0, 0), (33, 385, 5, 1, 1, 0, 0, True, F32, 1.0, 1),
-    (11573, 60, 4, 4, 1, 1, 0, False, BF16, 1.0, 1),
+    (11573, 60, 4, 4, 1, 1, 0, False, BF16, 1.0, 1), (18433, 256, 8, 8, 4, 1, 1, True, F32, 2.5, 1),
+    (15362, 192, 12, 3, 2, 1, 0, True, BF16, 1.0, 1), (13831, 160, 6, 8, 3, 1, 0, False, F32, 1.0, 0),
 ])
 def test_route_score_widths(L, T, E, k, G, keep, rank, sigmoid, bias, dt, scale, renorm):
     test_route_score(L, T, E, k, G, keep, rank, sigmoid, bias, dt, scale, renorm)
