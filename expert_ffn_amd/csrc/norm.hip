@@ -13,8 +13,11 @@
 // Memory bound: every input is read once and every output written once.  One
 // workgroup takes one row and keeps it in registers between the reduction and
 // the write; a thread holds C chunks of 8 elements, chunk i at
-// threadIdx + i * blockDim.  Sums and statistics are fp32, in a fixed order
-// (chunks in a thread, lanes, waves), so results are reproducible.
+// threadIdx + i * blockDim.  Before the block, rows of up to 512 elements share
+// workgroups, 16, 32 or 64 lanes a row: with a workgroup of 64 threads each their
+// dispatch decides (16384 bf16 rows of 64: 5.6 us, shared 3.0; codes 6.7 and 3.2).
+// After it that gained nothing (12.1 and 11.8).  Sums and statistics are fp32, in a
+// fixed order (chunks in a thread, lanes, waves), so results are reproducible.
 #include "block.h"
 #include "common.h"
 #include "route.h"
@@ -125,15 +128,44 @@ __device__ __forceinline__ RowStat block_stat(RowStat s, RowStat* red, bool top)
     return r;
 }
 
-template <int HT, int C, bool NORM>
-__global__ __launch_bounds__(1024) void norm_in_kernel(const void* __restrict__ h, int64_t ldh, int H, NormOut o) {
+// Sum and maximum over LPR lanes, 16, 32 or 64: the sums of block_stat where the
+// lanes past LPR hold zeros.
+template <int LPR>
+__device__ __forceinline__ RowStat lanes_stat(RowStat s, bool top) {
+    s.sum += __uint_as_float(dpp_u32<DPP_QUAD_1032>(__float_as_uint(s.sum)));
+    s.sum += __uint_as_float(dpp_u32<DPP_QUAD_2301>(__float_as_uint(s.sum)));
+    s.sum += __uint_as_float(dpp_u32<DPP_ROW_HALF_MIRROR>(__float_as_uint(s.sum)));
+    s.sum += __uint_as_float(dpp_u32<DPP_ROW_MIRROR>(__float_as_uint(s.sum)));
+    if (LPR >= 32) s.sum = sum16(s.sum);
+    if (LPR >= 64) s.sum = sum32(s.sum);
+    if (top) {
+        s.top = max(s.top, dpp_u32<DPP_QUAD_1032>(s.top));
+        s.top = max(s.top, dpp_u32<DPP_QUAD_2301>(s.top));
+        s.top = max(s.top, dpp_u32<DPP_ROW_HALF_MIRROR>(s.top));
+        s.top = max(s.top, dpp_u32<DPP_ROW_MIRROR>(s.top));
+        if (LPR >= 32) s.top = max16(s.top);
+        if (LPR >= 64) s.top = max32(s.top);
+    }
+    return s;
+}
+
+constexpr int SHARED_THREADS = 256;   // of a workgroup that several rows share
+
+// LPR = 0: a row per workgroup.  Else LPR lanes a row, C = 1.
+template <int HT, int C, bool NORM, int LPR>
+__global__ __launch_bounds__(LPR ? SHARED_THREADS : 1024) void norm_in_kernel(const void* __restrict__ h, int64_t ldh, int T, int H,
+                                                                              NormOut o) {
+    static_assert(LPR == 0 || C == 1, "a short row has one chunk per lane");
     __shared__ RowStat red[MAX_WAVES];
-    const int t = blockIdx.x, nt = blockDim.x, nchunk = H >> 3;
+    constexpr int D = LPR ? LPR : 1;
+    const int row = LPR ? static_cast<int>(blockIdx.x) * (SHARED_THREADS / D) + static_cast<int>(threadIdx.x) / D : blockIdx.x;
+    const int t = LPR ? min(row, T - 1) : row, tid = LPR ? threadIdx.x % D : threadIdx.x, nt = LPR ? LPR : blockDim.x;
+    const int nchunk = LPR && row >= T ? 0 : H >> 3;
     const int64_t hb = static_cast<int64_t>(t) * ldh;
     Raw8 hr[C], wr[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int c = threadIdx.x + i * nt;
+        const int c = tid + i * nt;
         if (c < nchunk) {
             hr[i] = load_raw8(h, HT, hb + 8 * c);
             if (NORM && o.w != nullptr) wr[i] = load_raw8(o.w, o.w_dt, 8 * c);
@@ -142,7 +174,7 @@ __global__ __launch_bounds__(1024) void norm_in_kernel(const void* __restrict__ 
     RowStat st = {0.0f, 0u};
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        if (static_cast<int>(threadIdx.x) + i * nt >= nchunk) continue;
+        if (tid + i * nt >= nchunk) continue;
         float v[8], w[8];
         widen8(hr[i], HT, v);
         if (NORM) {
@@ -155,13 +187,13 @@ __global__ __launch_bounds__(1024) void norm_in_kernel(const void* __restrict__ 
             for (int j = 0; j < 8; ++j) st.top = max(st.top, abs_bits(NORM ? v[j] * w[j] : v[j]));
         }
     }
-    st = block_stat(st, red, o.xq != nullptr);
+    st = LPR ? lanes_stat<LPR>(st, o.xq != nullptr) : block_stat(st, red, o.xq != nullptr);
     const float r = NORM ? 1.0f / sqrtf(st.sum / static_cast<float>(H) + o.eps) : 1.0f;
     const float s = code_step(st.top);
-    if (o.xq != nullptr && threadIdx.x == 0) o.xq_scale[t] = s * r;
+    if (o.xq != nullptr && tid == 0 && nchunk > 0) o.xq_scale[t] = s * r;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int c = threadIdx.x + i * nt;
+        const int c = tid + i * nt;
         if (c >= nchunk) continue;
         float v[8], w[8], x[8];
         widen8(hr[i], HT, v);
@@ -198,12 +230,20 @@ constexpr int NORM_MANY_ROWS = 1024;
 
 template <int HT, bool NORM>
 static hipError_t norm_in_by_chunks(const void* h, int64_t ldh, int T, int H, const NormOut& o, hipStream_t s) {
+    const int nchunk = H / 8;
+    if (nchunk <= 64) {
+        const int lpr = nchunk <= 16 ? 16 : nchunk <= 32 ? 32 : 64, rows = SHARED_THREADS / lpr;
+        auto kn = lpr == 16 ? norm_in_kernel<HT, 1, NORM, 16>
+                            : lpr == 32 ? norm_in_kernel<HT, 1, NORM, 32> : norm_in_kernel<HT, 1, NORM, 64>;
+        hipLaunchKernelGGL(kn, dim3((T + rows - 1) / rows), dim3(SHARED_THREADS), 0, s, h, ldh, T, H, o);
+        return hipGetLastError();
+    }
     int C;
-    const int nt = row_threads(H / 8, T >= NORM_MANY_ROWS ? 256 : 1024, &C);
+    const int nt = row_threads(nchunk, T >= NORM_MANY_ROWS ? 256 : 1024, &C);
     const dim3 grid(T), block(nt);
-    auto kn = C == 1 ? norm_in_kernel<HT, 1, NORM>
-                     : C == 2 ? norm_in_kernel<HT, 2, NORM> : norm_in_kernel<HT, 4, NORM>;
-    hipLaunchKernelGGL(kn, grid, block, 0, s, h, ldh, H, o);
+    auto kn = C == 1 ? norm_in_kernel<HT, 1, NORM, 0>
+                     : C == 2 ? norm_in_kernel<HT, 2, NORM, 0> : norm_in_kernel<HT, 4, NORM, 0>;
+    hipLaunchKernelGGL(kn, grid, block, 0, s, h, ldh, T, H, o);
     return hipGetLastError();
 }
 

@@ -388,6 +388,26 @@ def test_norm_out_without_post_norm_is_the_combine(L):
     close(f64(ho), f64(y0), 16 * U * np.abs(f64(routes)).max() * k, "combine")
 
 
+# rows that share a workgroup, with a ragged last one: 16, 32 and 64 lanes
+@pytest.mark.parametrize("T,H,ht,xt,off", [(17, 8, F32, BF16, 1.0), (4099, 128, BF16, BF16, 1.0), (31, 136, F32, F32, 0.0),
+                                           (2057, 256, BF16, F32, 0.0), (3, 264, F32, BF16, 1.0), (1029, 512, BF16, BF16, 0.0)])
+def test_norm_in_short_rows(L, T, H, ht, xt, off):
+    test_norm_in(L, T, H, ht, xt, off)
+
+
+@pytest.mark.parametrize("T,K,xt", [(15, 128, F32), (4097, 64, BF16), (9, 256, BF16), (33, 248, F32), (6, 512, BF16)])
+def test_quantize_short_rows(L, T, K, xt):
+    test_quantize_tokens(L, T, K, xt)
+
+
+@pytest.mark.parametrize("T,H,k,rt,yt,ht,gate,off,drop,nxt", [
+    (1, 512, 8, F32, BF16, BF16, "channel", 1.0, 0.0, "both"), (5, 504, 5, BF16, None, F32, "token", 0.0, 0.3, "xq"),
+    (2051, 64, 4, F32, BF16, BF16, "full", 1.0, 0.1, "both"), (7, 128, 32, BF16, F32, F32, None, 0.0, 0.5, "x"),
+])
+def test_norm_out_short_rows(L, T, H, k, rt, yt, ht, gate, off, drop, nxt):
+    test_norm_out(L, T, H, k, rt, yt, ht, gate, off, drop, nxt)
+
+
 # ------------------------------------------------------------ products ----
 def rand_codes(g, rows, K, pad=0, extreme=False):
     buf = torch.randint(-127, 128, (rows, K + pad), generator=g, device="cuda", dtype=torch.int32).to(torch.int8)
