@@ -290,7 +290,10 @@ __device__ __forceinline__ Raw8 load_src(const RowSrc& r, int c) {
     return Raw8{bload16(r.a, o), bload16(r.b, o + 16)};
 }
 
-template <int OT, int C>
+// FAR: out_routes of 2 GiB or more, a resource per route; else one, and 32-bit offsets
+// (a resource takes 25 scalar instructions, an offset 4: 16 rows of 2816 with 8 routes
+// 5.24 us, 5.04 with offsets; 16 of 7168 7.06 and 6.71).
+template <int OT, int C, bool FAR>
 __global__ __launch_bounds__(1024) void norm_out_kernel(NormOutParams p) {
     constexpr int CH = C == 4 ? 2 : 4;   // (within 128 registers)
     __shared__ RowStat red[2][MAX_WAVES];
@@ -317,6 +320,13 @@ __global__ __launch_bounds__(1024) void norm_out_kernel(NormOutParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[j] = __uint_as_float(r.a[0]);
     };
+    const uint32_t rowb = static_cast<uint32_t>(H) * (OT == F32 ? 4 : 2);
+    const rsrc_t routes = make_rsrc(p.out_routes, FAR ? 0 : static_cast<uint32_t>(p.T * p.k) * rowb);
+    auto load_route = [&](int pj, bool on, int c) {
+        if (FAR) return load_src(row_src(p.out_routes, OT, static_cast<int64_t>(pj) * H, H, on), c);
+        const uint32_t o = on && c < nchunk ? static_cast<uint32_t>(pj) * rowb + static_cast<uint32_t>(c) * (OT == F32 ? 32 : 16) : NO_LANE;
+        return Raw8{bload16(routes, o), OT == F32 ? bload16(routes, o + 16) : u32x4{0u, 0u, 0u, 0u}};
+    };
     float b[C][8];
     Raw8 hr[C], yr[C];
     RowStat st = {0.0f, 0u};
@@ -342,7 +352,7 @@ __global__ __launch_bounds__(1024) void norm_out_kernel(NormOutParams p) {
             for (int q = 0; q < CH; ++q) {
                 const bool on = j0 + q < p.k && pj[q] >= 0 && pj[q] < p.T * p.k;
                 wj[q] = on ? wj[q] : 0.0f;
-                rows[q] = load_src(row_src(p.out_routes, OT, static_cast<int64_t>(pj[q]) * H, H, on), c);
+                rows[q] = load_route(pj[q], on, c);
             }
 #pragma unroll
             for (int q = 0; q < CH; ++q) {
@@ -429,7 +439,9 @@ template <int OT>
 static hipError_t norm_out_by_chunks(const NormOutParams& p, hipStream_t s) {
     int C;
     const int nt = row_threads(p.H / 8, 1024, &C);
-    auto kn = C == 1 ? norm_out_kernel<OT, 1> : C == 2 ? norm_out_kernel<OT, 2> : norm_out_kernel<OT, 4>;
+    const bool far = static_cast<int64_t>(p.T) * p.k * p.H * (OT == F32 ? 4 : 2) >= (1ll << 31);
+    auto kn = far ? (C == 1 ? norm_out_kernel<OT, 1, true> : C == 2 ? norm_out_kernel<OT, 2, true> : norm_out_kernel<OT, 4, true>)
+                  : (C == 1 ? norm_out_kernel<OT, 1, false> : C == 2 ? norm_out_kernel<OT, 2, false> : norm_out_kernel<OT, 4, false>);
     hipLaunchKernelGGL(kn, dim3(p.T), dim3(nt), 0, s, p);
     return hipGetLastError();
 }

@@ -252,6 +252,36 @@ def test_offsets_past_32_bits(L):
     assert np.array_equal(ids.cpu().numpy(), want_ids)
 
 
+@pytest.mark.parametrize("T,k", [(5461, 3), (4096, 4), (4200, 10)])   # 2 GiB less one row, 2 GiB, 5.1 GiB of routes
+def test_norm_out_far_routes(L, T, k):
+    H, R = 32768, T * k
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    routes = torch.empty(R, H, device="cuda")
+    pos = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    tw = torch.full((T, k), float("nan"), device="cuda")
+    rows = [(0, 0, R - 1), (1, 1, R // 2), (T - 1, 0, 0), (T - 1, k - 1, R - 2), (T // 2, 2, R - 3)]
+    for t, j, r in rows:
+        routes[r] = torch.randn(H, generator=g, device="cuda")
+        pos[t, j], tw[t, j] = r, 0.5 + j
+    h = torch.randn(T, H, generator=g, device="cuda").to(BF16)
+    ho = torch.empty_like(h)
+    L.norm_out(h, ho, None, EPS, out_routes=routes, topk_w=tw, route_pos=pos)
+    want = h.clone()
+    for t in sorted({t for t, _, _ in rows}):
+        b = torch.zeros(H, device="cuda", dtype=torch.float64)
+        for t2, j, r in rows:
+            if t2 == t:
+                b += (0.5 + j) * routes[r].double()
+        want[t] = 0
+        # two products and their sum, then the residual: four roundings in 32 bits and the stored one
+        full = h[t].double() + b
+        assert ((ho[t].double() - full).abs() <= half_step(BF16) * 1.001 * full.abs() + 8 * U * (b.abs() + h[t].double().abs() + 4)).all()
+    got = ho.clone()
+    got[sorted({t for t, _, _ in rows})] = 0
+    assert torch.equal(got, want)
+
+
 def test_router_score_topk(L):
     """The router's product and the scored top-k on its logits."""
     for T, E, H, dt in ((1, 128, 2816, BF16), (17, 60, 192, F32), (130, 256, 704, BF16), (300, 257, 64, F32)):
