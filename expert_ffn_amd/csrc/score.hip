@@ -9,7 +9,7 @@
 // decide, and two programs that round differently choose different experts.  But
 // 64-bit exponentials and keys of every expert cost three times the instructions,
 // and a wave is bound by instructions here (T = 16383, E = 160, 6 MB of logits: 30 us
-// in 64 bits, 10 as below).  So:
+// in 64 bits, 9 as below).  So:
 //   - without a bias the scores order like the logits, and the logits are compared
 //     (all but sums of two scores that rank groups);
 //   - else the scores are taken in 32 bits with a bound on their error.  Where
@@ -441,7 +441,10 @@ struct RowLds {
 constexpr int ROW_T_LOGITS = 4096, ROW_T_SCORES = 6144, ROW_T_SCORES_E = 48;
 constexpr int ROW_E_MAX = 256, ROW_G_MAX = 16, ROW_K_MAX = 15;
 
-template <int VPL>
+// PACKED, for bf16 logits whose order decides: the 16 bits of an order image and the
+// complement of the expert's id make one key, so a round has no ids to look for (T =
+// 16383, E = 160: 10.5 -> 8.7 us; T = 16384, E = 256 15.7 -> 12.4).
+template <int VPL, bool PACKED>
 __global__ __launch_bounds__(256) void route_score_row_kernel(ScoreRouteParams p) {
     constexpr int NPL = (VPL + 3) / 4;
     __shared__ union Lds {
@@ -454,7 +457,7 @@ __global__ __launch_bounds__(256) void route_score_row_kernel(ScoreRouteParams p
     const bool live = t0 + row < p.T;
     const int t = live ? t0 + row : p.T - 1;
     const int E = p.E, G = p.n_group, size = E / G, k = p.k;
-    const bool grouped = p.topk_group < G, by_logit = by_logits(p);
+    const bool grouped = p.topk_group < G, by_logit = PACKED || by_logits(p);
     const float inv_size = 1.0f / static_cast<float>(size);
     RowLds<VPL>& L = lds[wave].row;
     float val[VPL], c[VPL], err = 0.0f;
@@ -489,10 +492,14 @@ __global__ __launch_bounds__(256) void route_score_row_kernel(ScoreRouteParams p
         }
     }
     bool sure = true;
-    const bool plain = p.bias == nullptr;
+    const bool plain = PACKED || p.bias == nullptr;
     uint32_t key[VPL];
 #pragma unroll
-    for (int s = 0; s < VPL; ++s) key[s] = r + 16 * s < E ? logit_ord(plain ? val[s] : c[s]) : 0u;
+    for (int s = 0; s < VPL; ++s) {
+        key[s] = logit_ord(plain ? val[s] : c[s]);
+        if (PACKED) key[s] = (key[s] & 0xFFFF0000u) | (0xFFFFu - (r + 16 * s));   // (a NaN keeps its id: above 0, below every number)
+        if (r + 16 * s >= E) key[s] = 0u;
+    }
     if (grouped) {
 #pragma unroll
         for (int s = 0; s < VPL; ++s) L.c[row][r + 16 * s] = c[s] == c[s] ? c[s] : -__builtin_inff();
@@ -545,14 +552,21 @@ __global__ __launch_bounds__(256) void route_score_row_kernel(ScoreRouteParams p
 #pragma unroll
         for (int s = 1; s < VPL; ++s) best = max(best, key[s]);
         best = row_max(best);
-        uint32_t e = 0xFFFFu;
+        uint32_t e;
+        if (PACKED) {
+            e = 0xFFFFu - (best & 0xFFFFu);
 #pragma unroll
-        for (int s = VPL - 1; s >= 0; --s) e = key[s] == best ? static_cast<uint32_t>(r + 16 * s) : e;
-        e = ~row_max(~e);   // the lowest id of the row that holds the maximum
-        const int d = static_cast<int>(e) - r;
+            for (int s = 0; s < VPL; ++s) key[s] = key[s] == best ? 0u : key[s];
+        } else {
+            e = 0xFFFFu;
 #pragma unroll
-        for (int s = 0; s < VPL; ++s)
-            if (d == 16 * s) key[s] = 0u;
+            for (int s = VPL - 1; s >= 0; --s) e = key[s] == best ? static_cast<uint32_t>(r + 16 * s) : e;
+            e = ~row_max(~e);   // the lowest id of the row that holds the maximum
+            const int d = static_cast<int>(e) - r;
+#pragma unroll
+            for (int s = 0; s < VPL; ++s)
+                if (d == 16 * s) key[s] = 0u;
+        }
         if (r == j) {
             my_id = static_cast<int>(e);
             my_key = best;
@@ -591,10 +605,12 @@ hipError_t launch_route_score(const ScoreRouteParams& p, hipStream_t s) {
     const dim3 block(256);
     if (p.T >= (by_logits(p) ? ROW_T_LOGITS : ROW_T_SCORES + ROW_T_SCORES_E * p.E) && p.E <= ROW_E_MAX && p.n_group <= ROW_G_MAX && p.k <= ROW_K_MAX) {
         const dim3 grid((p.T + 15) / 16);
-        auto kn = p.E <= 64 ? route_score_row_kernel<4>
-                            : p.E <= 128 ? route_score_row_kernel<8>
-                                         : p.E <= 160 ? route_score_row_kernel<10>
-                                                      : p.E <= 192 ? route_score_row_kernel<12> : route_score_row_kernel<16>;
+        const bool packed = by_logits(p) && p.logits_dt == BF16;
+        auto kn = p.E <= 64 ? (packed ? route_score_row_kernel<4, true> : route_score_row_kernel<4, false>)
+                  : p.E <= 128 ? (packed ? route_score_row_kernel<8, true> : route_score_row_kernel<8, false>)
+                  : p.E <= 160 ? (packed ? route_score_row_kernel<10, true> : route_score_row_kernel<10, false>)
+                  : p.E <= 192 ? (packed ? route_score_row_kernel<12, true> : route_score_row_kernel<12, false>)
+                               : (packed ? route_score_row_kernel<16, true> : route_score_row_kernel<16, false>);
         hipLaunchKernelGGL(kn, grid, block, 0, s, p);
         return hipGetLastError();
     }

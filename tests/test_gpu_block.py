@@ -135,6 +135,29 @@ def test_route_score_ties_and_specials(L, repeat):
     assert ids[0].tolist() == [1, 3, 4, 5]
 
 
+@pytest.mark.parametrize("repeat", [1, 690])
+def test_route_score_ties_and_specials_bf16(L, repeat):
+    """16-bit logits without a bias: ties, signed zeros, masks, infinities and NaN."""
+    inf, nan = float("inf"), float("nan")
+    for E, G, keep in ((70, 1, 1), (70, 7, 2), (129, 1, 1), (256, 16, 1)):
+        rows = torch.zeros(6, E)
+        rows[1, ::2] = -0.0
+        rows[2] = nan
+        rows[2, E - 1] = -inf
+        rows[3, 1::3] = inf
+        rows[3, ::5] = nan
+        rows[4] = torch.finfo(BF16).min
+        rows[4, 5] = -inf
+        rows[4, E - 2:] = torch.finfo(BF16).max
+        rows[5] = (torch.arange(E) * 7 % 5).float() - 2
+        l = rows.to(BF16).repeat(repeat, 1).cuda()
+        for sigmoid in (0, 1):
+            ids, w = run_route(L, l, 6, score=sigmoid, n_group=G, topk_group=keep)
+            want_ids, want_w = ref.route_score(f64(l), 6, sigmoid, None, G, keep)
+            assert np.array_equal(ids, want_ids), (E, G, sigmoid)
+            close(w, want_w, U * (1 + 1e-6) * np.abs(want_w) + 1e-45, "weights")
+
+
 @pytest.mark.parametrize("T", [40, 12289])
 def test_route_score_saturated(L, T):
     """Without a bias the experts of the kept groups are ordered by their logits, also where the scores (and so the
@@ -155,7 +178,8 @@ def test_route_score_saturated(L, T):
     (65, 340, 8, 1, 1, 0, 0, True, BF16, 2.5, 1), (7, 384, 20, 6, 2, 1, 1, True, F32, 1.0, 1),
     (13000, 260, 6, 26, 9, 1, 0, False, BF16, 1.0, 0), (33, 385, 5, 1, 1, 0, 0, True, F32, 1.0, 1),
     (11573, 60, 4, 4, 1, 1, 0, False, BF16, 1.0, 1), (18433, 256, 8, 8, 4, 1, 1, True, F32, 2.5, 1),
-    (15362, 192, 12, 3, 2, 1, 0, True, BF16, 1.0, 1), (13831, 160, 6, 8, 3, 1, 0, False, F32, 1.0, 0),
+    (15362, 192, 12, 3, 2, 1, 0, True, BF16, 1.0, 1), (4101, 250, 15, 10, 2, 0, 1, False, BF16, 1.0, 0),
+    (4096, 64, 6, 1, 1, 0, 0, False, BF16, 1.0, 1), (4097, 186, 9, 6, 4, 0, 0, False, BF16, 2.5, 1), (13831, 160, 6, 8, 3, 1, 0, False, F32, 1.0, 0),
 ])
 def test_route_score_widths(L, T, E, k, G, keep, rank, sigmoid, bias, dt, scale, renorm):
     test_route_score(L, T, E, k, G, keep, rank, sigmoid, bias, dt, scale, renorm)
