@@ -57,10 +57,15 @@ __device__ __forceinline__ void lds_copy16(rsrc_t r, uint8_t* dst, uint32_t off,
 // channels, so a lane holds both products of its channels.
 __host__ __device__ constexpr int waitcnt_vm_lds(int n) { return waitcnt_vm(n) & ~0x0F00; }   // and LDS reads to 0
 
+// the rows of out are 16-byte aligned
+__host__ __device__ __forceinline__ bool rows_in_pieces(const MatI8Params& p) {
+    return reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo * (p.out_dt == F32 ? 4 : 2) % 16 == 0;
+}
+
 // 16-byte chunk q of row r is stored at position q ^ swz(r)
 __device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 3); }
 
-template <int BN, int BT, int WN, int WT, int NSTG, int KG, bool GATED, int OT>
+template <int BN, int BT, int WN, int WT, int NSTG, int KG, bool GATED, int OT, bool PIECES>
 __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(MatI8Params p, int nt_n, int nt_t) {
     constexpr int NW = WN * WT, NB = BN / WN / 32, TB = BT / WT / 32;
     constexpr int BK = 128, RPC = 1024 / BK, CPR = BK / 16;   // K bytes of a step, rows of a copy, chunks of a row
@@ -259,7 +264,7 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
     static_assert(PART + 32 * RS * NW <= KG * RING, "epilogue regions");
     uint8_t* my = lds + PART + wave * 32 * RS;
     auto at = [&](int tok, int c) { return my + tok * RS + ((p2 ? c ^ (tok & (cpr - 1)) : c) << 4); };
-    const bool vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo * es % 16 == 0;
+    const bool vec = KG == 1 || rows_in_pieces(p);
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb) {
         const int tl = wt * (BT / WT) + 32 * tb;   // first token of the block in the tile
@@ -288,32 +293,44 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_i8_tile_kernel(Ma
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
+        if (PIECES) {
 #pragma unroll 4
-        for (int i0 = 0; i0 < 32 * cpr; i0 += 64) {
-            const int it = i0 + lane;
-            const int tok = it / cpr, c = it % cpr;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(at(tok, c));
-            const int t = tl + tok, ch = wn * CW + c * (16 / es);
-            if (t >= ntok || ch >= nch) continue;
-            const int64_t o = static_cast<int64_t>(t0 + t) * p.ldo + n0 + ch;
-            if (f32) {
-                float* d = static_cast<float*>(p.out) + o;
-                if (vec && ch + 4 <= nch) {
+            for (int i0 = 0; i0 < 32 * cpr; i0 += 64) {
+                const int it = i0 + lane;
+                const int tok = it / cpr, c = it % cpr;
+                const u32x4 v = *reinterpret_cast<const u32x4*>(at(tok, c));
+                const int t = tl + tok, ch = wn * CW + c * (16 / es);
+                if (t >= ntok || ch >= nch) continue;
+                uint8_t* d = static_cast<uint8_t*>(p.out) + (static_cast<int64_t>(t0 + t) * p.ldo + n0 + ch) * es;
+                if (vec && ch + 16 / es <= nch) {
                     *reinterpret_cast<u32x4*>(d) = v;
-                } else {
+                } else if (f32) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (ch + j < nch) d[j] = __uint_as_float(v[j]);
-                }
-            } else {
-                uint16_t* d = static_cast<uint16_t*>(p.out) + o;
-                if (vec && ch + 8 <= nch) {
-                    *reinterpret_cast<u32x4*>(d) = v;
+                        if (ch + j < nch) reinterpret_cast<uint32_t*>(d)[j] = v[j];
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (ch + j < nch) d[j] = static_cast<uint16_t>(v[j >> 1] >> (16 * (j & 1)));
+                        if (ch + j < nch) reinterpret_cast<uint16_t*>(d)[j] = static_cast<uint16_t>(v[j >> 1] >> (16 * (j & 1)));
                 }
+            }
+        } else {
+            // Rows that are not 16-byte aligned (!PIECES): neighbouring lanes store neighbouring
+            // elements (T = 4096, N = 5633, K = 704: 40 us, the chunks' elements lane by
+            // lane 63).  The small tiles with K groups have one or two waves here, and
+            // the fewer reads of the chunks serve them (N = 703: 4.0 us against 4.4).
+#pragma unroll 4
+            for (int i0 = 0; i0 < 32 * CW; i0 += 64) {
+                const int it = i0 + lane;
+                const int tok = it / CW, e = it % CW;
+                const uint8_t* s = at(tok, e * es / 16) + e * es % 16;
+                const int t = tl + tok, ch = wn * CW + e;
+                if (t >= ntok || ch >= nch) continue;
+                const int64_t o = static_cast<int64_t>(t0 + t) * p.ldo + n0 + ch;
+                if (f32)
+                    static_cast<uint32_t*>(p.out)[o] = *reinterpret_cast<const uint32_t*>(s);
+                else
+                    static_cast<uint16_t*>(p.out)[o] = *reinterpret_cast<const uint16_t*>(s);
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -457,8 +474,13 @@ static hipError_t tile(const MatI8Params& p, hipStream_t s) {
     constexpr int CH = GATED ? BN / 2 : BN;
     const int nt_n = (p.N + CH - 1) / CH, nt_t = (p.T + BT - 1) / BT;
     const int per = (nt_n * nt_t + 7) / 8;
-    auto kn = p.out_dt == F32 ? matmul_i8_tile_kernel<BN, BT, WN, WT, NSTG, KG, GATED, F32>
-                              : matmul_i8_tile_kernel<BN, BT, WN, WT, NSTG, KG, GATED, BF16>;
+    // (PIECES of the tiles with K groups is a choice inside)
+    constexpr bool ELEMENTS = KG > 1;
+    auto kn = KG > 1 || rows_in_pieces(p)
+                  ? (p.out_dt == F32 ? matmul_i8_tile_kernel<BN, BT, WN, WT, NSTG, KG, GATED, F32, true>
+                                     : matmul_i8_tile_kernel<BN, BT, WN, WT, NSTG, KG, GATED, BF16, true>)
+                  : (p.out_dt == F32 ? matmul_i8_tile_kernel<BN, BT, WN, WT, NSTG, KG, GATED, F32, ELEMENTS>
+                                     : matmul_i8_tile_kernel<BN, BT, WN, WT, NSTG, KG, GATED, BF16, ELEMENTS>);
     hipLaunchKernelGGL(kn, dim3(8 * per), dim3(64 * WN * WT * KG), 0, s, p, nt_n, nt_t);
     return hipGetLastError();
 }
@@ -505,14 +527,19 @@ static int pick_tile(int64_t T, int64_t rows, int K) {
 
 // Up to 16 tokens the kernel for few (210 shapes, T 1 to 16, N 704 to 8192, K 704 to
 // 8192: 1.37 times as fast as the best tile on average, T = 16, N = 2112, K = 2816 2.85
-// and 4.9 us, 8 of them slower, N = 8192, K = 4096 10.5 and 8.8).  Up to 32 as long as
-// every workgroup has a CU of its own: 1.36 times as fast (N = 2112, K = 2816 3.9 and
-// 5.0 us); with more, 5 % slower on average.
+// and 4.9 us, 8 of them slower, N = 8192, K = 4096 10.5 and 8.8).  Further as long as
+// every workgroup has a CU of its own: up to 32 tokens 1.36 times as fast (N = 2112, K =
+// 2816 3.9 and 5.0 us; with more workgroups 5 % slower), to 48 1.14 to 1.24 times, to 64
+// 1.04 to 1.13 times for up to 22 steps (K = 4096 none), to 80 as fast, to 96 slower.
 template <bool GATED>
 static hipError_t dispatch(const MatI8Params& p, hipStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.N) * (GATED ? 2 : 1);
     if (p.T <= 16) return few<1, GATED>(p, s);
-    if (p.T <= 32 && rows <= 256 * 16) return few<2, GATED>(p, s);
+    if (rows <= 256 * 16) {
+        if (p.T <= 32) return few<2, GATED>(p, s);
+        if (p.T <= 48) return few<3, GATED>(p, s);
+        if (p.T <= 64 && p.K <= 22 * 128) return few<4, GATED>(p, s);
+    }
     switch (pick_tile(p.T, rows, p.K)) {
         case 0: return tile<32, 32, 1, 1, 3, 4, GATED>(p, s);
         case 1: return tile<32, 64, 1, 2, 3, 4, GATED>(p, s);

@@ -505,6 +505,10 @@ def test_gated_matmul_i8(L, T, F, K, ot, act):
     (200, 4101, 272, F32, True), (200, 8200, 272, BF16, True), (1030, 4101, 272, F32, True), (1030, 4101, 272, BF16, False),
     (3000, 2053, 400, F32, False), (1030, 8200, 272, BF16, True), (200, 4101, 2816, BF16, False), (1030, 8200, 400, F32, True),
     (2100, 4101, 400, BF16, True),
+    # rows that can be stored in 16-byte pieces
+    (77, 128, 400, F32, False), (200, 4104, 2816, BF16, True), (1030, 4104, 272, BF16, False), (3000, 2056, 400, F32, True),
+    (33, 2056, 400, BF16, True), (48, 4096, 272, F32, False), (64, 2000, 2816, BF16, False), (64, 2000, 2832, BF16, True),
+    (49, 77, 144, F32, True),
 ])
 def test_matmul_i8_tiles(L, T, N, K, ot, bias):
     test_matmul_i8(L, T, N, K, ot, bias)
@@ -514,7 +518,8 @@ def test_matmul_i8_tiles(L, T, N, K, ot, bias):
     (77, 130, 1424, BF16, 0), (200, 601, 1424, F32, 1), (200, 1100, 2816, BF16, 1), (77, 130, 272, F32, 0),
     (77, 4101, 272, BF16, 0), (200, 4101, 272, F32, 0), (1030, 2053, 272, BF16, 0), (1030, 2053, 272, F32, 1),
     (3000, 1100, 400, BF16, 1), (1030, 4101, 272, F32, 0), (77, 4101, 2816, F32, 1), (1030, 4101, 400, BF16, 0),
-    (2100, 2053, 400, F32, 1),
+    (2100, 2053, 400, F32, 1), (1030, 2056, 272, BF16, 1), (77, 4104, 2816, BF16, 0), (3000, 1104, 400, F32, 0),
+    (40, 1000, 704, BF16, 0), (64, 2048, 1424, F32, 1), (33, 5, 16, BF16, 1),
 ])
 def test_gated_matmul_i8_tiles(L, T, F, K, ot, act):
     test_gated_matmul_i8(L, T, F, K, ot, act)
