@@ -373,7 +373,7 @@ def test_norm_out(L, T, H, k, rt, yt, ht, gate, off, drop, nxt):
                                None if y is None else f64(y), f64(wp), off, EPS, None if gt is None else f64(gt),
                                np.float64(np.float32(0.7)), np.float64(np.float32(1.3)))
     close(f64(ho), want, bound + half_step(ht) * (np.abs(want) + bound), "h_out")
-    # the next norm is that of the rows as stored: bit for bit the norm of them alone
+    # the next norm is that of the rows as stored: the codes are those of the norm of them alone
     if nxt:
         x2 = torch.empty(T, H, dtype=BF16, device="cuda")
         q2 = torch.empty(T, H, dtype=torch.int8, device="cuda")
