@@ -4,6 +4,7 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import shutil
 import subprocess
 from concurrent.futures import ThreadPoolExecutor
 
@@ -60,20 +61,33 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     del deps
     build_peaks()
-    build_binding()
     return LIB
 
 
-def build_binding() -> str:
+def rocm_include() -> str:
+    """The headers that belong to HIPCC."""
+    hipcc = shutil.which(HIPCC)
+    if hipcc is None:
+        raise RuntimeError(f"{HIPCC} was not found")
+    return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(hipcc))), "include")
+
+
+def build_binding():
     """The compiled Python binding of the operators around the expert FFN (host code, against torch's headers
-    and this library)."""
+    and this library).  Its functions take torch tensors: where torch is not installed it is left out, and
+    None returned."""
     import sysconfig
     spec = importlib.util.find_spec("torch")
+    if spec is None:
+        print("torch is not installed: the library is built without its Python binding _binding.so", flush=True)
+        return None
+    if shutil.which("g++") is None:
+        raise RuntimeError(f"g++ was not found: it compiles {BINDING_SRC}")
     torch_dir = os.path.dirname(spec.origin)
     inc, libs = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     tmp = BINDING + ".tmp%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-           f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", "-I/opt/rocm/include",
+           f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-I{rocm_include()}",
            f"-I{sysconfig.get_paths()['include']}", BINDING_SRC, "-o", tmp,
            LIB, "-Wl,-rpath,$ORIGIN", f"-L{libs}", f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10",
            "-lc10_hip"]
@@ -95,3 +109,4 @@ def build_peaks() -> str:
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_binding())
