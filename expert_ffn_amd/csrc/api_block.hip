@@ -28,10 +28,14 @@ Span span(const void* p, int64_t rows, int64_t ld, int64_t cols, int es) {
 bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
 int esize(int32_t dt) { return dt == MOE_F32 ? 4 : 2; }
 
+// Rows of ld elements that no address space holds (2^48 bytes and more): refused, so
+// that the byte counts of a span stay inside 64 bits.
+bool beyond(int64_t rows, int64_t ld) { return rows > 1 && ld > (1ll << 46) / rows; }
+
 // a row-major matrix read or written in 16-byte pieces
-moe_status check_rows(const char* fn, const char* name, const void* p, int64_t ld, int32_t cols, int es) {
+moe_status check_rows(const char* fn, const char* name, const void* p, int32_t rows, int64_t ld, int32_t cols, int es) {
     if (ld < cols) return fail(MOE_E_SHAPE, fn, "row stride %lld of %s is below %d", static_cast<long long>(ld), name, cols);
-    if (ld >= (1ll << 40)) return fail(MOE_E_SHAPE, fn, "row stride of %s too large", name);
+    if (ld >= (1ll << 40) || beyond(rows, ld)) return fail(MOE_E_SHAPE, fn, "row stride of %s too large", name);
     if (!aligned(p, 16) || ld * es % 16)
         return fail(MOE_E_ARG, fn, "rows of %s must be 16-byte aligned", name);
     return MOE_OK;
@@ -53,7 +57,7 @@ moe_status check_norm_out(const char* fn, int32_t T, int32_t H, const moe::NormO
     if ((o.xq == nullptr) != (o.xq_scale == nullptr)) return fail(MOE_E_ARG, fn, "xq and xq_scale go together");
     if (o.x) {
         if (!dt_ok(o.x_dt)) return fail(MOE_E_ARG, fn, "unknown dtype %d of x", o.x_dt);
-        if ((st = check_rows(fn, "x", o.x, o.ldx, H, esize(o.x_dt))) != MOE_OK) return st;
+        if ((st = check_rows(fn, "x", o.x, T, o.ldx, H, esize(o.x_dt))) != MOE_OK) return st;
     }
     if (o.xq) {
         if (o.ldq < H || o.ldq > LD_MAX)
@@ -126,7 +130,7 @@ moe_status moe_route_score_topk(const void* logits, int32_t logits_dtype, int64_
     if (st != MOE_OK) return st;
     if (T > 0 && (!logits || !topk_ids || !topk_w)) return fail(MOE_E_ARG, fn, "null pointer argument");
     if (!dt_ok(logits_dtype)) return fail(MOE_E_ARG, fn, "unknown dtype %d", logits_dtype);
-    if (ld_logits < E || ld_logits >= (1ll << 40))
+    if (ld_logits < E || ld_logits >= (1ll << 40) || beyond(T, ld_logits))
         return fail(MOE_E_SHAPE, fn, "row stride %lld of logits is below E=%d or too large", static_cast<long long>(ld_logits), E);
     if (!aligned(logits, esize(logits_dtype)) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
         return fail(MOE_E_ARG, fn, "a pointer is not aligned to its elements");
@@ -179,7 +183,7 @@ moe_status moe_norm_in(const void* h, int32_t h_dtype, int64_t ldh, int32_t T, i
     if (st != MOE_OK || T == 0) return st;
     if (!h) return fail(MOE_E_ARG, fn, "h is NULL");
     if (!dt_ok(h_dtype)) return fail(MOE_E_ARG, fn, "unknown dtype %d of h", h_dtype);
-    if ((st = check_rows(fn, "h", h, ldh, H, esize(h_dtype))) != MOE_OK) return st;
+    if ((st = check_rows(fn, "h", h, T, ldh, H, esize(h_dtype))) != MOE_OK) return st;
     const moe::NormOut o = {w, w_dtype, w_offset, eps, x, x_dtype, ldx, xq, ldq, xq_scale};
     Span out[3];
     if ((st = check_norm_out(fn, T, H, o, out)) != MOE_OK) return st;
@@ -195,7 +199,7 @@ moe_status moe_quantize_tokens(const void* x, int32_t x_dtype, int64_t ldx, int3
     if (st != MOE_OK || T == 0) return st;
     if (!x || !xq || !xq_scale) return fail(MOE_E_ARG, fn, "null pointer argument");
     if (!dt_ok(x_dtype)) return fail(MOE_E_ARG, fn, "unknown dtype %d", x_dtype);
-    if ((st = check_rows(fn, "x", x, ldx, K, esize(x_dtype))) != MOE_OK) return st;
+    if ((st = check_rows(fn, "x", x, T, ldx, K, esize(x_dtype))) != MOE_OK) return st;
     const moe::NormOut o = {nullptr, MOE_F32, 0.0f, 1.0f, nullptr, MOE_F32, 0, xq, ldq, xq_scale};
     Span out[3];
     if ((st = check_norm_out(fn, T, K, o, out)) != MOE_OK) return st;
@@ -227,17 +231,18 @@ moe_status moe_norm_out(const void* out_routes, int32_t out_dtype, const float* 
     if (w_offset != w_offset || block_scale != block_scale || res_scale != res_scale)
         return fail(MOE_E_ARG, fn, "w_offset or a scale is NaN");
     const int he = esize(h_dtype);
-    if ((st = check_rows(fn, "h", h, ldh, H, he)) != MOE_OK) return st;
-    if ((st = check_rows(fn, "h_out", h_out, ldho, H, he)) != MOE_OK) return st;
+    if ((st = check_rows(fn, "h", h, T, ldh, H, he)) != MOE_OK) return st;
+    if ((st = check_rows(fn, "h_out", h_out, T, ldho, H, he)) != MOE_OK) return st;
     if (k > 0 && (!aligned(out_routes, 16) || !aligned(topk_w, 4) || !aligned(route_pos, 4)))
         return fail(MOE_E_ARG, fn, "out_routes must be 16-byte aligned, topk_w and route_pos 4-byte aligned");
-    if (y && (st = check_rows(fn, "y", y, ldy, H, esize(y_dtype))) != MOE_OK) return st;
+    if (y && (st = check_rows(fn, "y", y, T, ldy, H, esize(y_dtype))) != MOE_OK) return st;
     if (w_post && !aligned(w_post, 16)) return fail(MOE_E_ARG, fn, "w_post is not 16-byte aligned");
     Span gs = {0, 0};
     if (gate) {
         if (gate_stride_h != 0 && gate_stride_h != 1)
             return fail(MOE_E_UNSUPPORTED, fn, "gate stride %lld along H is neither 0 nor 1", static_cast<long long>(gate_stride_h));
-        if (gate_stride_t < 0 || gate_stride_t >= (1ll << 40)) return fail(MOE_E_SHAPE, fn, "gate stride along T is negative or too large");
+        if (gate_stride_t < 0 || gate_stride_t >= (1ll << 40) || beyond(T, gate_stride_t))
+            return fail(MOE_E_SHAPE, fn, "gate stride along T is negative or too large");
         const int ge = esize(gate_dtype);
         if (!aligned(gate, gate_stride_h ? 16 : ge) || (gate_stride_h && gate_stride_t * ge % 16))
             return fail(MOE_E_ARG, fn, "rows of gate must be 16-byte aligned");
@@ -303,7 +308,8 @@ static moe_status matmul_entry(const char* fn, bool gated, const int8_t* xq, int
     if (ldx < K || ldw < K || ldx > LD_MAX || ldw > LD_MAX)
         return fail(MOE_E_SHAPE, fn, "row strides %lld of xq and %lld of wq must lie in [K=%d, 2^22]",
                     static_cast<long long>(ldx), static_cast<long long>(ldw), K);
-    if (ldo < N || ldo >= (1ll << 40)) return fail(MOE_E_SHAPE, fn, "row stride %lld of out is below N=%d or too large", static_cast<long long>(ldo), N);
+    if (ldo < N || ldo >= (1ll << 40) || beyond(T, ldo))
+        return fail(MOE_E_SHAPE, fn, "row stride %lld of out is below N=%d or too large", static_cast<long long>(ldo), N);
     if (!aligned(xq, 16) || !aligned(wq, 16) || ldx % 16 || ldw % 16)
         return fail(MOE_E_ARG, fn, "rows of xq and wq must be 16-byte aligned");
     if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4) || !aligned(out, esize(out_dtype)))

@@ -416,10 +416,10 @@ int32_t moe_slot_admit(int32_t* slot_of, int32_t E, int32_t* owner, int32_t S, i
 /*
  * ---- Around the expert FFN: routing by scores, the norms before and after the
  * block, and the 8-bit products of a dense (shared) expert beside the routed
- * ones.  Rows of the matrices below are `ld` elements apart (ld >= columns),
- * their elements contiguous.  No output may overlap another output or an input
- * unless said otherwise (MOE_E_ARG).  Nothing is written beside the rows and
- * columns named.
+ * ones.  Rows of the matrices below are `ld` elements apart (ld >= columns,
+ * below 2^40, and rows * ld at most 2^46), their elements contiguous.  No output
+ * may overlap another output or an input unless said otherwise (MOE_E_ARG).
+ * Nothing is written beside the rows and columns named.
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_rank;
