@@ -341,6 +341,7 @@ Signature S_norm_out = {"norm_out", 17, 4,
 BOUND(norm_out) {
     return guarded([&] {
         TAKE(S_norm_out);
+        if (!given(a[4]) && (given(a[5]) || given(a[6]))) raise(PyExc_ValueError, "topk_w and route_pos need out_routes");
         int dev;
         const Mat h = first(a[0], "h", ANY, &dev);
         const int32_t T = h.rows, H = h.cols;
