@@ -149,11 +149,16 @@ __device__ __forceinline__ float ord_value(uint32_t o) {   // the number of an o
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 // Errors of the 32-bit scores, U = 2^-24.  An exponential e^-x has its argument off
-// by x U (the product with log2 e; a softmax's v - m by x U more) and errs by 2 U
-// itself.  Sigmoid s = 1 / (1 + e): s (1 - s) (x + 2) U <= 0.75 U, the sum and the
-// division U each: below 3 U.  Softmax e / sum: with the mean of x under the
-// weights at most ln 512, the sum errs by (2 * 6.3 + 2 + 14 additions) U of itself,
-// the division and product by 3 U more, and s x <= 0.4: below (1 + 34 s) U.  A sum
+// by 1.23 x U (the product with log2 e and that constant's own 0.23 U; a softmax's
+// x = m - v by x U more) and errs by 2 U itself.  Sigmoid s = 1 / (1 + e): s (1 - s)
+// (1.23 x + 2) U <= 0.8 U, the sum and the division U each: below 3 U.  Softmax s = e /
+// sum: the score's own exponential errs by s (2.23 x + 2) U, and s x = s ln(q / s) <=
+// 0.37 q with q the largest score.  The sum errs by the mean of that under the weights
+// and U per addition, 13 of them with a token to a wave (8 experts a lane, 6 lane
+// steps), 19 with four tokens to a wave (16 and 4, E <= 256).  The mean of x is largest
+// where all the others are equal: (1 - q) ln(q (E - 1) / (1 - q)), at most 3.34 for E =
+// 256 and 3.89 for 512, over all q.  The division and the product add U each.  Together s
+// times 0.8 + 2.23 * 3.34 + 6 + 19 = 33.3 U (E = 512: 28.5 U): below (1 + 34 q) U.  A sum
 // with a bias rounds by U of the result.
 constexpr float SU = 5.9604645e-8f;
 __device__ __forceinline__ float score_err(int sigmoid, float smax) { return sigmoid ? 3.0f * SU : (1.0f + 34.0f * smax) * SU; }
