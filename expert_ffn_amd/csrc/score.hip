@@ -441,7 +441,6 @@ template <int VPL>
 struct RowLds {
     float c[4][16 * VPL];
     uint32_t g[4][16];
-    float f[4][16];
 };
 constexpr int ROW_T_LOGITS = 4096, ROW_T_SCORES = 6144, ROW_T_SCORES_E = 48;
 constexpr int ROW_E_MAX = 256, ROW_G_MAX = 16, ROW_K_MAX = 15;

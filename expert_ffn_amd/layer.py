@@ -132,9 +132,8 @@ class MoeBlock:
         bf16, f32 = torch.bfloat16, torch.float32
         self.x = torch.empty((T, H), dtype=bf16, device=d)
         self.logits = torch.empty((T, layer.E), dtype=f32, device=d)
-        # the sizes of the workspace do not grow with T alone: few tokens take wider slices of H
-        nbytes = max(router_ws_bytes(t, H, layer.E) for t in {min(T, 64), T})
-        self.router_ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=d)
+        # enough for fewer tokens too: their slices of H are as many or fewer
+        self.router_ws = torch.empty(max(router_ws_bytes(T, H, layer.E), 256), dtype=torch.uint8, device=d)
         self.x_next = torch.empty((T, H), dtype=bf16, device=d) if w_next is not None else None
         if dense is not None:
             self.xq = torch.empty((T, H), dtype=torch.int8, device=d)
