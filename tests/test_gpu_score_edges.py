@@ -58,3 +58,38 @@ def test_near_ties_from_the_scores(L, E, G, keep, top2, sigmoid):  # noqa: F811
     assert same.mean() > 0.99
     rows = same.all(axis=1)
     close(w[rows], want_w[rows], U * (1 + 1e-6) * np.abs(want_w[rows]) + 1e-45, "weights")
+
+
+@pytest.mark.parametrize("past", [-1, 0, 1])
+@pytest.mark.parametrize("E,k,G,keep,rank,sigmoid,bias,dt", [
+    (64, 6, 1, 1, 0, 0, True, F32), (128, 15, 16, 5, 1, 1, True, F32), (192, 12, 3, 2, 1, 0, True, BF16),
+    (256, 8, 8, 4, 1, 1, True, F32), (240, 8, 8, 3, 1, 0, False, F32),      # sums of two without a bias: scores
+    (256, 8, 1, 1, 0, 0, False, BF16), (100, 5, 10, 4, 0, 1, False, F32),   # logits alone
+])
+def test_switch_to_four_tokens_by_length(L, E, k, G, keep, rank, sigmoid, bias, dt, past):  # noqa: F811
+    """Token counts at and on both sides of the switch."""
+    T = four_tokens_from(E, not bias and not rank) + past
+    check(L, T, E, k, G, keep, rank, sigmoid, bias, dt)
+
+
+@pytest.mark.parametrize("E,k,G,keep,rank,sigmoid,bias,dt", [
+    (256, 8, 16, 4, 0, 1, True, F32), (256, 8, 32, 4, 0, 1, True, F32),     # groups: the most it takes, and more
+    (238, 8, 17, 5, 1, 0, True, BF16), (256, 8, 64, 20, 1, 0, False, F32),
+    (128, 15, 1, 1, 0, 0, True, F32), (128, 16, 1, 1, 0, 0, True, F32),     # k likewise
+    (256, 9, 1, 1, 0, 1, True, F32), (257, 9, 1, 1, 0, 1, True, F32),       # experts likewise
+])
+def test_switch_to_four_tokens_by_shape(L, E, k, G, keep, rank, sigmoid, bias, dt):  # noqa: F811
+    """Enough tokens for it; the groups, k or experts are the largest it takes, or one more."""
+    check(L, four_tokens_from(E, False) + 5, E, k, G, keep, rank, sigmoid, bias, dt)
+
+
+def check(L, T, E, k, G, keep, rank, sigmoid, bias, dt):  # noqa: F811
+    g = gen(T * 3 + E)
+    logits = normal(g, T, E, dtype=dt, scale=1.5)
+    b = normal(g, E, scale=0.2) if bias else None
+    print(f"[case] route T={T} E={E} k={k} G={G}", flush=True)
+    ids, w = run_route(L, logits, k, bias=b, score=sigmoid, n_group=G, topk_group=keep, group_rank=rank, scale=2.5)
+    want_ids, want_w = ref.route_score(f64(logits), k, sigmoid, None if b is None else f64(b), G, keep, rank == 1, scale=2.5)
+    assert np.array_equal(ids, want_ids)
+    # 64-bit arithmetic, one rounding to fp32
+    close(w, want_w, U * (1 + 1e-6) * np.abs(want_w) + 1e-45, "weights")
