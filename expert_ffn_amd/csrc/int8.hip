@@ -529,8 +529,11 @@ static int pick_tile(int64_t T, int64_t rows, int K) {
 // 8192: 1.37 times as fast as the best tile on average, T = 16, N = 2112, K = 2816 2.85
 // and 4.9 us, 8 of them slower, N = 8192, K = 4096 10.5 and 8.8).  Further as long as
 // every workgroup has a CU of its own: up to 32 tokens 1.36 times as fast (N = 2112, K =
-// 2816 3.9 and 5.0 us; with more workgroups 5 % slower), to 48 1.14 to 1.24 times, to 64
-// 1.04 to 1.13 times for up to 22 steps (K = 4096 none), to 80 as fast, to 96 slower.
+// 2816 3.9 and 5.0 us; with more workgroups 5 % slower), to 48 1.14 to 1.24 times, to 80 as
+// fast, to 96 slower.  To 64 tokens the length of a row counts (30 shapes at each of 22
+// lengths): 1.11 times as fast at 12 steps, 1.05 at 22; past that, rows of whole 128-byte
+// lines keep 1.03 to 1.06 up to 36 steps, others fall to 1.00 to 1.01 at 23, 0.99 at 25, 0.98
+// at 28 and 0.95 at 32: the limit is where those cross.
 template <bool GATED>
 static hipError_t dispatch(const MatI8Params& p, hipStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.N) * (GATED ? 2 : 1);
@@ -538,7 +541,7 @@ static hipError_t dispatch(const MatI8Params& p, hipStream_t s) {
     if (rows <= 256 * 16) {
         if (p.T <= 32) return few<2, GATED>(p, s);
         if (p.T <= 48) return few<3, GATED>(p, s);
-        if (p.T <= 64 && p.K <= 22 * 128) return few<4, GATED>(p, s);
+        if (p.T <= 64 && p.K <= 23 * 128) return few<4, GATED>(p, s);
     }
     switch (pick_tile(p.T, rows, p.K)) {
         case 0: return tile<32, 32, 1, 1, 3, 4, GATED>(p, s);

@@ -33,6 +33,16 @@ def test_matmul_ring(L, T, N, K, bf16, pieces):  # noqa: F811
     close(f64(out), want, bound + half_step(out.dtype) * (abs(want) + bound), "out")
 
 
+@pytest.mark.parametrize("T", [49, 64])
+@pytest.mark.parametrize("past", [0, 16])
+def test_switch_of_64_tokens_by_length(L, T, past):  # noqa: F811
+    """49 to 64 tokens at the longest rows of the kernel for few tokens, and one piece past them."""
+    K = tc.FEW_STEPS_64 * tc.STEP + past
+    assert (tc.kernel_of(T, 1003, K, False)[0] == ("few", 4)) == (past == 0)
+    test_matmul_ring(L, T, 1003, K, True, False)
+    test_gated_matmul_ring(L, T, 1003, K, False, True)
+
+
 @pytest.mark.parametrize("T,F,K,bf16,pieces", tc.GATED)
 def test_gated_matmul_ring(L, T, F, K, bf16, pieces):  # noqa: F811
     print(f"[case] gated_matmul_i8 T={T} F={F} K={K} {tc.kernel_of(T, F, K, True)}", flush=True)

@@ -39,10 +39,9 @@ def few_tokens(T, rows, K):
         return 1
     if rows > 256 * 16:
         return 0
-    limit = re.search(r"p\.T <= 64 && p\.K <= (\d+) \* 128", _SRC)
     if T <= 48:
         return (T + 15) // 16
-    return 4 if T <= 64 and K <= int(limit.group(1)) * STEP else 0
+    return 4 if T <= 64 and K <= FEW_STEPS_64 * STEP else 0
 
 
 def kernel_of(T, N, K, gated):
@@ -55,6 +54,8 @@ def kernel_of(T, N, K, gated):
     i = pick_tile(T, rows, K)
     return ("tile", i), -(-steps // KERNELS[i][5]), KERNELS[i][4]
 
+
+FEW_STEPS_64 = int(re.search(r"p\.T <= 64 && p\.K <= (\d+) \* 128", _SRC).group(1))   # of 49 to 64 tokens
 
 # T, N, K, bf16 output, rows of the output that can be stored in 16-byte pieces; ragged in tokens,
 # channels and K
