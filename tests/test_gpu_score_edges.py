@@ -83,6 +83,15 @@ def test_switch_to_four_tokens_by_shape(L, E, k, G, keep, rank, sigmoid, bias, d
     check(L, four_tokens_from(E, False) + 5, E, k, G, keep, rank, sigmoid, bias, dt)
 
 
+@pytest.mark.parametrize("by_logits,dt", [(True, BF16), (True, F32), (False, F32)])
+@pytest.mark.parametrize("E,G,keep", [(64, 8, 3), (65, 5, 2), (96, 1, 1), (96, 16, 6), (97, 1, 1), (128, 8, 3), (129, 3, 1),
+                                      (160, 10, 4), (161, 7, 3), (192, 1, 1), (193, 1, 1), (210, 14, 5), (224, 1, 1),
+                                      (224, 16, 7), (225, 15, 4), (256, 1, 1)])
+def test_widths_of_four_tokens(L, E, G, keep, by_logits, dt):  # noqa: F811
+    """The first and last expert count of each width, by logits and by scores."""
+    check(L, four_tokens_from(E, by_logits) + 2, E, 6, G, keep, 0, 0, not by_logits, dt)
+
+
 def check(L, T, E, k, G, keep, rank, sigmoid, bias, dt):  # noqa: F811
     g = gen(T * 3 + E)
     logits = normal(g, T, E, dtype=dt, scale=1.5)

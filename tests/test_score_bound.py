@@ -22,7 +22,7 @@ def coefficients():
 
 # experts of a launch, lanes that share a token, experts of a lane at most
 KERNELS = [(64, 64, 1), (128, 64, 2), (256, 64, 4), (384, 64, 6), (512, 64, 8),
-           (64, 16, 4), (128, 16, 8), (160, 16, 10), (192, 16, 12), (256, 16, 16)]
+           (64, 16, 4), (96, 16, 6), (128, 16, 8), (160, 16, 10), (192, 16, 12), (224, 16, 14), (256, 16, 16)]
 
 
 @pytest.mark.parametrize("E,lanes,per", KERNELS)
