@@ -156,7 +156,7 @@ moe_status moe_router_score_topk(const void* x, int32_t x_dtype, int32_t T, int3
         return fail(MOE_E_ARG, fn, "null pointer argument");
     if (!dt_ok(x_dtype)) return fail(MOE_E_ARG, fn, "unknown dtype %d", x_dtype);
     if (H < 64 || H % 64) return fail(MOE_E_SHAPE, fn, "H=%d is not a positive multiple of 64", H);
-    if (static_cast<int64_t>(T) * H >= (1ll << 31) || moe::router_part_floats(T, H, E) >= (1ll << 31))
+    if (T > moe::ROUTER_T_MAX || static_cast<int64_t>(T) * H >= (1ll << 31) || moe::router_part_floats(T, H, E) >= (1ll << 31))
         return fail(MOE_E_SHAPE, fn, "T=%d too large", T);
     if (T == 0) return MOE_OK;
     if (ws_bytes < moe_router_ws_bytes(T, H, E))

@@ -19,6 +19,7 @@ struct ScoreRouteParams {
     float* w;               // [T, k]
 };
 hipError_t launch_route_score(const ScoreRouteParams& p, hipStream_t s);
+constexpr int ROUTER_T_MAX = 65535 * 64;   // tokens of a router product: a grid row (z) per 64
 // the router's product in slices of H: part fp32 [*HS][T][E] (router_part_floats in all), summed in slice order by the reader
 hipError_t launch_router_part(const void* x, bool xf32, const float* wr, int T, int H, int E, float* part, int* HS,
                               hipStream_t s);

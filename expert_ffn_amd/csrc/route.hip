@@ -154,6 +154,7 @@ __global__ __launch_bounds__(256) void router_part_kernel(const void* __restrict
 // 16-byte LDS read each) and feeds them to 4 MFMAs: MFMA j's k = 0, 1 are
 // elements j and 4 + j.  No cross-wave sum.
 constexpr int RL_TB = 64, RL_EB = 64, RL_HL = 128;
+static_assert(ROUTER_T_MAX == 65535 * RL_TB, "grid rows of the router's product");
 
 template <bool XF32>
 __global__ __launch_bounds__(256) void router_part_large_kernel(const void* __restrict__ x,

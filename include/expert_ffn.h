@@ -454,7 +454,7 @@ moe_status moe_route_score_topk(const void* logits, int32_t logits_dtype, int64_
 /*
  * The router's product (logits = x . w_router^T in fp32, as moe_router_topk: same
  * operands, workspace and sums), then moe_route_score_topk on those logits, with
- * the logits written: two launches.  H a multiple of 64.
+ * the logits written: two launches.  H a multiple of 64; T <= 65535 * 64, T*H < 2^31.
  */
 moe_status moe_router_score_topk(const void* x, int32_t x_dtype, int32_t T, int32_t H, const float* w_router, int32_t E,
                                  int32_t k, const float* bias, int32_t score, int32_t n_group, int32_t topk_group,

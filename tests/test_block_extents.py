@@ -2,7 +2,7 @@
 checked (the check's byte counts stay inside 64 bits): the C ABI without a GPU."""
 import pytest
 
-from test_block_abi import GATED, MM, NORM_IN, NORM_OUT, QUANT, ROUTE, A, call, refused
+from test_block_abi import GATED, MM, NORM_IN, NORM_OUT, QUANT, ROUTE, ROUTER, A, call, refused
 from test_block_abi import L  # noqa: F401  (the fixture)
 
 FAR = (1 << 40) - 16                       # elements from row to row
@@ -33,3 +33,10 @@ def test_overlap_behind_a_wrapped_extent(L):  # noqa: F811
     """2^21 rows 2^40 elements apart are 2^63 bytes: an output inside them was not seen to overlap."""
     rc, msg = call(L, "moe_norm_in", NORM_IN, T=ROWS, ldh=FAR, hdt=0, x=A[0], xq=None, xs=None)
     assert rc == 2 and "too large" in msg, (rc, msg)
+
+
+def test_router_tokens_beyond_a_launch(L):  # noqa: F811
+    """The router's product has a grid row per 64 tokens, at most 65535: more tokens are refused, not left to the launch."""
+    few = dict(H=64, E=1, k=1, wsb=1 << 34)
+    refused(L, "moe_router_score_topk", ROUTER, 2, "too large", T=65535 * 64 + 1, **few)
+    assert "too large" not in call(L, "moe_router_score_topk", ROUTER, T=65535 * 64, **dict(few, wsb=16))[1]
