@@ -7,11 +7,13 @@
 //
 // The choice is that of 64-bit scores: 32-bit rounding loses differences that
 // decide, and two programs that round differently choose different experts.  But
-// 64-bit exponentials and keys of every expert cost three times the instructions,
-// and a wave is bound by instructions here (T = 16383, E = 160, 6 MB of logits: 30 us
-// in 64 bits, 9 as below).  So:
+// 64-bit exponentials and keys of every expert cost three times the instructions, and
+// the time follows (T = 16383, E = 160, 6 MB of logits: 30 us in 64 bits, 8.5 as below,
+// where the VALU issues in 34 % of the cycles and a wave waits 18 % of its time: the
+// rest is the latency of dependent lane steps, with four waves to a SIMD).  So:
 //   - without a bias the scores order like the logits, and the logits are compared
-//     (all but sums of two scores that rank groups);
+//     (all but sums of two scores that rank groups; logits that differ decide also
+//     where their scores are equal in 64 bits);
 //   - else the scores are taken in 32 bits with a bound on their error.  Where
 //     every gap that decides (between groups, between consecutive choices and the
 //     first one left out) exceeds twice the bound, the 64-bit choice is the same;

@@ -116,7 +116,12 @@ class MoeBlock:
 
     run() returns h_out [T, H] and, with w_next, the next block's normed rows.  h is fp32 or bf16; h_out
     may be h.  w_post, gate, bias, dense and w_next may be None.  The buffers hold up to the layer's T_max
-    tokens and are reused by the next run: calls on one block are ordered by the caller."""
+    tokens and are reused by the next run: calls on one block are ordered by the caller.
+
+    One norm (w_in) feeds the router, the routed and the dense experts, and one (w_post) covers the sum of
+    what they give; the dense expert takes 8-bit activations.  A block that norms these apart, or wants
+    16-bit activations there, calls norm_in, router_score_topk, the layer's steps and norm_out itself (y takes
+    the rows of any dense expert)."""
 
     def __init__(self, layer, w_in, w_router, w_post=None, eps=1e-6, w_offset=0.0, dense=None, gate=None,
                  block_scale=1.0, res_scale=1.0, w_next=None, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1,

@@ -439,10 +439,14 @@ typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_rank;
  *   renorm != 0 (0 where the sum is 0), times scale; computed in 64 bits and
  *   rounded once.
  * The choice is that of scores and c in 64 bits, so it does not depend on 32-bit
- * rounding.  Without a bias the scores order like the logits, and the logits are
- * compared (sums of two scores for MOE_GROUP_TOP2 groups of more than one expert).
- * A NaN logit scores 0 and ranks below every number, as does a NaN c; infinite logits take the limits (softmax: the experts at +inf share the
- * weight; a row of -inf alone scores 0 everywhere).
+ * rounding.  With bias NULL the logits are compared in place of c (sums of two
+ * scores still rank MOE_GROUP_TOP2 groups of more than one expert): they order
+ * like the scores, and where different logits have scores that are equal in 64
+ * bits (a sigmoid above about 37, a softmax 745 below its largest), the larger
+ * logit comes first, while a bias of zeros puts the lower id first.
+ * A NaN logit scores 0 and ranks below every number, as does a NaN c; infinite
+ * logits take the limits (softmax: the experts at +inf share the weight; a row of
+ * -inf alone scores 0 everywhere).
  * 1 <= k <= min(32, topk_group * E / n_group), E <= 512, n_group a divisor of E,
  * at most 64; scale finite; T <= 2^24, T*k <= 2^30.  T = 0 enqueues nothing.
  */
