@@ -622,7 +622,7 @@ hipError_t launch_route_score(const ScoreRouteParams& p, hipStream_t s) {
     if (p.T >= (by_logits(p) ? ROW_T_LOGITS : ROW_T_SCORES + ROW_T_SCORES_E * p.E) && p.E <= ROW_E_MAX && p.n_group <= ROW_G_MAX && p.k <= ROW_K_MAX) {
         const dim3 grid((p.T + 15) / 16);
         const bool packed = by_logits(p) && p.logits_dt == BF16;
-        // a width for every 32 experts: an idle pair of experts a lane costs 5 to 10 %
+        // a width for every 32 experts: two idle experts a lane cost 5 to 13 %
         // (T = 65536: E = 96 in 8 a lane 15.3, in 6 13.5 us; 160 in 12 21.0, in 10 19.3;
         // 224 in 16 28.0, in 14 25.0; T = 16384: 5.5 and 5.0, 6.9 and 6.4, 9.3 and 8.8)
         auto kn = packed ? row_kernel<true>(p.E) : row_kernel<false>(p.E);
