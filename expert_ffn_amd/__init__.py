@@ -77,8 +77,16 @@ def lib():
         L.moe_quantize_tokens.argtypes = [P, i32, i64, i32, i32, P, i64, P, P]
         L.moe_matmul_i8.argtypes = [P, i64, P, P, i64, P, P, i32, i32, i32, P, i32, i64, P]
         L.moe_gated_matmul_i8.argtypes = [P, i64, P, P, i64, P, i32, i32, i32, i32, P, i32, i64, P]
+        adapters = [P, i64, P, P, i64, P, i32, i32, P]
+        L.moe_matmul_bf16.argtypes = [P, i64, P, i64, i32, i32, i32, P, i32, i64] + adapters
+        L.moe_gated_matmul_bf16.argtypes = [P, i64, P, i64, i32, i32, i32, i32, P, i32, i64, P, i64] + adapters
+        L.moe_adapter_shrink.argtypes = [P, i64, i32, i32, P, P, i64, i32, i32, i32, P, P, P, i64, P]
+        L.moe_matmul_bf16_backward.argtypes = [P, i64, P, i64, P, i64, i32, i32, i32, P, i32, i64, P, i32, i64, P]
+        L.moe_gated_matmul_bf16_backward.argtypes = [P, i64, P, i64, i32, P, i64, P, i64, i32, i32, i32, P, i64, P, i32, i64, P, i32,
+                                                     i64, P]
         for name in ("moe_route_score_topk", "moe_router_score_topk", "moe_norm_in", "moe_norm_out", "moe_quantize_tokens", "moe_matmul_i8",
-                     "moe_gated_matmul_i8"):
+                     "moe_gated_matmul_i8", "moe_matmul_bf16", "moe_gated_matmul_bf16", "moe_adapter_shrink",
+                     "moe_matmul_bf16_backward", "moe_gated_matmul_bf16_backward"):
             getattr(L, name).restype = ctypes.c_int
         for name in ("moe_blob_layout", "moe_route_topk", "moe_permute", "moe_route_permute", "moe_expert_ffn",
                      "moe_ffn_gate_up", "moe_ffn_down", "moe_expert_ffn_noalloc", "moe_combine", "moe_quantize",
@@ -286,7 +294,8 @@ def budget_from_memory(free_bytes: int, reserve_bytes: int, expert_bytes: int, l
 # stride (elements of a row contiguous), and run on the tensors' GPU: on its
 # current stream when none is given.
 _BOUND = ("route_score_topk", "router_score_topk", "norm_in", "norm_out", "quantize_tokens", "matmul_i8",
-          "gated_matmul_i8")
+          "gated_matmul_i8", "matmul_bf16", "gated_matmul_bf16", "adapter_shrink", "matmul_bf16_backward",
+          "gated_matmul_bf16_backward")
 
 
 def __getattr__(name):

@@ -2,35 +2,25 @@
 // and after the block, and the 8-bit integer products.  Argument checks on the
 // host, then one launch on the caller's stream.
 #include "block.h"
+#include "checks.h"
 #include "kernels.h"
 #include "status.h"
 
 using moe::aligned;
+using moe::beyond;
+using moe::check_apart;
 using moe::dt_ok;
+using moe::esize;
 using moe::fail;
 using moe::hip_status;
+using moe::span;
+using moe::Span;
 
 namespace {
 
 constexpr int32_t ROWS_MAX = 1 << 21;   // rows of a call (one workgroup of at most 1024 threads each)
 constexpr int32_t K_MAX = 131056;       // 128 * 128 * K stays below 2^31
 constexpr int64_t LD_MAX = 1ll << 22;   // row stride of 8-bit operands: 31-bit offsets inside a tile
-
-// bytes [lo, hi) that a matrix of `rows` rows touches
-struct Span {
-    uintptr_t lo, hi;
-};
-Span span(const void* p, int64_t rows, int64_t ld, int64_t cols, int es) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-    if (!p || rows < 1) return {0, 0};
-    return {b, b + static_cast<uintptr_t>(((rows - 1) * ld + cols) * es)};
-}
-bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
-int esize(int32_t dt) { return dt == MOE_F32 ? 4 : 2; }
-
-// Rows of ld elements that no address space holds (2^48 bytes and more): refused, so
-// that the byte counts of a span stay inside 64 bits.
-bool beyond(int64_t rows, int64_t ld) { return rows > 1 && ld > (1ll << 46) / rows; }
 
 // a row-major matrix read or written in 16-byte pieces
 moe_status check_rows(const char* fn, const char* name, const void* p, int32_t rows, int64_t ld, int32_t cols, int es) {
@@ -70,17 +60,6 @@ moe_status check_norm_out(const char* fn, int32_t T, int32_t H, const moe::NormO
     s[2] = span(o.xq_scale, T, 1, 1, 4);
     return MOE_OK;
 }
-// no two outputs meet, and no output meets an input
-moe_status check_apart(const char* fn, const Span* in, int n_in, const Span* out, int n_out) {
-    for (int i = 0; i < n_out; ++i) {
-        for (int j = 0; j < i; ++j)
-            if (meet(out[i], out[j])) return fail(MOE_E_ARG, fn, "two outputs overlap");
-        for (int j = 0; j < n_in; ++j)
-            if (meet(out[i], in[j])) return fail(MOE_E_ARG, fn, "an output overlaps an input");
-    }
-    return MOE_OK;
-}
-
 }  // namespace
 
 extern "C" {

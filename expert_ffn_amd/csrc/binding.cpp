@@ -437,6 +437,152 @@ BOUND(gated_matmul_i8) {
     });
 }
 
+// a pool of adapters: [n, ...] of the given sizes, each adapter contiguous
+const at::Tensor& pool(PyObject* o, const char* name, int dev, int64_t* stride) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.dim() < 3) raise(PyExc_ValueError, "%s has shape %s, expected a pool of matrices", name, sizes(t).c_str());
+    check_device(t, name, dev);
+    check_kind(t, name, BF16);
+    int64_t each = 1;
+    for (int64_t i = t.dim() - 1; i > 0; each *= t.size(i--))
+        if (t.size(i) > 1 && t.stride(i) != each) raise(PyExc_ValueError, "an adapter of %s is not contiguous", name);
+    *stride = t.size(0) > 1 ? t.stride(0) : each;
+    return t;
+}
+struct Adapters {   // of a product: s, adapter_ids, b and ranks (or none of them)
+    Mat s;
+    int32_t *ids = nullptr, *ranks = nullptr, n = 0, R = 0;
+    const void* b = nullptr;
+    int64_t stride = 0;
+};
+Adapters adapters(PyObject* s, PyObject* ids, PyObject* b, PyObject* ranks, const Mat& x, int32_t rows, int32_t halves, int dev) {
+    Adapters A;
+    if (!given(s)) {
+        if (given(ids) || given(b) || given(ranks)) raise(PyExc_ValueError, "adapter_ids, b and ranks go with s");
+        return A;
+    }
+    const at::Tensor& t = pool(b, "b", dev, &A.stride);
+    if (t.dim() != 3 || t.size(1) != rows)
+        raise(PyExc_ValueError, "b has shape %s, expected (n, %d, R)", sizes(t).c_str(), rows);
+    A.n = size32(t.size(0), "b");
+    A.R = size32(t.size(2), "b");
+    A.b = t.data_ptr();
+    A.s = mat(s, "s", x.rows, static_cast<int64_t>(halves) * A.R, dev, BF16);
+    A.ids = static_cast<int32_t*>(vec(ids, "adapter_ids", x.rows, dev, I32));
+    A.ranks = vec_or_null<int32_t>(ranks, "ranks", A.n, dev, I32);
+    return A;
+}
+// a weight matrix [rows, K] whose row count the call takes from it
+Mat weights(PyObject* o, const char* name, int64_t K, int dev) {
+    const at::Tensor& t = tensor(o, name);
+    return mat(o, name, t.dim() == 2 ? size32(t.size(0), name) : 0, K, dev, BF16);
+}
+int32_t half_of(const Mat& w, const char* name) {
+    if (w.rows % 2) raise(PyExc_ValueError, "%s has %d rows: gate and up rows come in pairs", name, w.rows);
+    return w.rows / 2;
+}
+
+Signature S_mmb = {"matmul_bf16", 8, 3, {"x", "w", "out", "s", "adapter_ids", "b", "ranks", "stream"}, {}};
+BOUND(matmul_bf16) {
+    return guarded([&] {
+        TAKE(S_mmb);
+        int dev;
+        const Mat x = first(a[0], "x", BF16, &dev);
+        const Mat w = weights(a[1], "w", x.cols, dev);
+        const Mat o = mat(a[2], "out", x.rows, w.rows, dev, ANY);
+        const Adapters A = adapters(a[3], a[4], a[5], a[6], x, w.rows, 1, dev);
+        void* s = stream_of(a[7], dev);
+        on_device(dev, [&] {
+            return moe_matmul_bf16(x.p, x.ld, w.p, w.ld, x.rows, w.rows, x.cols, o.p, o.dt, o.ld, A.s.p, A.s.ld, A.ids, A.b, A.stride,
+                                   A.ranks, A.n, A.R, s);
+        });
+    });
+}
+
+Signature S_gmmb = {"gated_matmul_bf16", 10, 4, {"x", "w", "act", "out", "pre", "s", "adapter_ids", "b", "ranks", "stream"}, {}};
+BOUND(gated_matmul_bf16) {
+    return guarded([&] {
+        TAKE(S_gmmb);
+        int dev;
+        const Mat x = first(a[0], "x", BF16, &dev);
+        const Mat w = weights(a[1], "w", x.cols, dev);
+        const int32_t F = half_of(w, "w"), act = to_int(a[2], "act", -1);
+        const Mat o = mat(a[3], "out", x.rows, F, dev, ANY);
+        const Mat pre = given(a[4]) ? mat(a[4], "pre", x.rows, w.rows, dev, BF16) : Mat{};
+        const Adapters A = adapters(a[5], a[6], a[7], a[8], x, w.rows, 2, dev);
+        void* s = stream_of(a[9], dev);
+        on_device(dev, [&] {
+            return moe_gated_matmul_bf16(x.p, x.ld, w.p, w.ld, x.rows, F, x.cols, act, o.p, o.dt, o.ld, pre.p, pre.ld, A.s.p, A.s.ld,
+                                         A.ids, A.b, A.stride, A.ranks, A.n, A.R, s);
+        });
+    });
+}
+
+Signature S_shrink = {"adapter_shrink", 7, 5, {"x", "adapter_ids", "a", "scale", "s", "ranks", "stream"}, {}};
+BOUND(adapter_shrink) {
+    return guarded([&] {
+        TAKE(S_shrink);
+        int dev;
+        const Mat x = first(a[0], "x", BF16, &dev);
+        int64_t stride;
+        const at::Tensor& t = pool(a[2], "a", dev, &stride);
+        const int64_t nd = t.dim();
+        if (nd > 4 || t.size(nd - 1) != x.cols || (nd == 4 && t.size(1) != 1 && t.size(1) != 2))
+            raise(PyExc_ValueError, "a has shape %s, expected (n, R, %d) or (n, 2, R, %d)", sizes(t).c_str(), x.cols, x.cols);
+        const int32_t n = size32(t.size(0), "a"), R = size32(t.size(nd - 2), "a"), halves = nd == 4 ? static_cast<int32_t>(t.size(1)) : 1;
+        const Mat o = mat(a[4], "s", x.rows, static_cast<int64_t>(halves) * R, dev, BF16);
+        const int32_t* ids = static_cast<int32_t*>(vec(a[1], "adapter_ids", x.rows, dev, I32));
+        const float* scale = vec_or_null<float>(a[3], "scale", n, dev, F32);
+        const int32_t* ranks = vec_or_null<int32_t>(a[5], "ranks", n, dev, I32);
+        const void* pa = t.data_ptr();
+        void* s = stream_of(a[6], dev);
+        on_device(dev, [&] {
+            return moe_adapter_shrink(x.p, x.ld, x.rows, x.cols, ids, pa, stride, n, R, halves, scale, ranks, o.p, o.ld, s);
+        });
+    });
+}
+
+Signature S_mmbg = {"matmul_bf16_backward", 6, 3, {"x", "w", "dout", "dx", "dw", "stream"}, {}};
+BOUND(matmul_bf16_backward) {
+    return guarded([&] {
+        TAKE(S_mmbg);
+        int dev;
+        const Mat x = first(a[0], "x", BF16, &dev);
+        const Mat w = weights(a[1], "w", x.cols, dev);
+        const Mat d = mat(a[2], "dout", x.rows, w.rows, dev, BF16);
+        const Mat dx = given(a[3]) ? mat(a[3], "dx", x.rows, x.cols, dev, ANY) : Mat{};
+        const Mat dw = given(a[4]) ? mat(a[4], "dw", w.rows, x.cols, dev, ANY) : Mat{};
+        if (!given(a[3]) && !given(a[4])) raise(PyExc_ValueError, "neither dx nor dw is given");
+        if (x.rows == 0 && !given(a[4])) return;   // dx has no rows
+        void* s = stream_of(a[5], dev);
+        on_device(dev, [&] {
+            return moe_matmul_bf16_backward(x.p, x.ld, w.p, w.ld, d.p, d.ld, x.rows, w.rows, x.cols, dx.p, dx.dt, dx.ld, dw.p, dw.dt,
+                                            dw.ld, s);
+        });
+    });
+}
+
+Signature S_gmmbg = {"gated_matmul_bf16_backward", 9, 6, {"x", "w", "act", "pre", "dout", "dpre", "dx", "dw", "stream"}, {}};
+BOUND(gated_matmul_bf16_backward) {
+    return guarded([&] {
+        TAKE(S_gmmbg);
+        int dev;
+        const Mat x = first(a[0], "x", BF16, &dev);
+        const Mat w = weights(a[1], "w", x.cols, dev);
+        const int32_t F = half_of(w, "w"), act = to_int(a[2], "act", -1);
+        const Mat pre = mat(a[3], "pre", x.rows, w.rows, dev, BF16);
+        const Mat d = mat(a[4], "dout", x.rows, F, dev, BF16);
+        const Mat dp = mat(a[5], "dpre", x.rows, w.rows, dev, BF16);
+        const Mat dx = given(a[6]) ? mat(a[6], "dx", x.rows, x.cols, dev, ANY) : Mat{};
+        const Mat dw = given(a[7]) ? mat(a[7], "dw", w.rows, x.cols, dev, ANY) : Mat{};
+        void* s = stream_of(a[8], dev);
+        on_device(dev, [&] {
+            return moe_gated_matmul_bf16_backward(x.p, x.ld, w.p, w.ld, act, pre.p, pre.ld, d.p, d.ld, x.rows, F, x.cols, dp.p, dp.ld,
+                                                  dx.p, dx.dt, dx.ld, dw.p, dw.dt, dw.ld, s);
+        });
+    });
+}
+
 #define METHOD(name, doc) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL | METH_KEYWORDS, doc}
 PyMethodDef methods[] = {
@@ -473,6 +619,28 @@ PyMethodDef methods[] = {
            "gated_matmul_i8(xq, x_scale, wq, w_scale, act, out, stream=None)\n--\n\n"
            "out [T, F] = act(gate) * up of the int8 product of xq [T, K] with wq [2F, K] (gate rows, then up rows, as an\n"
            "expert's w13)."),
+    METHOD(matmul_bf16,
+           "matmul_bf16(x, w, out, s=None, adapter_ids=None, b=None, ranks=None, stream=None)\n--\n\n"
+           "out [T, N] = x [T, K] . w [N, K] in bf16, fp32 sums, out fp32 or bf16.  With s [T, R] (adapter_shrink), token t\n"
+           "adds s[t] . b[adapter_ids[t]] of its request's low-rank adapter: b [n, N, R], ranks int32 [n] (None: R), ids\n"
+           "int32 [T], outside [0, n): none."),
+    METHOD(gated_matmul_bf16,
+           "gated_matmul_bf16(x, w, act, out, pre=None, s=None, adapter_ids=None, b=None, ranks=None, stream=None)\n--\n\n"
+           "out [T, F] = act(gate) * up of the bf16 product of x [T, K] with w [2F, K] (gate rows, then up rows, as an\n"
+           "expert's w13); pre [T, 2F] takes the sums for the backward pass.  Adapters as for matmul_bf16, before the\n"
+           "activation: s [T, 2R] and b [n, 2F, R], gate's then up's."),
+    METHOD(adapter_shrink,
+           "adapter_shrink(x, adapter_ids, a, scale, s, ranks=None, stream=None)\n--\n\n"
+           "s[t] = scale[i] * (x[t] . a[i]), i = adapter_ids[t]: the first product of the tokens' low-rank adapters, zeros\n"
+           "without one and past a rank.  a [n, R, K] with s [T, R], or [n, 2, R, K] (gate and up) with s [T, 2R]; scale\n"
+           "fp32 [n] or None."),
+    METHOD(matmul_bf16_backward,
+           "matmul_bf16_backward(x, w, dout, dx=None, dw=None, stream=None)\n--\n\n"
+           "dx [T, K] = dout [T, N] . w, dw [N, K] = dout^T . x, each fp32 or bf16 or None."),
+    METHOD(gated_matmul_bf16_backward,
+           "gated_matmul_bf16_backward(x, w, act, pre, dout, dpre, dx=None, dw=None, stream=None)\n--\n\n"
+           "From pre [T, 2F] of the forward pass and dout [T, F]: dpre [T, 2F] (may be pre), dx [T, K] = dpre . w, dw\n"
+           "[2F, K] = dpre^T . x."),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Operators around the expert FFN (see expert_ffn_amd).", -1, methods,
@@ -481,7 +649,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Operators around the e
 }  // namespace
 
 PyMODINIT_FUNC PyInit__binding() {
-    for (Signature* s : {&S_route, &S_router, &S_norm_in, &S_quant, &S_norm_out, &S_mm, &S_gmm})
+    for (Signature* s : {&S_route, &S_router, &S_norm_in, &S_quant, &S_norm_out, &S_mm, &S_gmm, &S_mmb, &S_gmmb, &S_shrink, &S_mmbg, &S_gmmbg})
         for (int i = 0; i < s->n; ++i)
             if (!(s->interned[i] = PyUnicode_InternFromString(s->names[i]))) return nullptr;
     return PyModule_Create(&module);

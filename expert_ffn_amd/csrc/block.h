@@ -90,4 +90,63 @@ struct MatI8Params {
 };
 hipError_t launch_matmul_i8(const MatI8Params& p, bool gated, hipStream_t s);
 
+// ---------------------------------------------------- bfloat16 products --
+// out[t][n] = sum over k of (token operand)(t, k) (channel operand)(n, k).  An operand
+// is a matrix whose rows run along k, or one whose rows are the k (KIND):
+//   NT     x [T, K], w [N, K]: the product of a layer
+//   GATED  x [T, K], w [2N, K]: out = act(gate) up; pre [T, 2N] takes the sums
+//   NN     x [T, K], w [K, N]: the gradient of the rows
+//   TN     x [K, T], w [K, N]: the gradient of the weights
+enum MatKind { MAT_NT = 0, MAT_GATED = 1, MAT_NN = 2, MAT_TN = 3 };
+// Low-rank adapters of the tokens (NT, GATED): token t adds s[t] b[ids[t]]^T
+struct AdapterParams {
+    const uint16_t* s;      // [T, halves R], rows lds apart; null: no adapters
+    int64_t lds;
+    const int* ids;         // [T], outside [0, n): none
+    const uint16_t* b;      // [n] of [halves N, R], b_stride apart
+    int64_t b_stride;
+    const int* ranks;       // [n] or null: R
+    int n, R;
+};
+struct MatBf16Params {
+    const uint16_t* x;
+    int64_t ldx;
+    const uint16_t* w;
+    int64_t ldw;
+    int T, N, K, act;
+    void* out;              // [T, N], rows ldo apart
+    int out_dt;
+    int64_t ldo;
+    uint16_t* pre;          // GATED: [T, 2N], rows ldp apart, or null
+    int64_t ldp;
+    AdapterParams ad;
+};
+hipError_t launch_matmul_bf16(const MatBf16Params& p, MatKind kind, hipStream_t s);
+
+// dpre = the gradient of pre: dout u act'(g), then dout act(g)
+struct GatedGradParams {
+    const uint16_t* pre;    // [T, 2F], rows ldp apart
+    int64_t ldp;
+    const uint16_t* dout;   // [T, F], rows ldd apart
+    int64_t ldd;
+    uint16_t* dpre;         // [T, 2F], rows ldg apart
+    int64_t ldg;
+    int T, F, act;
+};
+hipError_t launch_gated_grad(const GatedGradParams& p, hipStream_t s);
+
+struct AdapterShrinkParams {
+    const uint16_t* x;      // [T, K], rows ldx apart
+    int64_t ldx;
+    const int* ids;         // [T]
+    const uint16_t* a;      // [n] of [halves, R, K], a_stride apart
+    int64_t a_stride;
+    const float* scale;     // [n] or null: 1
+    const int* ranks;       // [n] or null: R
+    int T, K, n, R, halves;
+    uint16_t* s;            // [T, halves R], rows lds apart
+    int64_t lds;
+};
+hipError_t launch_adapter_shrink(const AdapterShrinkParams& p, hipStream_t s);
+
 }  // namespace moe

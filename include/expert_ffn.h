@@ -545,6 +545,79 @@ moe_status moe_gated_matmul_i8(const int8_t* xq, int64_t ldx, const float* x_sca
                                const float* w_scale, int32_t T, int32_t F, int32_t K, int32_t act, void* out,
                                int32_t out_dtype, int64_t ldo, void* stream);
 
+/*
+ * bfloat16 products, the dense (shared) expert's in a block of bf16 weights:
+ *   moe_matmul_bf16        out[t][n] = sum_k x[t][k] * w[n][k]
+ *   moe_gated_matmul_bf16  w [2F, K] holds F gate rows, then F up rows (an expert's
+ *                          w13), and with the sums g and u
+ *                          out[t][f] = act(g[t][f]) * u[t][f]
+ *   x device bf16 [T, K], w device bf16 [N, K] (gated: [2F, K])
+ *   out device [T, N] (gated: [T, F]), fp32 or bf16
+ *   pre device bf16 [T, 2F] or NULL: g, then u of each row, for the backward pass
+ * Sums are fp32, in a fixed order; each output is rounded once to its type.
+ *
+ * Low-rank adapters of many requests: with s not NULL, token t adds
+ *   sum over j < rank of s[t][j] * b[a][n][j]     a = adapter_ids[t], rank = ranks[a]
+ * to the sum of channel n (gated: of gate channel f with s[t][j] and row f of b[a], of
+ * up channel f with s[t][R + j] and row F + f), before the activation.
+ *   s    device bf16 [T, R] (gated [T, 2R]): moe_adapter_shrink's
+ *   adapter_ids device int32 [T]; outside [0, n_adapters): no adapter
+ *   b    device bf16: adapter a's [N, R] (gated [2F, R]) contiguous at b + a * b_stride
+ *   ranks device int32 [n_adapters] or NULL: R of all; values outside [0, R] count as
+ *        the nearest of the two
+ * A token's row depends on its own adapter only; what lies past a rank is not used.
+ *
+ * K a multiple of 8 up to 2^20; rows of x, w and s 16-byte aligned with strides up to
+ * 2^21 elements; R a multiple of 8 up to 1024, b 16-byte aligned and b_stride a
+ * multiple of 8; T and N up to 2^24, T*N up to 2^36.  out and pre have any alignment of
+ * their elements.  T = 0 enqueues nothing.
+ */
+moe_status moe_matmul_bf16(const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t T, int32_t N, int32_t K, void* out,
+                           int32_t out_dtype, int64_t ldo, const void* s, int64_t lds, const int32_t* adapter_ids,
+                           const void* b, int64_t b_stride, const int32_t* ranks, int32_t n_adapters, int32_t R,
+                           void* stream);
+
+moe_status moe_gated_matmul_bf16(const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t T, int32_t F, int32_t K,
+                                 int32_t act, void* out, int32_t out_dtype, int64_t ldo, void* pre, int64_t ldp,
+                                 const void* s, int64_t lds, const int32_t* adapter_ids, const void* b, int64_t b_stride,
+                                 const int32_t* ranks, int32_t n_adapters, int32_t R, void* stream);
+
+/*
+ * The first product of the adapters:
+ *   s[t][h * R + j] = scale[a] * sum_k x[t][k] * a_pool[a][h][j][k]     a = adapter_ids[t]
+ * for j < ranks[a], and 0 for the other j and for tokens without an adapter.
+ *   x device bf16 [T, K]; a_pool device bf16: adapter a's [halves, R, K] contiguous at
+ *   a_pool + a * a_stride; halves 1, or 2 (gate and up) for moe_gated_matmul_bf16
+ *   scale device fp32 [n_adapters] or NULL: 1;  s device bf16 [T, halves * R]
+ * Sums and the scale are fp32, rounded once.  Shapes and alignment as above.
+ */
+moe_status moe_adapter_shrink(const void* x, int64_t ldx, int32_t T, int32_t K, const int32_t* adapter_ids,
+                              const void* a_pool, int64_t a_stride, int32_t n_adapters, int32_t R, int32_t halves,
+                              const float* scale, const int32_t* ranks, void* s, int64_t lds, void* stream);
+
+/*
+ * Backward passes of the products (without adapters), dout bf16 [T, N] (gated: [T, F])
+ * being the gradient of out:
+ *   moe_matmul_bf16_backward        dx = dout . w,  dw = dout^T . x
+ *   moe_gated_matmul_bf16_backward  dpre[t][f] = dout u act'(g), dpre[t][F + f] = dout act(g)
+ *                                   (bf16 [T, 2F]; pre as the forward pass wrote it),
+ *                                   dx = dpre . w,  dw = dpre^T . x
+ *   dx device [T, K] or NULL, dw device [N, K] (gated: [2F, K]) or NULL, each fp32 or bf16
+ * dpre may be pre itself (same pointer and stride).  dpre is rounded to bf16, and dx and
+ * dw are those of the rounded values; sums are fp32 in a fixed order, rounded once.  w is
+ * read for dx only, x for dw only: the other may be NULL where its result is not wanted.
+ * N (F) and K multiples of 8; rows of x, w, dout, pre and dpre 16-byte aligned with
+ * strides up to 2^21 elements.  T = 0 writes zeros into dw.
+ */
+moe_status moe_matmul_bf16_backward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* dout, int64_t ldd,
+                                    int32_t T, int32_t N, int32_t K, void* dx, int32_t dx_dtype, int64_t lddx, void* dw,
+                                    int32_t dw_dtype, int64_t lddw, void* stream);
+
+moe_status moe_gated_matmul_bf16_backward(const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t act,
+                                          const void* pre, int64_t ldp, const void* dout, int64_t ldd, int32_t T, int32_t F,
+                                          int32_t K, void* dpre, int64_t ldg, void* dx, int32_t dx_dtype, int64_t lddx,
+                                          void* dw, int32_t dw_dtype, int64_t lddw, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
