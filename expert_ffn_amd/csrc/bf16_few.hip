@@ -10,12 +10,10 @@ namespace moe {
 
 __device__ __forceinline__ int swz16(int r) { return (r & 15) >> 1; }
 
-constexpr int FEW_KG = 4, FEW_NSTG = 2;
-
-template <int TT, bool GATED, bool AD>
-__global__ __launch_bounds__(64 * FEW_KG) void matmul_bf16_few_kernel(MatBf16Params p) {
-    constexpr int KG = FEW_KG, NSTG = FEW_NSTG, BK = 64, STAGE = (16 + 16 * TT) * 128, CH = GATED ? 8 : 16, CPS = 2 + 2 * TT;
-    static_assert(KG >= 4 && NSTG == 2 && CPS <= 63, "256 threads for the results, copies in flight");
+template <int TT, int KG, int NSTG, bool GATED, bool AD>
+__global__ __launch_bounds__(64 * KG) void matmul_bf16_few_kernel(MatBf16Params p) {
+    constexpr int BK = 64, STAGE = (16 + 16 * TT) * 128, CH = GATED ? 8 : 16, CPS = 2 + 2 * TT;
+    static_assert(KG >= 4 && NSTG <= 4 && CPS * (NSTG - 1) <= 63, "256 threads for the results, copies in flight");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * NSTG * STAGE];
     __shared__ __attribute__((aligned(16))) float part[KG][TT][256];
     const int tid = threadIdx.x, lane = tid & 63, kg = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -56,21 +54,89 @@ __global__ __launch_bounds__(64 * FEW_KG) void matmul_bf16_few_kernel(MatBf16Par
         }
     };
     const int row = lane & 15, q = lane >> 4;
-    int aid[TT];   // the adapters of this lane's tokens
+    int aid[TT], rk[TT];   // the adapters of this lane's tokens, and their ranks
     if (AD) {
 #pragma unroll
-        for (int j = 0; j < TT; ++j) {
-            const int a = row + 16 * j < p.T ? p.ad.ids[row + 16 * j] : -1;
-            aid[j] = a >= 0 && a < p.ad.n ? a : -1;
-        }
+        for (int j = 0; j < TT; ++j) aid[j] = row + 16 * j < p.T ? p.ad.ids[row + 16 * j] : -1;
     }
 #pragma unroll
     for (int c = 0; c < NSTG; ++c)
         if (c < nk) copy(c, ring + c * STAGE);
+    // The low-rank part in items of one adapter and 32 ranks, which the waves take in
+    // turn; an adapter that several tokens have is taken once.  The operands are read
+    // straight from memory, those of a wave's first NI items here, behind the first copies.
+    // Each item's product is taken from zero and added in the lanes of its own tokens
+    // only, so that no value of one adapter, an infinity or NaN included, meets
+    // another request's row.
+    constexpr int NI = TT == 1 ? 4 : 2, H = GATED ? 2 : 1;
+    uint64_t left[TT];
+    int item_a = -1, item_k = 0, ia[NI], ik[NI];
+    u32x4 va[NI], vb[NI][TT][H];
+    auto advance = [&]() __attribute__((always_inline)) {   // to the next item; item_a < 0: there is none
+        if (item_a >= 0 && item_k + 32 < p.ad.R) {
+            item_k += 32;
+            return;
+        }
+        item_a = -1;
+        item_k = 0;
+#pragma unroll
+        for (int j = TT - 1; j >= 0; --j)
+            if (left[j]) item_a = __builtin_amdgcn_readlane(aid[j], __builtin_ctzll(left[j]));
+        if (item_a < 0) return;
+#pragma unroll
+        for (int j = 0; j < TT; ++j) left[j] &= ~__ballot(aid[j] == item_a);
+    };
+    auto items = [&]() __attribute__((always_inline)) {   // the operands of the next NI items of this wave
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            ia[n] = item_a;
+            ik[n] = item_k;
+            va[n] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+#pragma unroll
+                for (int h = 0; h < H; ++h) vb[n][j][h] = u32x4{0, 0, 0, 0};
+            const int k = item_k + 8 * q, ch = GATED ? row & 7 : row;
+            if (item_a >= 0 && k < p.ad.R) {
+                if (ch < nch)
+                    va[n] = *reinterpret_cast<const u32x4*>(p.ad.b + item_a * p.ad.b_stride +
+                                                            (static_cast<int64_t>(GATED ? row >> 3 : 0) * p.N + n0 + ch) * p.ad.R + k);
+#pragma unroll
+                for (int j = 0; j < TT; ++j)
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        if (aid[j] == item_a)
+                            vb[n][j][h] = *reinterpret_cast<const u32x4*>(p.ad.s + (row + 16 * j) * p.ad.lds + h * p.ad.R + k);
+            }
+#pragma unroll
+            for (int g = 0; g < KG; ++g)
+                if (item_a >= 0) advance();
+        }
+    };
+    if (AD) {
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            if (aid[j] >= p.ad.n) aid[j] = -1;
+            left[j] = __ballot(aid[j] >= 0);
+            rk[j] = p.ad.R;
+            if (p.ad.ranks != nullptr && aid[j] >= 0) rk[j] = p.ad.ranks[aid[j]];
+        }
+        advance();
+#pragma unroll
+        for (int g = 0; g < KG; ++g)
+            if (g < kg && item_a >= 0) advance();
+        items();
+    }
     f32x4 acc[TT] = {};
     for (int c = 0, buf = 0; c < nk; ++c) {
-        if (c + 1 < nk)
-            __builtin_amdgcn_s_waitcnt(waitcnt_vm(CPS));   // the next stage may still be on its way
+        // the stages behind this one may still be on their way
+        const int behind = min(nk - 1 - c, NSTG - 1);
+        if (NSTG > 3 && behind == 3)
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(3 * CPS));
+        else if (NSTG > 2 && behind == 2)
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * CPS));
+        else if (behind == 1)
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(CPS));
         else
             __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
         asm volatile("" ::: "memory");
@@ -83,7 +149,7 @@ __global__ __launch_bounds__(64 * FEW_KG) void matmul_bf16_few_kernel(MatBf16Par
 #pragma unroll
             for (int j = 0; j < TT; ++j) b[s][j] = *reinterpret_cast<const u32x4*>(st + (16 + 16 * j) * 128 + o);
         }
-        __builtin_amdgcn_s_waitcnt(wait_vm_lds(63));   // read, so the buffer may be filled again
+        __builtin_amdgcn_s_waitcnt(wait_vm_lds(63));   // the operands are read, so the buffer may be filled again
         asm volatile("" ::: "memory");
         if (c + NSTG < nk) copy(c + NSTG, st);
 #pragma unroll
@@ -93,40 +159,35 @@ __global__ __launch_bounds__(64 * FEW_KG) void matmul_bf16_few_kernel(MatBf16Par
         buf = buf + 1 == NSTG ? 0 : buf + 1;
     }
     if (AD) {
-        // The low-rank part as in the tile kernel: adapter by adapter, each from zero and
-        // added in the lanes of its own tokens; the waves take the adapters in turn.
-        uint64_t left[TT];
+        for (;;) {
 #pragma unroll
-        for (int j = 0; j < TT; ++j) left[j] = __ballot(aid[j] >= 0);
-        for (int unit = 0;; ++unit) {
-            int a = -1;
+            for (int n = 0; n < NI; ++n) {
+                if (ia[n] < 0) continue;
+                int rank = 0;
 #pragma unroll
-            for (int j = TT - 1; j >= 0; --j)
-                if (left[j]) a = __builtin_amdgcn_readlane(aid[j], __builtin_ctzll(left[j]));
-            if (a < 0) break;
-#pragma unroll
-            for (int j = 0; j < TT; ++j) left[j] &= ~__ballot(aid[j] == a);
-            if (unit % KG != kg) continue;
-            const int rank = p.ad.ranks ? min(p.ad.ranks[a], p.ad.R) : p.ad.R;
-            const uint16_t* pb = p.ad.b + a * p.ad.b_stride;
-            f32x4 low[TT] = {};
-            for (int h = 0; h < (GATED ? 2 : 1); ++h)
-                for (int k0 = 0; k0 < rank; k0 += 32) {
-                    const int k = k0 + 8 * q, n = GATED ? row & 7 : row;
-                    u32x4 va = {0, 0, 0, 0};
-                    if (k < rank && n < nch && (!GATED || (row >> 3) == h))
-                        va = low_ranks(*reinterpret_cast<const u32x4*>(pb + (static_cast<int64_t>(h) * p.N + n0 + n) * p.ad.R + k), rank - k);
-#pragma unroll
-                    for (int j = 0; j < TT; ++j) {
-                        u32x4 vb = {0, 0, 0, 0};
-                        if (k < rank && aid[j] == a)
-                            vb = *reinterpret_cast<const u32x4*>(p.ad.s + (row + 16 * j) * p.ad.lds + h * p.ad.R + k);
-                        low[j] = mfma16x16x32(va, vb, low[j]);
-                    }
+                for (int j = 0; j < TT; ++j) {
+                    const uint64_t same = __ballot(aid[j] == ia[n]);
+                    if (same) rank = __builtin_amdgcn_readlane(rk[j], __builtin_ctzll(same));
+                }
+                const u32x4 v = low_ranks(va[n], rank - ik[n] - 8 * q);
+                u32x4 half[H];
+                if (GATED) {
+                    const u32x4 none = {0, 0, 0, 0};
+                    half[0] = row < 8 ? v : none;
+                    half[H - 1] = row < 8 ? none : v;
+                } else {
+                    half[0] = v;
                 }
 #pragma unroll
-            for (int j = 0; j < TT; ++j)
-                if (aid[j] == a) acc[j] += low[j];
+                for (int j = 0; j < TT; ++j) {
+                    f32x4 low = {};
+#pragma unroll
+                    for (int h = 0; h < H; ++h) low = mfma16x16x32(half[h], vb[n][j][h], low);
+                    if (aid[j] == ia[n]) acc[j] += low;
+                }
+            }
+            if (item_a < 0) break;
+            items();
         }
     }
     // lane l: token l & 15 of tile j, tile rows 4 (l >> 4) ..
@@ -162,11 +223,11 @@ __global__ __launch_bounds__(64 * FEW_KG) void matmul_bf16_few_kernel(MatBf16Par
     }
 }
 
-template <int TT, bool GATED>
+template <int TT, bool GATED, int KG, int NSTG>
 static hipError_t few(const MatBf16Params& p, hipStream_t s) {
     constexpr int CH = GATED ? 8 : 16;
-    auto kn = p.ad.s ? matmul_bf16_few_kernel<TT, GATED, true> : matmul_bf16_few_kernel<TT, GATED, false>;
-    hipLaunchKernelGGL(kn, dim3((p.N + CH - 1) / CH), dim3(64 * FEW_KG), 0, s, p);
+    auto kn = p.ad.s ? matmul_bf16_few_kernel<TT, KG, NSTG, GATED, true> : matmul_bf16_few_kernel<TT, KG, NSTG, GATED, false>;
+    hipLaunchKernelGGL(kn, dim3((p.N + CH - 1) / CH), dim3(64 * KG), 0, s, p);
     return hipGetLastError();
 }
 
@@ -175,14 +236,20 @@ hipError_t tiles_gated(const MatBf16Params& p, hipStream_t s);
 hipError_t tiles_nn(const MatBf16Params& p, hipStream_t s);
 hipError_t tiles_tn(const MatBf16Params& p, hipStream_t s);
 
-// Which kernel.
+// Up to 16 tokens the kernel for few tokens (T = 1 and 16: 1.1 to 1.8 times as fast as the
+// best tile from 64 to 8192 weight rows, K 136 to 4096: N = 2816, K = 2112 3.8 and 5.9 us).
+// Further as long as every workgroup has a CU of its own: to 32 tokens 1.2 to 1.6 times as
+// fast (more workgroups: 5 to 10 % slower), to 48 1.0 to 1.3 times, to 64 as fast with K =
+// 1424, 1.1 to 1.2 times with K up to 1024.  Three stages against two: 4 to 9 % less
+// time up to 32 tokens, equal or slower for more.
 template <bool GATED>
 static hipError_t forward(const MatBf16Params& p, hipStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.N) * (GATED ? 2 : 1);
-    if (p.T <= 16) return few<1, GATED>(p, s);
+    if (p.T <= 16) return few<1, GATED, 4, 3>(p, s);
     if (rows <= 256 * 16) {
-        if (p.T <= 32) return few<2, GATED>(p, s);
-        if (p.T <= 48) return few<3, GATED>(p, s);
+        if (p.T <= 32) return few<2, GATED, 4, 3>(p, s);
+        if (p.T <= 48) return few<3, GATED, 4, 2>(p, s);
+        if (p.T <= 64 && p.K <= 1024) return few<4, GATED, 4, 2>(p, s);
     }
     return GATED ? tiles_gated(p, s) : tiles_nt(p, s);
 }

@@ -4,8 +4,8 @@
 
 namespace moe {
 
-hipError_t tiles_nn(const MatBf16Params& p, hipStream_t s) { return bf16_tiles<MAT_NN, false>(BF16_TILES, p, s); }
-hipError_t tiles_tn(const MatBf16Params& p, hipStream_t s) { return bf16_tiles<MAT_TN, false>(BF16_TILES, p, s); }
+hipError_t tiles_nn(const MatBf16Params& p, hipStream_t s) { return bf16_tiles<MAT_NN, false>(p, s); }
+hipError_t tiles_tn(const MatBf16Params& p, hipStream_t s) { return bf16_tiles<MAT_TN, false>(p, s); }
 
 // act(g) = g q with q = 1 / (1 + e^z):  act'(g) = q - g q (1 - q) dz/dg
 //   silu z = -g;  gelu (tanh form) z = -2 sqrt(2/pi) (g + 0.044715 g^3)

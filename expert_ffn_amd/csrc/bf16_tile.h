@@ -7,8 +7,10 @@
 // Sums are fp32 in the MFMA's accumulators, in a fixed order; the epilogue is fp32
 // and rounds once to the output type.
 //
-// MFMA operands: A = channels, B = tokens, D column = token, so a lane holds 4
-// consecutive channels of one token.
+// MFMA 16x16x32, A = channels, B = tokens, D column = token, so a lane holds 4
+// consecutive channels of one token.  Long products run at the power limit, where
+// this form gives 2.08 PFLOP/s and 32x32x16 1.85 (back to back on random values; on
+// zeros both 2.4): it moves half the accumulators per product.
 #pragma once
 
 #include <type_traits>
@@ -18,12 +20,7 @@
 
 namespace moe {
 
-typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
-
-__device__ __forceinline__ f32x16 mfma32_bf16(const u32x4& a, const u32x4& b, const f32x16& c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
 
 // LDS DMA: 64 lanes x 16 bytes to dst + 16 * lane (dst uniform); a lane past the
 // resource writes zeros.  Completion is the wave's vmcnt, waited for by the caller.
@@ -35,9 +32,12 @@ __device__ __forceinline__ void lds_dma16(rsrc_t r, uint8_t* dst, uint32_t off, 
 // 4 x 16 block of 16-bit values, its rows in memory, read by columns: the 16 lanes of
 // a group give the addresses of its 8-byte pieces (lane i: row i / 4, columns 4 (i % 4)
 // ..), and lane i receives column i, rows 0 .. 3.
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+__device__ __forceinline__ u32x2 lds_read_columns(lds_s16x4* __restrict__ p) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+}
 __device__ __forceinline__ u32x2 lds_read_columns(const uint8_t* p) {
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4*>(
-                                         reinterpret_cast<uintptr_t>(p))));
+    return lds_read_columns(reinterpret_cast<lds_s16x4*>(reinterpret_cast<uintptr_t>(p)));
 }
 
 // the first n of 8 ranks (16-bit values), zeros behind them
@@ -49,27 +49,37 @@ __device__ __forceinline__ u32x4 low_ranks(const u32x4& v, int n) {
     return r;
 }
 
+// no infinity or NaN among 8 bf16 values
+__device__ __forceinline__ bool all_finite(const u32x4& v) {
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ok = ok && (v[i] & 0x7F80u) != 0x7F80u && (v[i] & 0x7F800000u) != 0x7F800000u;
+    return ok;
+}
+
 __host__ __device__ constexpr int wait_vm_lds(int n) { return waitcnt_vm(n) & ~0x0F00; }   // and LDS reads to 0
 
 // 16-byte chunk q of row r (128 bytes) is stored at position q ^ swz_row(r)
-__device__ __forceinline__ int swz_row(int r) { return (r & 7) ^ ((r >> 3) & 3); }
+__device__ __forceinline__ int swz_row(int r) { return (r & 15) >> 1; }
 
 // One operand of a tile: ROWS channels or tokens, 64 k in a stage of ROWS * 128 bytes.
 //
 // Rows along k (!TR): [ROWS][128 bytes]; a copy writes 8 rows.  A 16-byte read of a
-// fragment is served 16 lanes at a time, lanes 0-3, 12-15, 20-27 (and 4-11, 16-19,
-// 28-31) together: swz_row makes their 16 rows fall into all 64 banks.
+// fragment (16 rows, 4 chunks) is served 16 lanes at a time, lanes 0-3, 12-15, 20-27
+// (and 4-11, 16-19, 28-31) together: swz_row makes their 16 rows fall into all 64 banks.
 //
-// Rows are the k (TR): [64][ROWS * 2 bytes].  A fragment is read by columns, four k of
-// 32 columns (64 bytes each) by half a wave at once: 64-byte pieces of rows that would
-// meet in the same banks are exchanged inside their row (swz_k), so that the four
-// pieces cover all 64 banks.
+// Rows are the k (TR): [64][ROWS * 2 bytes].  A fragment is read by columns: half a wave
+// reads 16 columns (32 bytes) of k 0 .. 3 and 8 .. 11 (of 4 .. 7 and 12 .. 15, and so on)
+// at once.  swz_k exchanges 32-byte pieces inside a row so that these eight cover all 64
+// banks.
 template <int ROWS, bool TR>
 struct Operand {
     static constexpr bool COLUMNS = TR;
     static constexpr int PITCH = TR ? ROWS * 2 : 128, CPR = PITCH / 16;
+    static_assert(!TR || PITCH % 256 == 0 || PITCH % 256 == 128 || PITCH == 64, "banks of a row");
     __device__ static int swz_k(int k) {
-        return PITCH % 256 == 0 ? (k & 3) << 2 : PITCH % 256 == 128 ? ((k >> 1) & 1) << 2 : 0;
+        const int far = (k >> 3) & 1;
+        return PITCH % 256 == 0 ? ((k & 3) | far << 2) << 1 : PITCH % 256 == 128 ? (((k >> 1) & 1) | far << 1) << 1 : far << 1;
     }
     // copy number c (1024 bytes each), lane l: row of the stage, and the 16-byte chunk of the source row
     __device__ static int row(int c, int lane) { return (c * 64 + lane) / CPR; }
@@ -84,13 +94,13 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
     constexpr bool GATED = KIND == MAT_GATED, TRA = KIND == MAT_NN || KIND == MAT_TN, TRB = KIND == MAT_TN;
     using OA = Operand<BN, TRA>;
     using OB = Operand<BT, TRB>;
-    constexpr int NW = WN * WT, NB = BN / WN / 32, TB = BT / WT / 32;
+    constexpr int NW = WN * WT, NB = BN / WN / 16, TB = BT / WT / 16;   // blocks of 16 channels, of 16 tokens
     constexpr int BK = 64;                                  // k of a step
     constexpr int STAGE = (BN + BT) * 128, DA = BN / 8 / NW, DB = BT / 8 / NW, CPS = DA + DB;
     constexpr int CH = GATED ? BN / 2 : BN;   // output channels per tile
     constexpr int CW = CH / WN;               // of a wave
     constexpr int RING = NSTG * STAGE;
-    static_assert(DA * 8 * NW == BN && DB * 8 * NW == BT && BN % 32 == 0, "tile shape");
+    static_assert(DA * 8 * NW == BN && DB * 8 * NW == BT && NB * 16 * WN == BN && TB * 16 * WT == BT && (!GATED || NB % 2 == 0), "tile shape");
     static_assert(NSTG >= 2 && NSTG <= 4 && CPS * (NSTG - 1) <= 63, "copies in flight");
     static_assert((KG - 1) * BN * BT * 4 <= KG * RING, "epilogue regions");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * RING];
@@ -146,7 +156,13 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
     // past the last are not requested, by a copy of the loop's body without copies; the
     // largest tiles (two stages) request them as zeros, which keeps their body short.
     constexpr bool TAIL = NSTG > 2;
-    auto copy = [&](int c, uint8_t* st, int i) {
+    rsrc_t wk = rsrc_t(), xk = rsrc_t();   // operands whose rows are the k: of the stage that is requested
+    auto stage = [&](int c) __attribute__((always_inline)) {
+        const int k = BK * (c * KG + kg);
+        if (TRA) wk = step_of(p.w, p.ldw, n0, nch, k);
+        if (TRB) xk = step_of(p.x, p.ldx, t0, ntok, k);
+    };
+    auto copy = [&](int c, uint8_t* st, int i) __attribute__((always_inline)) {
         const int k = BK * (c * KG + kg);
         // the scalar offset stays inside the resource: the range check subtracts it
         // from the resource's size
@@ -154,7 +170,7 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
         if (i < DA) {
             uint8_t* dst = st + (wave + NW * i) * 1024;
             if (TRA) {
-                lds_dma16(step_of(p.w, p.ldw, n0, nch, k), dst, ao[i], 0);
+                lds_dma16(wk, dst, ao[i], 0);
             } else {
                 const uint32_t o = b + 16 * OA::chunk(wave + NW * i, lane) < kb ? ao[i] : NO_LANE;
                 if (is_up(8 * (wave + NW * i)))   // 8 rows lie on one side of a gated block
@@ -166,91 +182,101 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
             const int j = i - DA;
             uint8_t* dst = st + BN * 128 + (wave + NW * j) * 1024;
             if (TRB) {
-                lds_dma16(step_of(p.x, p.ldx, t0, ntok, k), dst, bo[j], 0);
+                lds_dma16(xk, dst, bo[j], 0);
             } else {
                 lds_dma16(xr, dst, b + 16 * OB::chunk(wave + NW * j, lane) < kb ? bo[j] : NO_LANE, so);
             }
         }
     };
-    // Fragments: row (channel, token) l & 31 of a 32-row block, k 16 s + 8 (l >> 5) .. + 7
-    const int l32 = lane & 31, hh = lane >> 5;
+    // Fragments: row (channel, token) l & 15 of a block, k 32 s + 8 (l >> 4) .. + 7
+    const int l16 = lane & 15, q4 = lane >> 4;
     auto base_of = [&](auto o, int first) {   // lane's part of the address
         using O = decltype(o);
-        if (!O::COLUMNS) return (first + l32) * 128;
-        const int k = 8 * hh + (lane & 15) / 4;
-        const int q = first / 8 + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+        if (!O::COLUMNS) return (first + l16) * 128;
+        const int k = 8 * q4 + l16 / 4, q = first / 8 + ((lane >> 1) & 1);
         return k * O::PITCH + ((q ^ O::swz_k(k)) << 4) + 8 * (lane & 1);
     };
     int abase[NB], bbase[TB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) abase[b] = base_of(OA(), wn * (BN / WN) + 32 * b);
+    for (int b = 0; b < NB; ++b) abase[b] = base_of(OA(), wn * (BN / WN) + 16 * b);
 #pragma unroll
-    for (int b = 0; b < TB; ++b) bbase[b] = BN * 128 + base_of(OB(), wt * (BT / WT) + 32 * b);
+    for (int b = 0; b < TB; ++b) bbase[b] = BN * 128 + base_of(OB(), wt * (BT / WT) + 16 * b);
     u32x4 fa[2][NB], fb[2][TB];
-    auto fragment = [&](bool tr, int pitch, const uint8_t* at, int s) {
-        if (!tr) return *reinterpret_cast<const u32x4*>(at + ((2 * s + hh) ^ swz_row(l32)) * 16);
-        const u32x2 lo = lds_read_columns(at + 16 * s * pitch), hi = lds_read_columns(at + (16 * s + 4) * pitch);
+    auto fragment = [&](bool tr, int pitch, const uint8_t* at, int s) __attribute__((always_inline)) {
+        if (!tr) return *reinterpret_cast<const u32x4*>(at + ((4 * s + q4) ^ swz_row(l16)) * 16);
+        const u32x2 lo = lds_read_columns(at + 32 * s * pitch), hi = lds_read_columns(at + (32 * s + 4) * pitch);
         return u32x4{lo[0], lo[1], hi[0], hi[1]};
     };
-    auto read = [&](const uint8_t* st, int s, int set) {
-#pragma unroll
-        for (int i = 0; i < NB; ++i) fa[set][i] = fragment(TRA, OA::PITCH, st + abase[i], s);
-#pragma unroll
-        for (int i = 0; i < TB; ++i) fb[set][i] = fragment(TRB, OB::PITCH, st + bbase[i], s);
+    // operand q of round s: the channels' fragments, then the tokens'
+    auto read = [&](const uint8_t* st, int s, int q) __attribute__((always_inline)) {
+        if (q < NB)
+            fa[s & 1][q] = fragment(TRA, OA::PITCH, st + abase[q], s);
+        else
+            fb[s & 1][q - NB] = fragment(TRB, OB::PITCH, st + bbase[q - NB], s);
     };
-    f32x16 acc[NB][TB] = {};
-    // Within a step the operands of MFMA round s + 1 are read while round s runs.  The
-    // step's last round runs after the barrier: at the barrier every wave holds the
-    // last operands of stage c in registers and its copies of stage c + 1 have landed,
-    // so the reads of stage c + 1 begin, and the copies of stage c + NSTG go to the
-    // buffer of stage c, while that round is computed.  The copies of a stage are
-    // spread between the MFMAs of its rounds, so that the address unit (16 cycles a
-    // copy, for all waves of the CU) works beside them.
-    constexpr int S = BK / 16;   // rounds of a step (even: a step starts with set 0)
-    constexpr int M = (NSTG > 2 ? S : 2) * NB * TB;
-    auto round = [&](int s, int c, uint8_t* to) {
+    f32x4 acc[NB][TB] = {};
+    // Rounds of 32 k, S to a step.  While round s runs, token block by token block, the
+    // operands of the next round are read, about as many with each block and the last
+    // with the last block but one: a token fragment then takes the registers of one
+    // that is used up.  The step's last round runs after the barrier: at the barrier
+    // every wave holds the last operands of stage c in registers and its copies of stage
+    // c + 1 have landed, so the reads of stage c + 1 begin, and the copies of stage c +
+    // NSTG go to the buffer of stage c, while that round is computed.  The copies of a
+    // stage are spread between the MFMAs, so that the address unit (16 cycles a copy,
+    // for all waves of the CU) works beside them.
+    constexpr int S = BK / 32;
+    constexpr int NR = NB + TB, RG = TB > 1 ? TB - 1 : 1;   // operands of a round, the blocks they are read with
+    constexpr int M = (NSTG > 2 ? S : 1) * NB * TB;
+    auto round = [&](int s, const uint8_t* st, int rs, int c, uint8_t* to) __attribute__((always_inline)) {   // reads round rs of stage st (null: nothing)
 #pragma unroll
-        for (int m = 0; m < NB * TB; ++m) {
-            const int i = m / TB, j = m % TB, slot = (s + 1) % S * NB * TB + m;
-            acc[i][j] = mfma32_bf16(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
-            if (c >= 0) {
+        for (int j = 0; j < TB; ++j) {
+            if (st != nullptr) {
 #pragma unroll
-                for (int q = slot * CPS / M; q < (slot + 1) * CPS / M && q < CPS; ++q) copy(c, to, q);
+                for (int q = 0; q < NR; ++q)
+                    if (q * RG / NR == j) read(st, rs, q);
             }
-            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int slot = (s + 1) % S * NB * TB + j * NB + i;
+                acc[i][j] = mfma16x16x32(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
+                if (c >= 0) {
+#pragma unroll
+                    for (int q = slot * CPS / M; q < (slot + 1) * CPS / M && q < CPS; ++q) copy(c, to, q);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
-    auto most = [&](const uint8_t* st, int c, uint8_t* to) {   // rounds 0 .. S - 2, each reading the next one's operands first
+    auto most = [&](const uint8_t* st, int c, uint8_t* to) __attribute__((always_inline)) {   // rounds 0 .. S - 2
 #pragma unroll
-        for (int s = 0; s + 1 < S; ++s) {
-            read(st, s + 1, (s + 1) & 1);
-            __builtin_amdgcn_sched_barrier(0);
-            round(s, c, to);
-        }
+        for (int s = 0; s + 1 < S; ++s) round(s, st, s + 1, c, to);
     };
 #pragma unroll
     for (int c = 0; c < NSTG; ++c) {
         if (TAIL && c >= nk) break;
+        stage(c);
 #pragma unroll
         for (int q = 0; q < CPS; ++q) copy(c, ring + c * STAGE, q);
     }
-    // the adapters of this lane's tokens
-    int aid[TB];
+    int aid[TB], rk[TB];   // the adapters of this lane's tokens, and their ranks
     if (AD) {
 #pragma unroll
         for (int j = 0; j < TB; ++j) {
-            const int t = wt * (BT / WT) + 32 * j + l32;
+            const int t = wt * (BT / WT) + 16 * j + l16;
             const int a = t < ntok ? p.ad.ids[t0 + t] : -1;
             aid[j] = a >= 0 && a < p.ad.n ? a : -1;
+            rk[j] = p.ad.R;
+            if (p.ad.ranks != nullptr && aid[j] >= 0) rk[j] = min(p.ad.ranks[aid[j]], p.ad.R);
         }
     }
     __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
     __syncthreads();
-    read(ring, 0, 0);
+#pragma unroll
+    for (int q = 0; q < NR; ++q) read(ring, 0, q);
     most(ring, -1, ring);
     int buf = 0;
     // from step c to step c + 1: `left` of the stages behind that one may still be on their way
-    auto step = [&](int left, int next) {
+    auto step = [&](int left, int next) __attribute__((always_inline)) {
         if (NSTG > 3 && left >= 2)
             __builtin_amdgcn_s_waitcnt(wait_vm_lds(CPS * 2));
         else if (NSTG > 2 && left >= 1)
@@ -263,65 +289,103 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
         uint8_t* done = ring + buf * STAGE;
         buf = buf + 1 == NSTG ? 0 : buf + 1;
         const uint8_t* st = ring + buf * STAGE;
-        read(st, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        round(S - 1, next, done);
+        if (next >= 0) stage(next);
+        round(S - 1, st, 0, next, done);
         most(st, next, done);
     };
     int c = 0;
     for (; c + (TAIL ? NSTG : 1) < nk; ++c) step(NSTG - 2, c + NSTG);
     if (TAIL)
         for (; c + 1 < nk; ++c) step(nk - 2 - c, -1);
-    round(S - 1, -1, ring);
+    round(S - 1, nullptr, 0, -1, ring);
     if (AD) {
-        // The low-rank part, adapter by adapter of this wave's tokens: 16 ranks are one
-        // MFMA, the operands straight from memory.  Each adapter's product is taken from
-        // zero and added in the columns (lanes) of its own tokens only, so that no value
-        // of one adapter, an infinity or NaN included, meets another request's row.
+        // The low-rank part in items of one adapter of this wave's tokens, one half (gated)
+        // and 32 ranks, NI of them at a time, their operands straight from memory; the K
+        // groups take the items in turn.  Tokens of other adapters are zeros.  An item whose
+        // adapter holds an infinity or NaN is taken from zero and added in the columns
+        // (lanes) of its own tokens only, so that it does not meet another request's row.
+        constexpr int NI = NB + TB <= 4 ? 4 : NB + TB <= 9 ? 2 : 1, NH = GATED ? NB / 2 : NB;
         uint64_t left[TB];
 #pragma unroll
         for (int j = 0; j < TB; ++j) left[j] = __ballot(aid[j] >= 0);
-        int unit = 0;
-        for (;;) {
-            int a = -1;
-#pragma unroll
-            for (int j = TB - 1; j >= 0; --j)
-                if (left[j]) a = __builtin_amdgcn_readlane(aid[j], __builtin_ctzll(left[j]));
-            if (a < 0) break;
-            bool has[TB];
-#pragma unroll
-            for (int j = 0; j < TB; ++j) {
-                const uint64_t same = __ballot(aid[j] == a);
-                has[j] = same != 0;
-                left[j] &= ~same;
+        int item_a = -1, item_h = 0, item_k = 0, rank = 0;
+        auto advance = [&]() __attribute__((always_inline)) {   // to the next item; item_a < 0: there is none
+            if (item_a >= 0) {
+                if (item_k + 32 < rank) {
+                    item_k += 32;
+                    return;
+                }
+                item_k = 0;
+                if (GATED && item_h == 0) {
+                    item_h = 1;
+                    return;
+                }
             }
-            if (KG > 1 && unit++ % KG != kg) continue;
-            const int rank = p.ad.ranks ? min(p.ad.ranks[a], p.ad.R) : p.ad.R;
-            const uint16_t* pb = p.ad.b + a * p.ad.b_stride;
+            item_h = item_k = 0;
+            for (;;) {
+                item_a = -1;
 #pragma unroll
-            for (int j = 0; j < TB; ++j) {
-                if (!has[j]) continue;
-                const int t = t0 + wt * (BT / WT) + 32 * j + l32;
-                f32x16 low[NB] = {};
-                for (int h = 0; h < (GATED ? 2 : 1); ++h)
-                    for (int k = 8 * hh; k < rank + 8 * hh; k += 16) {
-                        u32x4 vb = {0, 0, 0, 0}, va[NB] = {};
-                        if (k < rank) {
-                            if (aid[j] == a) vb = *reinterpret_cast<const u32x4*>(p.ad.s + t * p.ad.lds + h * p.ad.R + k);
-#pragma unroll
-                            for (int i = 0; i < NB; ++i) {
-                                const int row = wn * (BN / WN) + 32 * i + l32, n = channel(row);
-                                if (n < nch && is_up(row) == (h == 1))
-                                    va[i] = low_ranks(*reinterpret_cast<const u32x4*>(pb + (static_cast<int64_t>(h) * p.N + n0 + n) * p.ad.R + k),
-                                                      rank - k);
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < NB; ++i) low[i] = mfma32_bf16(va[i], vb, low[i]);
+                for (int j = TB - 1; j >= 0; --j)
+                    if (left[j]) {
+                        const int lane_of = __builtin_ctzll(left[j]);
+                        item_a = __builtin_amdgcn_readlane(aid[j], lane_of);
+                        rank = __builtin_amdgcn_readlane(rk[j], lane_of);
                     }
-                if (aid[j] == a) {
+                if (item_a < 0) return;
 #pragma unroll
-                    for (int i = 0; i < NB; ++i) acc[i][j] += low[i];
+                for (int j = 0; j < TB; ++j) left[j] &= ~__ballot(aid[j] == item_a);
+                if (rank > 0) return;
+            }
+        };
+        advance();
+        for (int g = 0; g < kg && item_a >= 0; ++g) advance();
+        while (item_a >= 0) {
+            u32x4 va[NI][NH], vb[NI][TB];
+            int ia[NI], ih[NI];
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                ia[n] = item_a;
+                ih[n] = item_h;
+                const int k = item_k + 8 * q4;
+                const bool in = item_a >= 0 && k < rank;
+                const uint16_t* pb = p.ad.b + item_a * p.ad.b_stride + k;
+                const uint16_t* ps = p.ad.s + item_h * p.ad.R + k;
+#pragma unroll
+                for (int i = 0; i < NH; ++i) {
+                    const int c = wn * CW + 16 * i + l16;
+                    va[n][i] = u32x4{0, 0, 0, 0};
+                    if (in && c < nch)
+                        va[n][i] = low_ranks(*reinterpret_cast<const u32x4*>(pb + (static_cast<int64_t>(item_h) * p.N + n0 + c) * p.ad.R),
+                                             rank - k);
+                }
+#pragma unroll
+                for (int j = 0; j < TB; ++j) {
+                    vb[n][j] = u32x4{0, 0, 0, 0};
+                    if (in && aid[j] == item_a)
+                        vb[n][j] = *reinterpret_cast<const u32x4*>(ps + (t0 + wt * (BT / WT) + 16 * j + l16) * p.ad.lds);
+                }
+                for (int g = 0; g < KG && item_a >= 0; ++g) advance();
+            }
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                if (ia[n] < 0) continue;
+                bool finite = true;
+#pragma unroll
+                for (int i = 0; i < NH; ++i) finite = finite && all_finite(va[n][i]);
+                const bool plain = __all(finite);
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    if (GATED && (i & 1) != ih[n]) continue;
+                    const u32x4& v = va[n][GATED ? i / 2 : i];
+#pragma unroll
+                    for (int j = 0; j < TB; ++j) {
+                        if (plain) {
+                            acc[i][j] = mfma16x16x32(v, vb[n][j], acc[i][j]);
+                        } else {
+                            const f32x4 low = mfma16x16x32(v, vb[n][j], f32x4{0, 0, 0, 0});
+                            if (aid[j] == ia[n]) acc[i][j] += low;
+                        }
+                    }
                 }
             }
         }
@@ -329,67 +393,59 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
     __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));   // zero stages have landed too
     __syncthreads();   // the rings are free
     if (KG > 1) {
-        float* part = reinterpret_cast<float*>(lds);
+        f32x4* part = reinterpret_cast<f32x4*>(lds);
+        auto at = [&](int g, int i, int j) { return part + ((((g - 1) * NW + wave) * NB + i) * TB + j) * 64 + lane; };
         if (kg > 0) {
 #pragma unroll
             for (int i = 0; i < NB; ++i)
 #pragma unroll
-                for (int j = 0; j < TB; ++j)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        *reinterpret_cast<f32x4*>(part + (((((kg - 1) * NW + wave) * NB + i) * TB + j) * 4 + v) * 256 + lane * 4) =
-                            f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+                for (int j = 0; j < TB; ++j) *at(kg, i, j) = acc[i][j];
         }
         __syncthreads();
         if (kg > 0) return;
 #pragma unroll
-        for (int q = 1; q < KG; ++q)
+        for (int g = 1; g < KG; ++g)
 #pragma unroll
             for (int i = 0; i < NB; ++i)
 #pragma unroll
-                for (int j = 0; j < TB; ++j)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const f32x4 o = *reinterpret_cast<const f32x4*>(
-                            part + (((((q - 1) * NW + wave) * NB + i) * TB + j) * 4 + v) * 256 + lane * 4);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][4 * v + e] += o[e];
-                    }
+                for (int j = 0; j < TB; ++j) acc[i][j] += *at(g, i, j);
     }
-    // Epilogue, 32 tokens at a time: the wave's [32 tokens][CW channels] go through
+    // Epilogue, TK tokens at a time: the wave's [TK tokens][CW channels] go through
     // LDS (16-byte chunks at position c ^ token) and leave as row pieces; rows that are
     // not 16-byte aligned leave by elements, neighbouring lanes storing neighbouring
     // ones.  With groups, the partial sums may lie where another wave of group 0 still
     // reads: the waves' regions start behind them.
-    constexpr int PART = KG > 1 ? (KG - 1) * BN * BT * 4 : 0;
+    constexpr int PART = KG > 1 ? (KG - 1) * BN * BT * 4 : 0, TK = TB % 2 ? 16 : 32;
     auto leave = [&](auto type, int tb, void* out, int64_t ldo, int col0, auto value) {
         constexpr int es = decltype(type)::value == F32 ? 4 : 2, cpr = CW * es / 16;   // 16-byte chunks per row
         constexpr bool p2 = (cpr & (cpr - 1)) == 0;           // else the rows are 16 bytes apart instead
         constexpr int RS = CW * es + (p2 ? 0 : 16);
-        static_assert(PART + 32 * RS * NW <= KG * RING, "epilogue regions");
-        uint8_t* my = lds + PART + wave * 32 * RS;
+        constexpr int REGION = TK * (CW * 4 + 16);   // of a wave, the same for both types: they may follow each other
+        static_assert(RS * TK <= REGION && PART + REGION * NW <= KG * RING, "epilogue regions");
+        uint8_t* my = lds + PART + wave * REGION;
         auto at = [&](int tok, int c) { return my + tok * RS + ((p2 ? c ^ (tok & (cpr - 1)) : c) << 4); };
-        const int tl = wt * (BT / WT) + 32 * tb;   // first token of the block in the tile
+        const int tl = wt * (BT / WT) + TK * tb;   // first token of these in the tile
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int j = 0; j < TK / 16; ++j)
 #pragma unroll
-            for (int q = 0; q < (GATED ? 2 : 4); ++q) {   // 4 channels
-                const int cl = (GATED ? 16 : 32) * b + 8 * q + 4 * hh;
+            for (int b = 0; b < (GATED ? NB / 2 : NB); ++b) {   // 4 channels
+                const int cl = 16 * b + 4 * q4, tok = 16 * j + l16;
                 float v[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = value(b, 4 * q + j);
+                for (int e = 0; e < 4; ++e) v[e] = value(b, TK / 16 * tb + j, e);
                 if (es == 4)
-                    *reinterpret_cast<f32x4*>(at(l32, cl >> 2)) = f32x4{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<f32x4*>(at(tok, cl >> 2)) = f32x4{v[0], v[1], v[2], v[3]};
                 else
-                    *reinterpret_cast<u32x2*>(at(l32, cl >> 3) + 8 * hh) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    *reinterpret_cast<u32x2*>(at(tok, cl >> 3) + 8 * (q4 & 1)) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         uint8_t* base = static_cast<uint8_t*>(out) + ((t0 + tl) * ldo + n0 + col0) * es;
         if (reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * es % 16 == 0 && col0 * es % 16 == 0) {
 #pragma unroll 4
-            for (int i0 = 0; i0 < 32 * cpr; i0 += 64) {
+            for (int i0 = 0; i0 < TK * cpr; i0 += 64) {
                 const int it = i0 + lane;
+                if (TK * cpr % 64 && it >= TK * cpr) continue;
                 const int tok = it / cpr, c = it % cpr;
                 const u32x4 v = *reinterpret_cast<const u32x4*>(at(tok, c));
                 const int ch = wn * CW + c * (16 / es);
@@ -409,7 +465,7 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
             }
         } else {
 #pragma unroll 4
-            for (int i0 = 0; i0 < 32 * CW; i0 += 64) {
+            for (int i0 = 0; i0 < TK * CW; i0 += 64) {
                 const int it = i0 + lane;
                 const int tok = it / CW, e = it % CW;
                 const uint8_t* s = at(tok, e * es / 16) + e * es % 16;
@@ -428,17 +484,17 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
     using is_f32 = std::integral_constant<int, F32>;
     using is_bf16 = std::integral_constant<int, BF16>;
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb) {
-        auto result = [&](int b, int v) {
-            return GATED ? act_fn(p.act, acc[b][tb][v]) * acc[b][tb][GATED ? v + 8 : v] : acc[b][tb][v];
-        };
+    for (int tb = 0; tb < TB * 16 / TK; ++tb) {
+        auto gate = [&](int b, int j, int e) { return acc[GATED ? 2 * b : b][j][e]; };
+        auto up = [&](int b, int j, int e) { return acc[GATED ? 2 * b + 1 : b][j][e]; };
+        auto result = [&](int b, int j, int e) { return GATED ? act_fn(p.act, gate(b, j, e)) * up(b, j, e) : gate(b, j, e); };
         if (p.out_dt == F32)
             leave(is_f32(), tb, p.out, p.ldo, 0, result);
         else
             leave(is_bf16(), tb, p.out, p.ldo, 0, result);
         if (GATED && p.pre != nullptr) {
-            leave(is_bf16(), tb, p.pre, p.ldp, 0, [&](int b, int v) { return acc[b][tb][v]; });
-            leave(is_bf16(), tb, p.pre, p.ldp, p.N, [&](int b, int v) { return acc[b][tb][GATED ? v + 8 : v]; });
+            leave(is_bf16(), tb, p.pre, p.ldp, 0, gate);
+            leave(is_bf16(), tb, p.pre, p.ldp, p.N, up);
         }
     }
 }
@@ -454,24 +510,75 @@ static hipError_t bf16_tile(const MatBf16Params& p, hipStream_t s) {
 }
 
 // Which tile: the one with the smallest estimated time.  A launch of W workgroups
-// over 256 CUs takes ceil(W / 256) of them after each other, so with `steps` K steps
-// about steps * max(alone, ceil(W / 256) * full) + fixed: `full` is the time of a step,
-// `alone` that of a workgroup that has its CU for itself where it is longer.
+// over 256 CUs takes ceil(W / 256) of them after each other, so with `steps` 64-element
+// K steps about fixed + max(steps * alone + end, ceil(W / 256) * (steps * full + end)):
+// `full` is the time of a step, `alone` that of a workgroup that has its CU for itself
+// (several of the small ones fit on a CU), `end` that of prologue and epilogue.  The
+// figures (us) are fitted to times of 18 tiles at 60 shapes of each kind (T 16 to 8192,
+// the other sizes 64 to 8192); of those, these ten lose 0.5 to 0.8 % on average against
+// the best of all 18 (the ends of the range: T = 80, N = 2336, K = 232, TN: 32 x 32 3.4
+// us, 256 x 256 9.8; T = 8192, N = 4096, K = 8192: 32 x 32 1612 us, 256 x 256 404), and
+// the choice by the estimate another 1.6 to 2.4 %.  192 x 192 is there for three stages
+// of copies under 160 KB (gated T = 4096, 2 x 2112 x 2816: 85 us, 256 x 192 99, 128 x 192
+// 94).  Gated 256 x 256 does not fit the registers (152 us there).
 struct Bf16Tile {
     int bn, bt;
-    float alone, full, fixed;
+    float alone, full, fixed, end;
 };
-constexpr int N_BF16_TILES = 10;
+template <int KIND>
+struct Bf16Tiles;
+template <>
+struct Bf16Tiles<MAT_NT> {
+    static constexpr Bf16Tile T[] = {
+        {32, 32, 0.071f, 0.091f, 1.28f, 2.31f},   {64, 32, 0.117f, 0.139f, 1.09f, 2.69f},   {64, 64, 0.103f, 0.190f, 0.80f, 3.06f},
+        {64, 64, 0.238f, 0.198f, 2.59f, 0.72f},   {128, 64, 0.322f, 0.271f, 2.59f, 1.92f},  {128, 128, 0.420f, 0.423f, 0.00f, 4.81f},
+        {128, 192, 0.557f, 0.557f, 2.06f, 4.09f}, {192, 192, 0.597f, 0.639f, 0.00f, 10.46f}, {256, 192, 0.894f, 0.923f, 0.00f, 8.89f},
+        {256, 256, 1.033f, 1.083f, 0.00f, 11.41f},
+    };
+};
+template <>
+struct Bf16Tiles<MAT_GATED> {
+    static constexpr Bf16Tile T[] = {
+        {32, 32, 0.125f, 0.099f, 1.16f, 2.01f},   {64, 32, 0.186f, 0.158f, 1.04f, 2.20f},   {64, 64, 0.125f, 0.230f, 0.73f, 2.51f},
+        {64, 64, 0.267f, 0.207f, 2.30f, 0.63f},   {128, 64, 0.370f, 0.308f, 1.98f, 1.60f},  {128, 128, 0.462f, 0.469f, 0.00f, 4.28f},
+        {128, 192, 0.483f, 0.566f, 0.00f, 5.81f}, {192, 192, 0.544f, 0.733f, 0.00f, 8.11f}, {256, 192, 1.063f, 1.025f, 0.00f, 6.96f},
+    };
+};
+template <>
+struct Bf16Tiles<MAT_NN> {
+    static constexpr Bf16Tile T[] = {
+        {32, 32, 0.102f, 0.143f, 1.29f, 1.53f},   {64, 32, 0.182f, 0.175f, 0.96f, 1.96f},   {64, 64, 0.183f, 0.223f, 0.62f, 2.44f},
+        {64, 64, 0.268f, 0.220f, 2.22f, 0.50f},   {128, 64, 0.348f, 0.304f, 2.08f, 1.04f},  {128, 128, 0.450f, 0.485f, 0.03f, 3.67f},
+        {128, 192, 0.574f, 0.606f, 0.00f, 4.12f}, {192, 192, 0.777f, 0.808f, 0.00f, 4.64f}, {256, 192, 0.956f, 0.956f, 0.01f, 4.39f},
+        {256, 256, 1.077f, 1.144f, 0.00f, 5.29f},
+    };
+};
+template <>
+struct Bf16Tiles<MAT_TN> {
+    static constexpr Bf16Tile T[] = {
+        {32, 32, 0.120f, 0.163f, 1.46f, 1.46f},   {64, 32, 0.041f, 0.193f, 1.25f, 1.86f},   {64, 64, 0.198f, 0.238f, 1.31f, 1.75f},
+        {64, 64, 0.262f, 0.220f, 2.35f, 0.46f},   {128, 64, 0.191f, 0.338f, 2.51f, 0.66f},  {128, 128, 0.531f, 0.534f, 0.25f, 3.01f},
+        {128, 192, 0.533f, 0.638f, 0.00f, 3.78f}, {192, 192, 0.810f, 0.823f, 0.00f, 4.19f}, {256, 192, 0.950f, 0.959f, 0.00f, 4.71f},
+        {256, 256, 1.269f, 1.270f, 0.00f, 5.36f},
+    };
+};
 
-static int pick_bf16_tile(const Bf16Tile* tiles, int64_t T, int64_t rows, int K) {
-    int best = N_BF16_TILES - 1;
+static float bf16_tile_us(const Bf16Tile& c, int64_t T, int64_t rows, int K) {
+    const int64_t W = ((rows + c.bn - 1) / c.bn) * ((T + c.bt - 1) / c.bt);
+    if (W >= (1 << 22)) return 1e30f;   // keeps every launch below 2^32 threads
+    const float steps = static_cast<float>((K + 63) / 64);
+    const float alone = steps * c.alone + c.end, turns = static_cast<float>((W + 255) / 256) * (steps * c.full + c.end);
+    return c.fixed + (alone > turns ? alone : turns);
+}
+
+template <int KIND, bool AD>
+static int pick_bf16_tile(int64_t T, int64_t rows, int K) {
+    // (256 x 256 with adapters does not fit the registers either)
+    constexpr int n = KIND == MAT_NT && AD ? 9 : sizeof(Bf16Tiles<KIND>::T) / sizeof(Bf16Tile);
+    int best = n - 1;
     float best_us = 1e30f;
-    for (int i = 0; i < N_BF16_TILES; ++i) {
-        const Bf16Tile& c = tiles[i];
-        const int64_t W = ((rows + c.bn - 1) / c.bn) * ((T + c.bt - 1) / c.bt);
-        if (W >= (1 << 22)) continue;   // keeps every launch below 2^32 threads
-        const float turns = static_cast<float>((W + 255) / 256) * c.full;
-        const float us = static_cast<float>((K + 63) / 64) * (turns > c.alone ? turns : c.alone) + c.fixed;
+    for (int i = 0; i < n; ++i) {
+        const float us = bf16_tile_us(Bf16Tiles<KIND>::T[i], T, rows, K);
         if (us < best_us) {
             best_us = us;
             best = i;
@@ -481,25 +588,20 @@ static int pick_bf16_tile(const Bf16Tile* tiles, int64_t T, int64_t rows, int K)
 }
 
 template <int KIND, bool AD>
-static hipError_t bf16_tiles(const Bf16Tile* tiles, const MatBf16Params& p, hipStream_t s) {
-    switch (pick_bf16_tile(tiles, p.T, static_cast<int64_t>(p.N) * (KIND == MAT_GATED ? 2 : 1), p.K)) {
+static hipError_t bf16_tiles(const MatBf16Params& p, hipStream_t s) {
+    switch (pick_bf16_tile<KIND, AD>(p.T, static_cast<int64_t>(p.N) * (KIND == MAT_GATED ? 2 : 1), p.K)) {
         case 0: return bf16_tile<KIND, AD, 32, 32, 1, 1, 3, 4>(p, s);
-        case 1: return bf16_tile<KIND, AD, 32, 64, 1, 2, 3, 4>(p, s);
+        case 1: return bf16_tile<KIND, AD, 64, 32, 2, 1, 3, 4>(p, s);
         case 2: return bf16_tile<KIND, AD, 64, 64, 2, 2, 4, 2>(p, s);
         case 3: return bf16_tile<KIND, AD, 64, 64, 2, 2, 3, 1>(p, s);
         case 4: return bf16_tile<KIND, AD, 128, 64, 2, 2, 3, 1>(p, s);
         case 5: return bf16_tile<KIND, AD, 128, 128, 2, 4, 4, 1>(p, s);
-        case 6: return bf16_tile<KIND, AD, 192, 128, 2, 4, 3, 1>(p, s);
-        case 7: return bf16_tile<KIND, AD, 256, 128, 4, 2, 3, 1>(p, s);
+        case 6: return bf16_tile<KIND, AD, 128, 192, 2, 4, 3, 1>(p, s);
+        case 7: return bf16_tile<KIND, AD, 192, 192, 2, 4, 3, 1>(p, s);
         case 8: return bf16_tile<KIND, AD, 256, 192, 4, 2, 2, 1>(p, s);
-        default: return bf16_tile<KIND, AD, 256, 256, 4, 2, 2, 1>(p, s);
     }
+    if constexpr (KIND != MAT_GATED && !AD) return bf16_tile<KIND, AD, 256, 256, 4, 2, 2, 1>(p, s);
+    return hipErrorInvalidValue;   // not reached
 }
-
-constexpr Bf16Tile BF16_TILES[N_BF16_TILES] = {
-    {32, 32, 0.12f, 0.12f, 1.3f},   {32, 64, 0.14f, 0.14f, 1.7f},   {64, 64, 0.18f, 0.18f, 1.9f},   {64, 64, 0.32f, 0.20f, 0.2f},
-    {128, 64, 0.32f, 0.32f, 1.2f},  {128, 128, 0.52f, 0.52f, 0.4f}, {192, 128, 0.66f, 0.66f, 0.7f}, {256, 128, 0.79f, 0.79f, 1.1f},
-    {256, 192, 1.08f, 1.08f, 1.1f}, {256, 256, 1.32f, 1.32f, 0.3f},
-};
 
 }  // namespace moe
