@@ -2,108 +2,59 @@
 //
 //   s[t] = scale[a] (x[t] A[a]^T)      a = ids[t]; zeros where there is none
 //
-// MFMA 16x16x32, A = ranks, B = tokens, operands straight from memory: lane l holds row
-// l & 15, k 8 (l >> 4) .. of a step.  D columns are tokens, and each adapter's sums are
-// stored for its own tokens only, so nothing of one request meets another's.
-#include "block.h"
-#include "common.h"
+// A workgroup takes 16 TT tokens, 16 RB ranks of one half (y), and every gridDim.z-th of
+// the adapters that occur among its tokens.  Its KG waves take the K steps of 64 in turn,
+// each with a ring of NSTG stages of its own, filled by LDS DMA: 8 rows of 128 bytes a
+// copy.  (Fragments straight from memory touch 16 lines an instruction, for which the
+// address unit takes about 80 cycles: 9.5 us for 14 adapters of 2 x 16 ranks, K = 2816.)
+// Tokens of other adapters are not read.  MFMA 16x16x32, A = ranks, B = tokens: D columns
+// are tokens, and each adapter's sums are stored for its own tokens only, so nothing of
+// one request meets another's.
+#include <algorithm>
+
+#include "bf16_tile.h"
 
 namespace moe {
 
-// zeros for the tokens of a block that have no adapter: ranks r0 .. r0 + 8 * chunks of half h
-__device__ __forceinline__ void clear_others(const AdapterShrinkParams& p, int t0, int tokens, int h, int r0, int chunks, int threads) {
-    for (int i = threadIdx.x; i < tokens * chunks; i += threads) {
-        const int t = t0 + i / chunks, r = r0 + i % chunks * 8;
-        if (t >= p.T || r >= p.R) continue;
-        const int a = p.ids[t];
-        if (a < 0 || a >= p.n) *reinterpret_cast<u32x4*>(p.s + t * p.lds + h * p.R + r) = u32x4{0, 0, 0, 0};
-    }
-}
-
-// Few tokens: a workgroup for each token (y) of a block of 16 and each 16 ranks (z),
-// which ends if an earlier token of the block has the same adapter.  Its KG waves share K
-// in steps of 32, and each requests U steps at once: the time is that of the chain ids,
-// operands, sums.  x does not wait for the ids, nor the first 16 ranks for the rank.
-template <int KG, int U>
-__global__ __launch_bounds__(64 * KG) void adapter_shrink_few_kernel(AdapterShrinkParams p) {
-    __shared__ __attribute__((aligned(16))) f32x4 part[KG][64];
-    const int tid = threadIdx.x, lane = tid & 63, kg = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row = lane & 15, q = lane >> 4;
-    const int t0 = blockIdx.x * 16, me = blockIdx.y;
-    const int rblocks = (p.R + 15) / 16;   // of a half
-    const int h = blockIdx.z / rblocks, r0 = blockIdx.z % rblocks * 16;
-    const int id = t0 + row < p.T ? p.ids[t0 + row] : -1;
-    u32x4 vb[U];
-    auto tokens = [&](int k0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = k0 + 32 * KG * u + 8 * q;
-            vb[u] = u32x4{0, 0, 0, 0};
-            if (t0 + row < p.T && k < p.K) vb[u] = *reinterpret_cast<const u32x4*>(p.x + (t0 + row) * p.ldx + k);
-        }
-    };
-    tokens(32 * kg);
-    if (me == 0) clear_others(p, t0, 16, h, r0, 2, 64 * KG);
-    const int a = __builtin_amdgcn_readlane(id, me);
-    if (t0 + me >= p.T || a < 0 || a >= p.n) return;
-    const uint64_t same = __ballot(id == a) & 0xFFFF;
-    if (__builtin_ctzll(same) != me) return;
-    int rank = p.R;
-    if (p.ranks != nullptr) rank = min(p.ranks[a], p.R);
-    const uint16_t* pa = p.a + a * p.a_stride + (static_cast<int64_t>(h) * p.R + r0 + row) * p.K;
-    f32x4 acc = {0, 0, 0, 0};
-    if (r0 == 0 || r0 < rank)
-        for (int k0 = 32 * kg;;) {
-            u32x4 va[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = k0 + 32 * KG * u + 8 * q;
-                va[u] = u32x4{0, 0, 0, 0};
-                if (r0 + row < p.R && k < p.K) va[u] = *reinterpret_cast<const u32x4*>(pa + k);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) acc = mfma16x16x32(va[u], vb[u], acc);
-            k0 += 32 * KG * U;
-            if (k0 >= p.K) break;
-            tokens(k0);
-        }
-    part[kg][lane] = acc;
-    __syncthreads();
-    if (tid >= 64) return;
-    f32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int g = 0; g < KG; ++g) v += part[g][lane];
-    const int r = r0 + 4 * q;   // 4 ranks of one token
-    if (id != a || r >= p.R) return;
-    const float scale = p.scale ? p.scale[a] : 1.0f;
-    float o[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = r + e < rank ? scale * v[e] : 0.0f;
-    *reinterpret_cast<u32x2*>(p.s + (t0 + row) * p.lds + h * p.R + r) = u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
-}
-
-// Many tokens: a workgroup takes 16 TT tokens, 16 RB ranks, and the adapters of these
-// tokens one after the other (gridDim.y workgroups share them); its waves share K in
-// steps of 64.
-template <int TT, int RB, int KG>
+template <int TT, int RB, int KG, int NSTG>
 __global__ __launch_bounds__(64 * KG) void adapter_shrink_kernel(AdapterShrinkParams p) {
-    __shared__ __attribute__((aligned(16))) float part[KG][RB][TT][256];
+    constexpr int BT = 16 * TT, BR = 16 * RB, BK = 64, STAGE = (BT + BR) * 128, CA = 2 * RB, CX = 2 * TT, CPS = CA + CX;
+    static_assert(NSTG >= 2 && NSTG <= 3 && CPS * (NSTG - 1) <= 63 && RB * TT * 1024 <= NSTG * STAGE, "copies in flight, sums in the ring");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * NSTG * STAGE];
+    __shared__ int idl[BT];
     const int tid = threadIdx.x, lane = tid & 63, kg = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row = lane & 15, q = lane >> 4;
-    const int t0 = blockIdx.x * 16 * TT;
-    const int rblocks = (p.R + 16 * RB - 1) / (16 * RB);   // of a half
-    const int h = blockIdx.z / rblocks, r0 = blockIdx.z % rblocks * 16 * RB;
-    int aid[TT];
+    const int l16 = lane & 15, q = lane >> 4;
+    const int t0 = blockIdx.x * BT;
+    const int rblocks = (p.R + BR - 1) / BR;   // of a half
+    const int h = blockIdx.y / rblocks, r0 = blockIdx.y % rblocks * BR;
+    const int rows = min(BT, p.T - t0), ranks = min(BR, p.R - r0);
+    auto id_of = [&](int t) {   // -1: none
+        const int a = p.ids[t0 + min(t, rows - 1)];
+        return t < rows && a >= 0 && a < p.n ? a : -1;
+    };
+    int aid[TT], idc[CX];   // of the tokens that this lane computes, and of those it copies
+#pragma unroll
+    for (int j = 0; j < TT; ++j) aid[j] = id_of(16 * j + l16);
+#pragma unroll
+    for (int i = 0; i < CX; ++i) idc[i] = id_of(8 * i + lane / 8);
+    const rsrc_t xr = make_rsrc(p.x + t0 * p.ldx, static_cast<uint32_t>(((rows - 1) * p.ldx + p.K) * 2));
+    uint8_t* ring = lds + kg * NSTG * STAGE;
+    const uint32_t kb = 2u * p.K;
+    uint32_t chunk[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) chunk[i] = ((lane % 8) ^ swz_row(8 * i + lane / 8)) * 16;
+    const int nk = ((p.K + BK - 1) / BK + KG - 1) / KG;
     uint64_t left[TT];
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-        const int t = t0 + 16 * j + row;
-        const int a = t < p.T ? p.ids[t] : -1;
-        aid[j] = a >= 0 && a < p.n ? a : -1;
-        left[j] = __ballot(aid[j] >= 0);
-    }
-    if (blockIdx.y == 0) clear_others(p, t0, 16 * TT, h, r0, 2 * RB, 64 * KG);
-    for (unsigned unit = 0;; ++unit) {
+    for (int j = 0; j < TT; ++j) left[j] = __ballot(aid[j] >= 0);
+    if (tid < BT) idl[tid] = id_of(tid);
+    if (blockIdx.z == 0)   // tokens without an adapter
+        for (int i = tid; i < BT * 2 * RB; i += 64 * KG) {
+            const int t = i / (2 * RB), r = i % (2 * RB) * 8;
+            if (t < rows && r < ranks && id_of(t) < 0)
+                *reinterpret_cast<u32x4*>(p.s + (t0 + t) * p.lds + h * p.R + r0 + r) = u32x4{0, 0, 0, 0};
+        }
+    for (unsigned skip = blockIdx.z;;) {   // adapters of other workgroups before the next one of this
         int a = -1;
 #pragma unroll
         for (int j = TT - 1; j >= 0; --j)
@@ -111,69 +62,112 @@ __global__ __launch_bounds__(64 * KG) void adapter_shrink_kernel(AdapterShrinkPa
         if (a < 0) return;
 #pragma unroll
         for (int j = 0; j < TT; ++j) left[j] &= ~__ballot(aid[j] == a);
-        if (unit % gridDim.y != blockIdx.y) continue;
-        const int rank = p.ranks ? min(p.ranks[a], p.R) : p.R;
-        const uint16_t* pa = p.a + a * p.a_stride + static_cast<int64_t>(h) * p.R * p.K;
-        f32x4 acc[RB][TT] = {};
-        if (r0 < rank) {
-#pragma unroll 2
-            for (int k0 = 64 * kg; k0 < p.K; k0 += 64 * KG) {
-                u32x4 va[2][RB], vb[2][TT];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int k = k0 + 32 * s + 8 * q;
-#pragma unroll
-                    for (int i = 0; i < RB; ++i) {
-                        const int r = r0 + 16 * i + row;
-                        va[s][i] = u32x4{0, 0, 0, 0};
-                        if (r < rank && k < p.K) va[s][i] = *reinterpret_cast<const u32x4*>(pa + static_cast<int64_t>(r) * p.K + k);
-                    }
-#pragma unroll
-                    for (int j = 0; j < TT; ++j) {
-                        vb[s][j] = u32x4{0, 0, 0, 0};
-                        if (aid[j] == a && k < p.K)
-                            vb[s][j] = *reinterpret_cast<const u32x4*>(p.x + (t0 + 16 * j + row) * p.ldx + k);
-                    }
-                }
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int i = 0; i < RB; ++i)
-#pragma unroll
-                        for (int j = 0; j < TT; ++j) acc[i][j] = mfma16x16x32(va[s][i], vb[s][j], acc[i][j]);
-            }
+        if (skip > 0) {
+            --skip;
+            continue;
         }
+        skip = gridDim.z - 1;
+        const rsrc_t ar = make_rsrc(p.a + a * p.a_stride + (static_cast<int64_t>(h) * p.R + r0) * p.K, static_cast<uint32_t>(ranks) * kb);
+        uint32_t ao[CA], xo[CX];
+#pragma unroll
+        for (int i = 0; i < CA; ++i) {
+            const int row = 8 * i + lane / 8;
+            ao[i] = row < ranks ? row * kb + chunk[i & 1] : NO_LANE;
+        }
+#pragma unroll
+        for (int i = 0; i < CX; ++i)
+            xo[i] = idc[i] == a ? static_cast<uint32_t>((8 * i + lane / 8) * p.ldx * 2 + chunk[i & 1]) : NO_LANE;
+        // what lies past K is zeros; stages past the last are not requested
+        auto copy = [&](int c, uint8_t* st) __attribute__((always_inline)) {
+            const uint32_t k = 2 * BK * (c * KG + kg);
+            const uint32_t so = k < kb ? k : 0;   // inside the resource
+#pragma unroll
+            for (int i = 0; i < CPS; ++i) {
+                const bool in = k + chunk[i & 1] < kb;
+                if (i < CA)
+                    lds_dma16(ar, st + i * 1024, in ? ao[i] : NO_LANE, so);
+                else
+                    lds_dma16(xr, st + i * 1024, in ? xo[i - CA] : NO_LANE, so);
+            }
+        };
+        const int rank = p.ranks != nullptr ? min(p.ranks[a], p.R) : p.R;
+        const float scale = p.scale != nullptr ? p.scale[a] : 1.0f;
+#pragma unroll
+        for (int c = 0; c < NSTG; ++c)
+            if (c < nk) copy(c, ring + c * STAGE);
+        f32x4 acc[RB][TT] = {};
+        for (int c = 0, buf = 0; c < nk; ++c) {
+            const int behind = min(nk - 1 - c, NSTG - 1);   // the stages behind this one may still be on their way
+            if (NSTG > 2 && behind == 2)
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * CPS));
+            else if (behind == 1)
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm(CPS));
+            else
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+            asm volatile("" ::: "memory");
+            uint8_t* st = ring + buf * STAGE;
+            u32x4 va[2][RB], vb[2][TT];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int o = l16 * 128 + (((4 * s + q) ^ swz_row(l16)) << 4);
+#pragma unroll
+                for (int i = 0; i < RB; ++i) va[s][i] = *reinterpret_cast<const u32x4*>(st + i * 2048 + o);
+#pragma unroll
+                for (int j = 0; j < TT; ++j) vb[s][j] = *reinterpret_cast<const u32x4*>(st + (RB + j) * 2048 + o);
+            }
+            __builtin_amdgcn_s_waitcnt(wait_vm_lds(63));   // the operands are read, so the buffer may be filled again
+            asm volatile("" ::: "memory");
+            if (c + NSTG < nk) copy(c + NSTG, st);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+#pragma unroll
+                    for (int j = 0; j < TT; ++j) acc[i][j] = mfma16x16x32(va[s][i], vb[s][j], acc[i][j]);
+            buf = buf + 1 == NSTG ? 0 : buf + 1;
+        }
+        // the sums of a wave go to its own ring, where nothing is under way any more
 #pragma unroll
         for (int i = 0; i < RB; ++i)
 #pragma unroll
-            for (int j = 0; j < TT; ++j) *reinterpret_cast<f32x4*>(&part[kg][i][j][lane * 4]) = acc[i][j];
+            for (int j = 0; j < TT; ++j) *reinterpret_cast<f32x4*>(ring + (i * TT + j) * 1024 + lane * 16) = acc[i][j];
         __syncthreads();
-        const float scale = p.scale ? p.scale[a] : 1.0f;
         for (int i = tid; i < RB * TT * 64; i += 64 * KG) {   // 4 ranks of one token
-            const int l = i & 63, j = (i >> 6) % TT, b = (i >> 6) / TT;
-            const int t = t0 + 16 * j + (l & 15), r = r0 + 16 * b + 4 * (l >> 4);
-            if (t >= p.T || r >= p.R || p.ids[t] != a) continue;
+            const int l = i & 63, b = i >> 6;
+            const int t = 16 * (b % TT) + (l & 15), r = 16 * (b / TT) + 4 * (l >> 4);
+            if (idl[t] != a || r >= ranks) continue;
             f32x4 v = {0, 0, 0, 0};
 #pragma unroll
-            for (int g = 0; g < KG; ++g) v += *reinterpret_cast<const f32x4*>(&part[g][b][j][l * 4]);
+            for (int g = 0; g < KG; ++g) v += *reinterpret_cast<const f32x4*>(lds + g * NSTG * STAGE + b * 1024 + l * 16);
             float o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = r + e < rank ? scale * v[e] : 0.0f;
-            *reinterpret_cast<u32x2*>(p.s + t * p.lds + h * p.R + r) = u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+            for (int e = 0; e < 4; ++e) o[e] = r0 + r + e < rank ? scale * v[e] : 0.0f;
+            *reinterpret_cast<u32x2*>(p.s + (t0 + t) * p.lds + h * p.R + r0 + r) = u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
         }
-        __syncthreads();
+        __syncthreads();   // the sums are read
     }
 }
 
-hipError_t launch_adapter_shrink(const AdapterShrinkParams& p, hipStream_t s) {
-    if (p.T <= 64) {
-        hipLaunchKernelGGL((adapter_shrink_few_kernel<16, 8>), dim3((p.T + 15) / 16, p.T < 16 ? p.T : 16, (p.R + 15) / 16 * p.halves),
-                           dim3(1024), 0, s, p);
-    } else {
-        const int blocks = (p.T + 31) / 32;
-        hipLaunchKernelGGL((adapter_shrink_kernel<2, 4, 8>), dim3(blocks, 4, (p.R + 63) / 64 * p.halves), dim3(512), 0, s, p);
-    }
+constexpr int SHRINK_KG = 8, SHRINK_NSTG = 2;
+
+// `most`: the workgroups that the CUs hold at once share the adapters of a block
+template <int TT, int RB>
+static hipError_t shrink(const AdapterShrinkParams& p, int most, hipStream_t s) {
+    const int blocks = (p.T + 16 * TT - 1) / (16 * TT), ranks = (p.R + 16 * RB - 1) / (16 * RB) * p.halves;
+    const int share = std::max<int64_t>(1, std::min<int64_t>(std::min(p.T, 16 * TT), most / (static_cast<int64_t>(blocks) * ranks)));
+    hipLaunchKernelGGL((adapter_shrink_kernel<TT, RB, SHRINK_KG, SHRINK_NSTG>), dim3(blocks, ranks, share), dim3(64 * SHRINK_KG), 0, s, p);
     return hipGetLastError();
+}
+
+// The smallest blocks while they leave CUs idle, larger ones (fewer reads of the same
+// rows) behind that.  Runs of 150 tokens, K = 2816: 512 x 64 ranks 16 x 16 5.3 us, 32 x 32
+// 7.3; 1024 x 2 x 32 ranks 16 x 16 8.6, 32 x 16 6.4, 32 x 32 7.5; 2048 x 2 x 32 ranks 13.3,
+// 10.7, 9.4.  16 waves took 0 to 20 % longer than 8, three stages 0 to 10 %.
+hipError_t launch_adapter_shrink(const AdapterShrinkParams& p, hipStream_t s) {
+    const int64_t small = static_cast<int64_t>((p.T + 15) / 16) * ((p.R + 15) / 16) * p.halves;
+    if (small < 256) return shrink<1, 1>(p, 512, s);
+    if (small < 512) return shrink<2, 1>(p, 256, s);
+    return shrink<2, 2>(p, 256, s);
 }
 
 }  // namespace moe

@@ -13,9 +13,11 @@ __device__ __forceinline__ int swz16(int r) { return (r & 15) >> 1; }
 template <int TT, int KG, int NSTG, bool GATED, bool AD>
 __global__ __launch_bounds__(64 * KG) void matmul_bf16_few_kernel(MatBf16Params p) {
     constexpr int BK = 64, STAGE = (16 + 16 * TT) * 128, CH = GATED ? 8 : 16, CPS = 2 + 2 * TT;
-    static_assert(KG >= 4 && NSTG <= 4 && CPS * (NSTG - 1) <= 63, "256 threads for the results, copies in flight");
+    static_assert(KG >= 4 && NSTG >= 2 && NSTG <= 3, "256 threads for the results, copies in flight");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * NSTG * STAGE];
     __shared__ __attribute__((aligned(16))) float part[KG][TT][256];
+    __shared__ __attribute__((aligned(16))) int ids_of[AD ? KG : 1][64];
+    __shared__ uint64_t lists[AD ? KG : 1][64];
     const int tid = threadIdx.x, lane = tid & 63, kg = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n0 = blockIdx.x * CH, nch = min(CH, p.N - n0);
     const uint32_t kb = 2u * p.K;
@@ -54,91 +56,84 @@ __global__ __launch_bounds__(64 * KG) void matmul_bf16_few_kernel(MatBf16Params 
         }
     };
     const int row = lane & 15, q = lane >> 4;
-    int aid[TT], rk[TT];   // the adapters of this lane's tokens, and their ranks
-    if (AD) {
-#pragma unroll
-        for (int j = 0; j < TT; ++j) aid[j] = row + 16 * j < p.T ? p.ad.ids[row + 16 * j] : -1;
-    }
+    int id_l = -1;   // of token `lane`
+    if (AD) id_l = p.ad.ids[min(lane, p.T - 1)];
 #pragma unroll
     for (int c = 0; c < NSTG; ++c)
         if (c < nk) copy(c, ring + c * STAGE);
-    // The low-rank part in items of one adapter and 32 ranks, which the waves take in
-    // turn; an adapter that several tokens have is taken once.  The operands are read
-    // straight from memory, those of a wave's first NI items here, behind the first copies.
-    // Each item's product is taken from zero and added in the lanes of its own tokens
-    // only, so that no value of one adapter, an infinity or NaN included, meets
-    // another request's row.
-    constexpr int NI = TT == 1 ? 4 : 2, H = GATED ? 2 : 1;
-    uint64_t left[TT];
-    int item_a = -1, item_k = 0, ia[NI], ik[NI];
-    u32x4 va[NI], vb[NI][TT][H];
-    auto advance = [&]() __attribute__((always_inline)) {   // to the next item; item_a < 0: there is none
-        if (item_a >= 0 && item_k + 32 < p.ad.R) {
-            item_k += 32;
-            return;
-        }
-        item_a = -1;
-        item_k = 0;
+    // The low-rank part, 32 ranks at a time: the tokens' s, and NI adapters' rows at once,
+    // straight from memory; the waves take the adapters in turn, one that several tokens
+    // have once.  The first ones are requested here, behind the first copies.  Each
+    // adapter's product is taken from zero and added in the lanes of its own tokens only,
+    // so that no value of one adapter, an infinity or NaN included, meets another
+    // request's row.
+    constexpr int H = GATED ? 2 : 1, NI = 8, LOADS = H * (TT + NI);
+    static_assert(CPS * (NSTG - 1) + LOADS <= 63, "loads in flight");
+    int rank_l = p.ad.R, aid[TT];              // the token's rank; the adapters of this lane's columns
+    int count = 0, at = 0, ia[NI], k0 = 0;     // adapters with these ranks, the wave's next; the first rank
+    bool leader = false;
+    u32x4 va[NI][H], vb[TT][H];
+    const rsrc_t sr = AD ? make_rsrc(p.ad.s, static_cast<uint32_t>(((p.T - 1) * p.ad.lds + H * p.ad.R) * 2)) : rsrc_t();
+    auto tokens = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = TT - 1; j >= 0; --j)
-            if (left[j]) item_a = __builtin_amdgcn_readlane(aid[j], __builtin_ctzll(left[j]));
-        if (item_a < 0) return;
+        for (int j = 0; j < TT; ++j)
 #pragma unroll
-        for (int j = 0; j < TT; ++j) left[j] &= ~__ballot(aid[j] == item_a);
+            for (int h = 0; h < H; ++h)
+                vb[j][h] = bload16(sr, aid[j] >= 0 && k0 + 8 * q < p.ad.R
+                                           ? static_cast<uint32_t>((row + 16 * j) * p.ad.lds + h * p.ad.R + k0 + 8 * q) * 2 : NO_LANE);
+        at = kg;
     };
-    auto items = [&]() __attribute__((always_inline)) {   // the operands of the next NI items of this wave
+    auto adapters = [&]() __attribute__((always_inline)) {   // the next NI of this wave
+        const int ch = GATED ? row & 7 : row;
+        const uint32_t bytes = static_cast<uint32_t>(nch) * p.ad.R * 2u;
+        const uint32_t off = ch < nch && k0 + 8 * q < p.ad.R ? static_cast<uint32_t>(ch * p.ad.R + k0 + 8 * q) * 2 : NO_LANE;
+        uint64_t of[NI];
+#pragma unroll
+        for (int n = 0; n < NI; ++n) of[n] = lists[kg][min(at + n * KG, 63)];
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
-            ia[n] = item_a;
-            ik[n] = item_k;
-            va[n] = u32x4{0, 0, 0, 0};
+            const bool in = at + n * KG < count;
+            ia[n] = in ? __builtin_amdgcn_readfirstlane(static_cast<int>(of[n])) : -1;
+            const uint16_t* pb = p.ad.b + max(ia[n], 0) * p.ad.b_stride + static_cast<int64_t>(n0) * p.ad.R;
 #pragma unroll
-            for (int j = 0; j < TT; ++j)
-#pragma unroll
-                for (int h = 0; h < H; ++h) vb[n][j][h] = u32x4{0, 0, 0, 0};
-            const int k = item_k + 8 * q, ch = GATED ? row & 7 : row;
-            if (item_a >= 0 && k < p.ad.R) {
-                if (ch < nch)
-                    va[n] = *reinterpret_cast<const u32x4*>(p.ad.b + item_a * p.ad.b_stride +
-                                                            (static_cast<int64_t>(GATED ? row >> 3 : 0) * p.N + n0 + ch) * p.ad.R + k);
-#pragma unroll
-                for (int j = 0; j < TT; ++j)
-#pragma unroll
-                    for (int h = 0; h < H; ++h)
-                        if (aid[j] == item_a)
-                            vb[n][j][h] = *reinterpret_cast<const u32x4*>(p.ad.s + (row + 16 * j) * p.ad.lds + h * p.ad.R + k);
-            }
-#pragma unroll
-            for (int g = 0; g < KG; ++g)
-                if (item_a >= 0) advance();
+            for (int h = 0; h < H; ++h)   // gate's rows and up's, the lanes of the other half zeros
+                va[n][h] = bload16(make_rsrc(pb + static_cast<int64_t>(h) * p.N * p.ad.R, bytes),
+                                   in && (!GATED || (row >> 3) == h) ? off : NO_LANE);
         }
+        at += NI * KG;
     };
     if (AD) {
+        if (lane >= p.T || id_l < 0 || id_l >= p.ad.n) id_l = -1;
+        leader = is_leader(id_l, 16 * TT, ids_of[kg]);
 #pragma unroll
-        for (int j = 0; j < TT; ++j) {
-            if (aid[j] >= p.ad.n) aid[j] = -1;
-            left[j] = __ballot(aid[j] >= 0);
-            rk[j] = p.ad.R;
-            if (p.ad.ranks != nullptr && aid[j] >= 0) rk[j] = p.ad.ranks[aid[j]];
-        }
-        advance();
-#pragma unroll
-        for (int g = 0; g < KG; ++g)
-            if (g < kg && item_a >= 0) advance();
-        items();
+        for (int j = 0; j < TT; ++j) aid[j] = ids_of[kg][16 * j + row];
+        if (p.ad.ranks != nullptr) rank_l = p.ad.ranks[max(id_l, 0)];
+        count = list_adapters(leader, id_l, 1, 0, lists[kg]);   // all: their ranks are not waited for here
+        tokens();
+        adapters();
+        // the waits below count these loads: they stay in front of them
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     }
     f32x4 acc[TT] = {};
     for (int c = 0, buf = 0; c < nk; ++c) {
-        // the stages behind this one may still be on their way
+        // the stages behind this one, and behind the first ones the items, may still be on
+        // their way
         const int behind = min(nk - 1 - c, NSTG - 1);
-        if (NSTG > 3 && behind == 3)
-            __builtin_amdgcn_s_waitcnt(waitcnt_vm(3 * CPS));
-        else if (NSTG > 2 && behind == 2)
+        if (AD && c < NSTG) {
+            if (NSTG > 2 && behind == 2)
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * CPS + LOADS));
+            else if (behind == 1)
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm(CPS + LOADS));
+            else
+                __builtin_amdgcn_s_waitcnt(waitcnt_vm(LOADS));
+        } else if (NSTG > 2 && behind == 2) {
             __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * CPS));
-        else if (behind == 1)
+        } else if (behind == 1) {
             __builtin_amdgcn_s_waitcnt(waitcnt_vm(CPS));
-        else
+        } else {
             __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        }
         asm volatile("" ::: "memory");
         uint8_t* st = ring + buf * STAGE;
         u32x4 a[2], b[2][TT];
@@ -163,31 +158,26 @@ __global__ __launch_bounds__(64 * KG) void matmul_bf16_few_kernel(MatBf16Params 
 #pragma unroll
             for (int n = 0; n < NI; ++n) {
                 if (ia[n] < 0) continue;
-                int rank = 0;
+                const int rank = __builtin_amdgcn_readlane(rank_l, __builtin_ctzll(__ballot(id_l == ia[n])));
+                if (rank < k0 + 32) {   // some lane holds less than 8 ranks
 #pragma unroll
-                for (int j = 0; j < TT; ++j) {
-                    const uint64_t same = __ballot(aid[j] == ia[n]);
-                    if (same) rank = __builtin_amdgcn_readlane(rk[j], __builtin_ctzll(same));
-                }
-                const u32x4 v = low_ranks(va[n], rank - ik[n] - 8 * q);
-                u32x4 half[H];
-                if (GATED) {
-                    const u32x4 none = {0, 0, 0, 0};
-                    half[0] = row < 8 ? v : none;
-                    half[H - 1] = row < 8 ? none : v;
-                } else {
-                    half[0] = v;
+                    for (int h = 0; h < H; ++h) va[n][h] = low_ranks(va[n][h], rank - k0 - 8 * q);
                 }
 #pragma unroll
                 for (int j = 0; j < TT; ++j) {
                     f32x4 low = {};
 #pragma unroll
-                    for (int h = 0; h < H; ++h) low = mfma16x16x32(half[h], vb[n][j][h], low);
+                    for (int h = 0; h < H; ++h) low = mfma16x16x32(va[n][h], vb[j][h], low);
                     if (aid[j] == ia[n]) acc[j] += low;
                 }
             }
-            if (item_a < 0) break;
-            items();
+            if (at >= count) {   // the next 32 ranks, of the adapters that have them
+                k0 += 32;
+                if (k0 >= p.ad.R) break;
+                count = list_adapters(leader, id_l, rank_l, k0, lists[kg]);
+                tokens();
+            }
+            adapters();
         }
     }
     // lane l: token l & 15 of tile j, tile rows 4 (l >> 4) ..

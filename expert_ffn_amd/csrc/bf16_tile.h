@@ -49,12 +49,30 @@ __device__ __forceinline__ u32x4 low_ranks(const u32x4& v, int n) {
     return r;
 }
 
-// no infinity or NaN among 8 bf16 values
-__device__ __forceinline__ bool all_finite(const u32x4& v) {
-    bool ok = true;
+// The adapters that occur among up to 64 tokens, lane t's id (-1: none), once each: the
+// first token of an adapter is its leader.  ids: 64 words of LDS of this wave's own.
+__device__ __forceinline__ bool is_leader(int id, int count, int* ids) {
+    const int lane = threadIdx.x & 63;
+    ids[lane] = id;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    int first = 64;
+    for (int t = (count + 3) / 4 * 4 - 4; t >= 0; t -= 4) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(ids + t);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ok = ok && (v[i] & 0x7F80u) != 0x7F80u && (v[i] & 0x7F800000u) != 0x7F800000u;
-    return ok;
+        for (int e = 3; e >= 0; --e) first = static_cast<int>(v[e]) == id ? t + e : first;
+    }
+    return id >= 0 && first == lane;
+}
+// their ids and ranks, those with more than `past` ranks, into list (64 pairs of words of LDS); how many
+__device__ __forceinline__ int list_adapters(bool leader, int id, int rank, int past, uint64_t* list) {
+    const uint64_t m = __ballot(leader && rank > past);
+    if (leader && rank > past)
+        list[__builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(m), 0))] =
+            static_cast<uint64_t>(static_cast<uint32_t>(rank)) << 32 | static_cast<uint32_t>(id);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    return __builtin_popcountll(m);
 }
 
 __host__ __device__ constexpr int wait_vm_lds(int n) { return waitcnt_vm(n) & ~0x0F00; }   // and LDS reads to 0
@@ -104,6 +122,9 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
     static_assert(NSTG >= 2 && NSTG <= 4 && CPS * (NSTG - 1) <= 63, "copies in flight");
     static_assert((KG - 1) * BN * BT * 4 <= KG * RING, "epilogue regions");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * RING];
+    __shared__ __attribute__((aligned(16))) int ids_of[AD ? NW * KG : 1][64];
+    __shared__ uint64_t lists[AD ? NW * KG : 1][64];
+    static_assert(!AD || BT / WT <= 64, "tokens of a wave");
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kg = wid / NW, wave = wid % NW, wn = wave % WN, wt = wave / WN;
     // XCD-aware order: workgroups go to the 8 XCDs in turn, so XCD x takes one
@@ -251,6 +272,9 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
 #pragma unroll
         for (int s = 0; s + 1 < S; ++s) round(s, st, s + 1, c, to);
     };
+    const int tw = wt * (BT / WT);   // the wave's first token of the tile
+    int id_l = -1;                   // of the wave's token `lane`
+    if (AD) id_l = p.ad.ids[t0 + min(tw + lane, ntok - 1)];
 #pragma unroll
     for (int c = 0; c < NSTG; ++c) {
         if (TAIL && c >= nk) break;
@@ -258,31 +282,86 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
 #pragma unroll
         for (int q = 0; q < CPS; ++q) copy(c, ring + c * STAGE, q);
     }
-    int aid[TB], rk[TB];   // the adapters of this lane's tokens, and their ranks
+    int rank_l = p.ad.R, aid[TB];    // its rank; the adapters of this lane's columns
+    bool leader = false;
     if (AD) {
+        if (lane >= BT / WT || tw + lane >= ntok || id_l < 0 || id_l >= p.ad.n) id_l = -1;
+        if (p.ad.ranks != nullptr) rank_l = p.ad.ranks[max(id_l, 0)];
+        leader = is_leader(id_l, BT / WT, ids_of[wid]);
 #pragma unroll
-        for (int j = 0; j < TB; ++j) {
-            const int t = wt * (BT / WT) + 16 * j + l16;
-            const int a = t < ntok ? p.ad.ids[t0 + t] : -1;
-            aid[j] = a >= 0 && a < p.ad.n ? a : -1;
-            rk[j] = p.ad.R;
-            if (p.ad.ranks != nullptr && aid[j] >= 0) rk[j] = min(p.ad.ranks[aid[j]], p.ad.R);
-        }
+        for (int j = 0; j < TB; ++j) aid[j] = ids_of[wid][16 * j + l16];
     }
+    // The low-rank part, one half (gated) and 32 ranks at a time: the tokens' s, and the
+    // rows of NI of the adapters of this wave's tokens at once, straight from memory; the K
+    // groups take the adapters in turn.  Each adapter's product is taken from zero and
+    // added in the columns (lanes) of its own tokens only, so that no value of one adapter,
+    // an infinity or NaN included, meets another request's row.
+    // The first ones are requested at the start by the small tiles, else before the steps
+    // that request no more copies; LOADS loads, masked lanes among them.
+    constexpr bool AHEAD = NB + TB <= 4;
+    constexpr int NI = NB + TB <= 4 ? 8 : NB + TB <= 9 ? 3 : 1, NH = GATED ? NB / 2 : NB;
+    constexpr int LOADS = AD && !AHEAD && TAIL ? TB + NI * NH : 0;
+    static_assert(CPS * (NSTG - 2) + LOADS <= 63, "loads in flight");
+    int count = 0, at = 0, h = 0, k0 = 0;   // adapters of this phase, the group's next; half, first rank
+    u32x4 va[NI][NH], vb[TB];
+    int ia[NI], rank_of[NI];
+    const rsrc_t sr = AD ? make_rsrc(p.ad.s + t0 * p.ad.lds, static_cast<uint32_t>(((ntok - 1) * p.ad.lds + (GATED ? 2 : 1) * p.ad.R) * 2))
+                         : rsrc_t();
+    auto tokens = [&]() __attribute__((always_inline)) {
+        count = list_adapters(leader, id_l, min(rank_l, p.ad.R), k0, lists[wid]);
+        at = kg;
+#pragma unroll
+        for (int j = 0; j < TB; ++j)
+            vb[j] = bload16(sr, aid[j] >= 0 && k0 + 8 * q4 < p.ad.R
+                                    ? static_cast<uint32_t>((tw + 16 * j + l16) * p.ad.lds + h * p.ad.R + k0 + 8 * q4) * 2 : NO_LANE);
+    };
+    auto adapters = [&]() __attribute__((always_inline)) {   // the next NI of this group
+        uint64_t of[NI];
+#pragma unroll
+        for (int n = 0; n < NI; ++n) of[n] = lists[wid][min(at + n * KG, 63)];
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            const bool in = at + n * KG < count;
+            ia[n] = in ? __builtin_amdgcn_readfirstlane(static_cast<int>(of[n])) : -1;
+            rank_of[n] = __builtin_amdgcn_readfirstlane(static_cast<int>(of[n] >> 32));
+            const bool ranks = in && k0 + 8 * q4 < rank_of[n];   // the lane has some
+            const rsrc_t br = make_rsrc(p.ad.b + max(ia[n], 0) * p.ad.b_stride + (static_cast<int64_t>(h) * p.N + n0) * p.ad.R,
+                                        static_cast<uint32_t>(nch) * p.ad.R * 2u);
+#pragma unroll
+            for (int i = 0; i < NH; ++i) {
+                const int c = wn * CW + 16 * i + l16;
+                va[n][i] = bload16(br, ranks && c < nch ? static_cast<uint32_t>(c * p.ad.R + k0 + 8 * q4) * 2 : NO_LANE);
+            }
+        }
+        at += NI * KG;
+    };
+    auto first_adapters = [&]() __attribute__((always_inline)) {
+        tokens();
+        adapters();
+        // the waits that follow count these loads: they stay in front of them
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
     __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
     __syncthreads();
+    if (AD && AHEAD) first_adapters();
 #pragma unroll
     for (int q = 0; q < NR; ++q) read(ring, 0, q);
     most(ring, -1, ring);
     int buf = 0;
-    // from step c to step c + 1: `left` of the stages behind that one may still be on their way
-    auto step = [&](int left, int next) __attribute__((always_inline)) {
-        if (NSTG > 3 && left >= 2)
-            __builtin_amdgcn_s_waitcnt(wait_vm_lds(CPS * 2));
+    // from step c to step c + 1: `left` of the stages behind that one, and `more` later
+    // loads, may still be on their way (the first stages have landed: no wait for the items
+    // that were requested after them)
+    auto step = [&](int c, int left, auto more, int next) __attribute__((always_inline)) {
+        constexpr int MORE = decltype(more)::value;
+        if (AD && AHEAD && c + 1 < NSTG)
+            __builtin_amdgcn_s_waitcnt(wait_vm_lds(63));
+        else if (NSTG > 3 && left >= 2)
+            __builtin_amdgcn_s_waitcnt(wait_vm_lds(CPS * 2 + MORE));
         else if (NSTG > 2 && left >= 1)
-            __builtin_amdgcn_s_waitcnt(wait_vm_lds(CPS));
+            __builtin_amdgcn_s_waitcnt(wait_vm_lds(CPS + MORE));
         else
-            __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));
+            __builtin_amdgcn_s_waitcnt(wait_vm_lds(MORE));
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
@@ -294,100 +373,43 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
         most(st, next, done);
     };
     int c = 0;
-    for (; c + (TAIL ? NSTG : 1) < nk; ++c) step(NSTG - 2, c + NSTG);
+    for (; c + (TAIL ? NSTG : 1) < nk; ++c) step(c, NSTG - 2, std::integral_constant<int, 0>(), c + NSTG);
+    if (AD && !AHEAD) first_adapters();
     if (TAIL)
-        for (; c + 1 < nk; ++c) step(nk - 2 - c, -1);
+        for (; c + 1 < nk; ++c) step(c, nk - 2 - c, std::integral_constant<int, LOADS>(), -1);
     round(S - 1, nullptr, 0, -1, ring);
     if (AD) {
-        // The low-rank part in items of one adapter of this wave's tokens, one half (gated)
-        // and 32 ranks, NI of them at a time, their operands straight from memory; the K
-        // groups take the items in turn.  Tokens of other adapters are zeros.  An item whose
-        // adapter holds an infinity or NaN is taken from zero and added in the columns
-        // (lanes) of its own tokens only, so that it does not meet another request's row.
-        constexpr int NI = NB + TB <= 4 ? 4 : NB + TB <= 9 ? 2 : 1, NH = GATED ? NB / 2 : NB;
-        uint64_t left[TB];
-#pragma unroll
-        for (int j = 0; j < TB; ++j) left[j] = __ballot(aid[j] >= 0);
-        int item_a = -1, item_h = 0, item_k = 0, rank = 0;
-        auto advance = [&]() __attribute__((always_inline)) {   // to the next item; item_a < 0: there is none
-            if (item_a >= 0) {
-                if (item_k + 32 < rank) {
-                    item_k += 32;
-                    return;
-                }
-                item_k = 0;
-                if (GATED && item_h == 0) {
-                    item_h = 1;
-                    return;
-                }
-            }
-            item_h = item_k = 0;
-            for (;;) {
-                item_a = -1;
-#pragma unroll
-                for (int j = TB - 1; j >= 0; --j)
-                    if (left[j]) {
-                        const int lane_of = __builtin_ctzll(left[j]);
-                        item_a = __builtin_amdgcn_readlane(aid[j], lane_of);
-                        rank = __builtin_amdgcn_readlane(rk[j], lane_of);
-                    }
-                if (item_a < 0) return;
-#pragma unroll
-                for (int j = 0; j < TB; ++j) left[j] &= ~__ballot(aid[j] == item_a);
-                if (rank > 0) return;
-            }
-        };
-        advance();
-        for (int g = 0; g < kg && item_a >= 0; ++g) advance();
-        while (item_a >= 0) {
-            u32x4 va[NI][NH], vb[NI][TB];
-            int ia[NI], ih[NI];
-#pragma unroll
-            for (int n = 0; n < NI; ++n) {
-                ia[n] = item_a;
-                ih[n] = item_h;
-                const int k = item_k + 8 * q4;
-                const bool in = item_a >= 0 && k < rank;
-                const uint16_t* pb = p.ad.b + item_a * p.ad.b_stride + k;
-                const uint16_t* ps = p.ad.s + item_h * p.ad.R + k;
-#pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    const int c = wn * CW + 16 * i + l16;
-                    va[n][i] = u32x4{0, 0, 0, 0};
-                    if (in && c < nch)
-                        va[n][i] = low_ranks(*reinterpret_cast<const u32x4*>(pb + (static_cast<int64_t>(item_h) * p.N + n0 + c) * p.ad.R),
-                                             rank - k);
-                }
-#pragma unroll
-                for (int j = 0; j < TB; ++j) {
-                    vb[n][j] = u32x4{0, 0, 0, 0};
-                    if (in && aid[j] == item_a)
-                        vb[n][j] = *reinterpret_cast<const u32x4*>(ps + (t0 + wt * (BT / WT) + 16 * j + l16) * p.ad.lds);
-                }
-                for (int g = 0; g < KG && item_a >= 0; ++g) advance();
-            }
+        for (;;) {
 #pragma unroll
             for (int n = 0; n < NI; ++n) {
                 if (ia[n] < 0) continue;
-                bool finite = true;
+                if (rank_of[n] & 7) {   // some lane holds less than 8 ranks
 #pragma unroll
-                for (int i = 0; i < NH; ++i) finite = finite && all_finite(va[n][i]);
-                const bool plain = __all(finite);
+                    for (int i = 0; i < NH; ++i) va[n][i] = low_ranks(va[n][i], rank_of[n] - k0 - 8 * q4);
+                }
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    if (GATED && (i & 1) != ih[n]) continue;
-                    const u32x4& v = va[n][GATED ? i / 2 : i];
+                for (int j = 0; j < TB; ++j) {
+                    f32x4 low[NH];
 #pragma unroll
-                    for (int j = 0; j < TB; ++j) {
-                        if (plain) {
-                            acc[i][j] = mfma16x16x32(v, vb[n][j], acc[i][j]);
-                        } else {
-                            const f32x4 low = mfma16x16x32(v, vb[n][j], f32x4{0, 0, 0, 0});
-                            if (aid[j] == ia[n]) acc[i][j] += low;
-                        }
+                    for (int i = 0; i < NH; ++i) low[i] = mfma16x16x32(va[n][i], vb[j], f32x4{0, 0, 0, 0});
+                    if (aid[j] == ia[n]) {
+#pragma unroll
+                        for (int i = 0; i < NB; ++i)
+                            if (!GATED || (i & 1) == h) acc[i][j] += low[GATED ? i / 2 : i];
                     }
                 }
             }
+            if (at >= count) {   // the other half, then the next 32 ranks, of the adapters that have them
+                if (GATED && h == 0) {
+                    h = 1;
+                } else {
+                    h = 0;
+                    k0 += 32;
+                    if (k0 >= p.ad.R) break;
+                }
+                tokens();
+            }
+            adapters();
         }
     }
     __builtin_amdgcn_s_waitcnt(wait_vm_lds(0));   // zero stages have landed too
@@ -598,7 +620,7 @@ static hipError_t bf16_tiles(const MatBf16Params& p, hipStream_t s) {
         case 5: return bf16_tile<KIND, AD, 128, 128, 2, 4, 4, 1>(p, s);
         case 6: return bf16_tile<KIND, AD, 128, 192, 2, 4, 3, 1>(p, s);
         case 7: return bf16_tile<KIND, AD, 192, 192, 2, 4, 3, 1>(p, s);
-        case 8: return bf16_tile<KIND, AD, 256, 192, 4, 2, 2, 1>(p, s);
+        case 8: return bf16_tile<KIND, AD, 256, 192, AD ? 2 : 4, AD ? 4 : 2, 2, 1>(p, s);   // (64 tokens of a wave at most)
     }
     if constexpr (KIND != MAT_GATED && !AD) return bf16_tile<KIND, AD, 256, 256, 4, 2, 2, 1>(p, s);
     return hipErrorInvalidValue;   // not reached
