@@ -123,30 +123,26 @@ moe_status check_gradients(const char* fn, const Gradients& g) {
     return MOE_OK;
 }
 hipError_t launch_gradients(const Gradients& g, hipStream_t s) {
-    MatBf16Params p{};
-    p.x = static_cast<const uint16_t*>(g.d);
-    p.ldx = g.ldd;
-    p.N = g.K;
-    hipError_t e = hipSuccess;
-    if (g.dx && g.T > 0) {
-        p.w = static_cast<const uint16_t*>(g.w);
-        p.ldw = g.ldw;
-        p.T = g.T; p.K = g.M;
-        p.out = g.dx;
-        p.out_dt = g.dx_dt;
-        p.ldo = g.lddx;
-        e = launch_matmul_bf16(p, MAT_NN, s);
-    }
-    if (g.dw && e == hipSuccess) {
-        p.w = static_cast<const uint16_t*>(g.x);
-        p.ldw = g.ldx;
-        p.T = g.M; p.K = g.T;
-        p.out = g.dw;
-        p.out_dt = g.dw_dt;
-        p.ldo = g.lddw;
-        e = launch_matmul_bf16(p, MAT_TN, s);
-    }
-    return e;
+    MatBf16Params rows{}, weights{};
+    rows.x = weights.x = static_cast<const uint16_t*>(g.d);
+    rows.ldx = weights.ldx = g.ldd;
+    rows.N = weights.N = g.K;
+    rows.T = weights.K = g.T;
+    rows.K = weights.T = g.M;
+    rows.w = static_cast<const uint16_t*>(g.w);
+    rows.ldw = g.ldw;
+    rows.out = g.dx;
+    rows.out_dt = g.dx_dt;
+    rows.ldo = g.lddx;
+    weights.w = static_cast<const uint16_t*>(g.x);
+    weights.ldw = g.ldx;
+    weights.out = g.dw;
+    weights.out_dt = g.dw_dt;
+    weights.ldo = g.lddw;
+    const bool dx = g.dx && g.T > 0;   // (without tokens dw is zeros, and dx has no rows)
+    if (dx && g.dw) return launch_matmul_bf16_pair(rows, weights, s);
+    if (dx) return launch_matmul_bf16(rows, MAT_NN, s);
+    return g.dw ? launch_matmul_bf16(weights, MAT_TN, s) : hipSuccess;
 }
 
 }  // namespace

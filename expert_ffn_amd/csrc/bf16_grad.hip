@@ -1,11 +1,77 @@
 // Gradients of the bfloat16 products: the tile kernel on operands whose rows are the k,
 // and the gated activation's gradient.
+#include <algorithm>
+
 #include "bf16_tile.h"
 
 namespace moe {
 
 hipError_t tiles_nn(const MatBf16Params& p, hipStream_t s) { return bf16_tiles<MAT_NN, false>(p, s); }
 hipError_t tiles_tn(const MatBf16Params& p, hipStream_t s) { return bf16_tiles<MAT_TN, false>(p, s); }
+
+template <int BN, int BT, int WN, int WT, int NSTG, int KG>
+static hipError_t pair(const MatBf16Params& p, const MatBf16Params& r, hipStream_t s) {
+    auto tiles = [](int size, int tile) { return (size + tile - 1) / tile; };
+    const int pn = tiles(p.N, BN), pt = tiles(p.T, BT), rn = tiles(r.N, BN), rt = tiles(r.T, BT);
+    const int first = (pn * pt + 7) / 8 * 8, second = (rn * rt + 7) / 8 * 8;
+    hipLaunchKernelGGL((matmul_bf16_pair_kernel<BN, BT, WN, WT, NSTG, KG>), dim3(first + second), dim3(64 * WN * WT * KG), 0, s, p, pn, pt,
+                       r, rn, rt, first);
+    return hipGetLastError();
+}
+
+// Both gradients in one launch, or one after the other: the smaller estimate.  In one
+// launch the workgroups of both fill the CUs together: the sum of their times over the
+// CUs, 0.3 of the longer one's for the uneven end, times a factor of the tile, fitted
+// to 51 shapes (T 16 to 4096) with six tiles; a launch of its own costs another 0.5 us.  The
+// choice is 1.4 % slower than the best on average.  T = 333, 1408 x 1424: 10.5 us in one
+// launch, 14.2 in two; T = 1001, 2816 x 704: 17.1 and 21.0; T = 43, 184 x 536: 3.4 and 6.2;
+// T = 4096, 2816 x 2112: 98.9 and 97.7.
+struct PairTile {
+    int tile;   // of Bf16Tiles
+    float factor;
+};
+constexpr PairTile PAIR_TILES[] = {{0, 1.0f}, {1, 1.1f}, {3, 1.0f}, {4, 1.25f}, {5, 1.0f}, {7, 0.85f}};
+
+static int pick_pair(const MatBf16Params& p, const MatBf16Params& r) {
+    int best = -1;
+    float best_us = 0.5f + bf16_tile_us(Bf16Tiles<MAT_NN>::T[pick_bf16_tile<MAT_NN, false>(p.T, p.N, p.K)], p.T, p.N, p.K) +
+                    bf16_tile_us(Bf16Tiles<MAT_TN>::T[pick_bf16_tile<MAT_TN, false>(r.T, r.N, r.K)], r.T, r.N, r.K);
+    for (const PairTile& c : PAIR_TILES) {
+        float work = 0.0f, alone = 0.0f, longest = 0.0f, fixed = 0.0f;
+        int64_t groups = 0;
+        auto add = [&](const Bf16Tile& t, const MatBf16Params& q) {
+            const int64_t W = ((q.N + t.bn - 1) / t.bn) * ((q.T + t.bt - 1ll) / t.bt);
+            const float steps = static_cast<float>((q.K + 63) / 64), full = steps * t.full + t.end;
+            groups += W;
+            work += static_cast<float>(W) / 256.0f * full;
+            alone = std::max(alone, steps * t.alone + t.end);
+            longest = std::max(longest, full);
+            fixed = std::max(fixed, t.fixed);
+        };
+        add(Bf16Tiles<MAT_NN>::T[c.tile], p);
+        add(Bf16Tiles<MAT_TN>::T[c.tile], r);
+        if (groups >= (1 << 22)) continue;   // keeps every launch below 2^32 threads
+        const float us = c.factor * (fixed + std::max(alone, work + 0.3f * longest));
+        if (us < best_us) {
+            best_us = us;
+            best = c.tile;
+        }
+    }
+    return best;
+}
+
+hipError_t launch_matmul_bf16_pair(const MatBf16Params& p, const MatBf16Params& r, hipStream_t s) {
+    switch (pick_pair(p, r)) {
+        case 0: return pair<32, 32, 1, 1, 3, 4>(p, r, s);
+        case 1: return pair<64, 32, 2, 1, 3, 4>(p, r, s);
+        case 3: return pair<64, 64, 2, 2, 3, 1>(p, r, s);
+        case 4: return pair<128, 64, 2, 2, 3, 1>(p, r, s);
+        case 5: return pair<128, 128, 2, 4, 4, 1>(p, r, s);
+        case 7: return pair<192, 192, 2, 4, 3, 1>(p, r, s);
+    }
+    const hipError_t e = tiles_nn(p, s);
+    return e == hipSuccess ? tiles_tn(r, s) : e;
+}
 
 // act(g) = g q with q = 1 / (1 + e^z):  act'(g) = q - g q (1 - q) dz/dg
 //   silu z = -g;  gelu (tanh form) z = -2 sqrt(2/pi) (g + 0.044715 g^3)

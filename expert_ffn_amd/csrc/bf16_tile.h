@@ -107,8 +107,10 @@ struct Operand {
     }
 };
 
+// One tile: number `id` of nt_n x nt_t (see the order below).  lds: KG * NSTG * (BN + BT) * 128 bytes.
 template <int BN, int BT, int WN, int WT, int NSTG, int KG, int KIND, bool AD>
-__global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(MatBf16Params p, int nt_n, int nt_t) {
+__device__ __forceinline__ void matmul_bf16_tile(const MatBf16Params& p, int nt_n, int nt_t, int block, uint8_t* lds, int (*ids_of)[64],
+                                                 uint64_t (*lists)[64]) {
     constexpr bool GATED = KIND == MAT_GATED, TRA = KIND == MAT_NN || KIND == MAT_TN, TRB = KIND == MAT_TN;
     using OA = Operand<BN, TRA>;
     using OB = Operand<BT, TRB>;
@@ -121,9 +123,6 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
     static_assert(DA * 8 * NW == BN && DB * 8 * NW == BT && NB * 16 * WN == BN && TB * 16 * WT == BT && (!GATED || NB % 2 == 0), "tile shape");
     static_assert(NSTG >= 2 && NSTG <= 4 && CPS * (NSTG - 1) <= 63, "copies in flight");
     static_assert((KG - 1) * BN * BT * 4 <= KG * RING, "epilogue regions");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * RING];
-    __shared__ __attribute__((aligned(16))) int ids_of[AD ? NW * KG : 1][64];
-    __shared__ uint64_t lists[AD ? NW * KG : 1][64];
     static_assert(!AD || BT / WT <= 64, "tokens of a wave");
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kg = wid / NW, wave = wid % NW, wn = wave % WN, wt = wave / WN;
@@ -131,7 +130,7 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
     // contiguous range of the tile list, which runs down 8 token tiles before it
     // goes to the next channel tile
     const int ntile = nt_n * nt_t, per = (ntile + 7) / 8;
-    const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    const int id = (block & 7) * per + (block >> 3);
     if (id >= ntile) return;
     constexpr int GRP = 8;
     const int g0 = id / (GRP * nt_n) * GRP, gh = min(GRP, nt_t - g0), r = id - g0 * nt_n;
@@ -519,6 +518,27 @@ __global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(
             leave(is_bf16(), tb, p.pre, p.ldp, p.N, up);
         }
     }
+}
+
+template <int BN, int BT, int WN, int WT, int NSTG, int KG, int KIND, bool AD>
+__global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_tile_kernel(MatBf16Params p, int nt_n, int nt_t) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * NSTG * (BN + BT) * 128];
+    __shared__ __attribute__((aligned(16))) int ids_of[AD ? WN * WT * KG : 1][64];
+    __shared__ uint64_t lists[AD ? WN * WT * KG : 1][64];
+    matmul_bf16_tile<BN, BT, WN, WT, NSTG, KG, KIND, AD>(p, nt_n, nt_t, blockIdx.x, lds, ids_of, lists);
+}
+
+// Both gradients of a product in one launch: the workgroups of the rows' (NN), then those
+// of the weights' (TN).
+template <int BN, int BT, int WN, int WT, int NSTG, int KG>
+__global__ __launch_bounds__(64 * WN * WT * KG, 1) void matmul_bf16_pair_kernel(MatBf16Params p, int np_n, int np_t, MatBf16Params r,
+                                                                               int nr_n, int nr_t, int first) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[KG * NSTG * (BN + BT) * 128];
+    const int block = blockIdx.x;
+    if (block < first)
+        matmul_bf16_tile<BN, BT, WN, WT, NSTG, KG, MAT_NN, false>(p, np_n, np_t, block, lds, nullptr, nullptr);
+    else
+        matmul_bf16_tile<BN, BT, WN, WT, NSTG, KG, MAT_TN, false>(r, nr_n, nr_t, block - first, lds, nullptr, nullptr);
 }
 
 template <int KIND, bool AD, int BN, int BT, int WN, int WT, int NSTG, int KG>

@@ -122,6 +122,8 @@ struct MatBf16Params {
     AdapterParams ad;
 };
 hipError_t launch_matmul_bf16(const MatBf16Params& p, MatKind kind, hipStream_t s);
+// both gradients of one product: rows (NN) and weights (TN)
+hipError_t launch_matmul_bf16_pair(const MatBf16Params& rows, const MatBf16Params& weights, hipStream_t s);
 
 // dpre = the gradient of pre: dout u act'(g), then dout act(g)
 struct GatedGradParams {

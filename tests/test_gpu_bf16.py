@@ -234,3 +234,35 @@ def test_adapters(L, T, N, K, n, R, gated, kind, uneven):  # noqa: F811
     v = v.cpu().numpy()
     want, bound = block_ref.gated(v[:, :N], v[:, N:], 1)
     close(f64(out), want, bound, "out")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_backward_of_no_tokens(L, dt):  # noqa: F811
+    """The weights' gradient of no tokens is zeros; the rows' has no rows."""
+    N, K = 112, 72
+    x, d, w = torch.empty(0, K, dtype=BF16, device="cuda"), torch.empty(0, N, dtype=BF16, device="cuda"), whole(gen(1), N, K)
+    dw, buf = padded(N, K, DT[dt], 8, 2.0)
+    L.matmul_bf16_backward(x, w, d, dx=torch.empty(0, K, device="cuda"), dw=dw)
+    torch.cuda.synchronize()
+    check_padding(buf, K, 2.0)
+    assert (dw == 0).all()
+    L.matmul_bf16_backward(x, w, d, dx=torch.empty(0, K, device="cuda"))
+    dw.fill_(3.0)
+    g = d[:, :N // 2]
+    L.gated_matmul_bf16_backward(x, w, 0, d, g, torch.empty_like(d), dw=dw)
+    torch.cuda.synchronize()
+    assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("T,N,K", GRAD)
+def test_one_gradient_is_that_of_both(L, T, N, K):  # noqa: F811
+    """dx and dw asked for apart (a launch each) and together (one launch for small shapes): exact sums."""
+    g = gen(T + 5 * N + K)
+    x, w, d = whole(g, T, K), whole(g, N, K), whole(g, T, N)
+    out = [torch.full((r, K), 7.0, dtype=BF16, device="cuda") for r in (T, N, T, N)]
+    L.matmul_bf16_backward(x, w, d, dx=out[0], dw=out[1])
+    L.matmul_bf16_backward(x, w, d, dx=out[2])
+    L.matmul_bf16_backward(x, w, d, dw=out[3])
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])
+    equal(out[0], d.to(F64) @ w.to(F64).contiguous(), "dx")
