@@ -565,7 +565,8 @@ moe_status moe_gated_matmul_i8(const int8_t* xq, int64_t ldx, const float* x_sca
  *   b    device bf16: adapter a's [N, R] (gated [2F, R]) contiguous at b + a * b_stride
  *   ranks device int32 [n_adapters] or NULL: R of all; values outside [0, R] count as
  *        the nearest of the two
- * A token's row depends on its own adapter only; what lies past a rank is not used.
+ * A token's row depends on its own adapter only (the order of its fp32 sums also on the
+ * adapters of the tokens around it); what lies past a rank is not used.
  *
  * K a multiple of 8 up to 2^20; rows of x, w and s 16-byte aligned with strides up to
  * 2^21 elements; R a multiple of 8 up to 1024, b 16-byte aligned and b_stride a
