@@ -94,7 +94,7 @@ template <int ROWS, bool TR>
 struct Operand {
     static constexpr bool COLUMNS = TR;
     static constexpr int PITCH = TR ? ROWS * 2 : 128, CPR = PITCH / 16;
-    static_assert(!TR || PITCH % 256 == 0 || PITCH % 256 == 128 || PITCH == 64, "banks of a row");
+    static_assert(!TR || PITCH % 64 == 0, "banks of a row");
     __device__ static int swz_k(int k) {
         const int far = (k >> 3) & 1;
         return PITCH % 256 == 0 ? ((k & 3) | far << 2) << 1 : PITCH % 256 == 128 ? (((k >> 1) & 1) | far << 1) << 1 : far << 1;
@@ -247,10 +247,11 @@ __device__ __forceinline__ void matmul_bf16_tile(const MatBf16Params& p, int nt_
     constexpr int S = BK / 32;
     constexpr int NR = NB + TB, RG = TB > 1 ? TB - 1 : 1;   // operands of a round, the blocks they are read with
     constexpr int M = (NSTG > 2 ? S : 1) * NB * TB;
-    auto round = [&](int s, const uint8_t* st, int rs, int c, uint8_t* to) __attribute__((always_inline)) {   // reads round rs of stage st (null: nothing)
+    // round s; reads round rs of stage st, where that is wanted
+    auto round = [&](int s, auto reads, const uint8_t* st, int rs, int c, uint8_t* to) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < TB; ++j) {
-            if (st != nullptr) {
+            if (decltype(reads)::value) {
 #pragma unroll
                 for (int q = 0; q < NR; ++q)
                     if (q * RG / NR == j) read(st, rs, q);
@@ -269,7 +270,7 @@ __device__ __forceinline__ void matmul_bf16_tile(const MatBf16Params& p, int nt_
     };
     auto most = [&](const uint8_t* st, int c, uint8_t* to) __attribute__((always_inline)) {   // rounds 0 .. S - 2
 #pragma unroll
-        for (int s = 0; s + 1 < S; ++s) round(s, st, s + 1, c, to);
+        for (int s = 0; s + 1 < S; ++s) round(s, std::true_type(), st, s + 1, c, to);
     };
     const int tw = wt * (BT / WT);   // the wave's first token of the tile
     int id_l = -1;                   // of the wave's token `lane`
@@ -368,7 +369,7 @@ __device__ __forceinline__ void matmul_bf16_tile(const MatBf16Params& p, int nt_
         buf = buf + 1 == NSTG ? 0 : buf + 1;
         const uint8_t* st = ring + buf * STAGE;
         if (next >= 0) stage(next);
-        round(S - 1, st, 0, next, done);
+        round(S - 1, std::true_type(), st, 0, next, done);
         most(st, next, done);
     };
     int c = 0;
@@ -376,7 +377,7 @@ __device__ __forceinline__ void matmul_bf16_tile(const MatBf16Params& p, int nt_
     if (AD && !AHEAD) first_adapters();
     if (TAIL)
         for (; c + 1 < nk; ++c) step(c, nk - 2 - c, std::integral_constant<int, LOADS>(), -1);
-    round(S - 1, nullptr, 0, -1, ring);
+    round(S - 1, std::false_type(), ring, 0, -1, ring);
     if (AD) {
         for (;;) {
 #pragma unroll
@@ -556,13 +557,16 @@ static hipError_t bf16_tile(const MatBf16Params& p, hipStream_t s) {
 // K steps about fixed + max(steps * alone + end, ceil(W / 256) * (steps * full + end)):
 // `full` is the time of a step, `alone` that of a workgroup that has its CU for itself
 // (several of the small ones fit on a CU), `end` that of prologue and epilogue.  The
-// figures (us) are fitted to times of 18 tiles at 60 shapes of each kind (T 16 to 8192,
-// the other sizes 64 to 8192); of those, these ten lose 0.5 to 0.8 % on average against
-// the best of all 18 (the ends of the range: T = 80, N = 2336, K = 232, TN: 32 x 32 3.4
-// us, 256 x 256 9.8; T = 8192, N = 4096, K = 8192: 32 x 32 1612 us, 256 x 256 404), and
-// the choice by the estimate another 1.6 to 2.4 %.  192 x 192 is there for three stages
-// of copies under 160 KB (gated T = 4096, 2 x 2112 x 2816: 85 us, 256 x 192 99, 128 x 192
-// 94).  Gated 256 x 256 does not fit the registers (152 us there).
+// figures (us) are fitted to times of 21 tiles at 80 to 90 shapes of each kind (T 16 to
+// 8192, the other sizes 64 to 8192); of those, these twelve lose 0.3 to 0.5 % on average
+// against the best of all 21 (the ends of the range: T = 752, N = 960, K = 536, TN: 64 x 64
+// 4.8 us, 256 x 256 15.5; T = 8192, N = 4096, K = 8192: 32 x 32 1612 us, 256 x 256 404),
+// and the choice by the estimate another 0.7 to 2.1 %.
+// A tile's LDS reads a step, (BN / 16 * WT + BT / 16 * WN) KB at 128 bytes a cycle, take longer
+// than its MFMA where the waves' parts are small: 128 x 128 in four waves of 64 x 64 takes 33
+// us at T = 1024, N = 2816, K = 4224, NN, in eight 40.  192 x 192 is there for three stages of
+// copies under 160 KB (gated T = 2048, 2 x 2112 x 2816: 42 us, 256 x 192 48, 128 x 192 54).
+// Gated 256 x 256 does not fit the registers (T = 4096: 152 us, 192 x 192 85).
 struct Bf16Tile {
     int bn, bt;
     float alone, full, fixed, end;
@@ -572,36 +576,38 @@ struct Bf16Tiles;
 template <>
 struct Bf16Tiles<MAT_NT> {
     static constexpr Bf16Tile T[] = {
-        {32, 32, 0.071f, 0.091f, 1.28f, 2.31f},   {64, 32, 0.117f, 0.139f, 1.09f, 2.69f},   {64, 64, 0.103f, 0.190f, 0.80f, 3.06f},
-        {64, 64, 0.238f, 0.198f, 2.59f, 0.72f},   {128, 64, 0.322f, 0.271f, 2.59f, 1.92f},  {128, 128, 0.420f, 0.423f, 0.00f, 4.81f},
-        {128, 192, 0.557f, 0.557f, 2.06f, 4.09f}, {192, 192, 0.597f, 0.639f, 0.00f, 10.46f}, {256, 192, 0.894f, 0.923f, 0.00f, 8.89f},
-        {256, 256, 1.033f, 1.083f, 0.00f, 11.41f},
+        {32, 32, 0.077f, 0.090f, 1.07f, 2.17f},  {64, 32, 0.135f, 0.145f, 0.91f, 2.51f},  {64, 64, 0.100f, 0.213f, 0.54f, 2.90f},
+        {64, 64, 0.233f, 0.220f, 2.44f, 0.52f},  {64, 96, 0.240f, 0.240f, 0.47f, 4.06f},  {96, 96, 0.113f, 0.206f, 0.77f, 8.33f},
+        {128, 64, 0.194f, 0.243f, 0.17f, 6.29f}, {128, 128, 0.398f, 0.412f, 0.52f, 5.56f}, {128, 192, 0.566f, 0.566f, 2.57f, 2.79f},
+        {192, 192, 0.617f, 0.617f, 4.72f, 4.78f}, {256, 192, 0.961f, 0.967f, 0.00f, 7.65f}, {256, 256, 1.052f, 1.052f, 5.01f, 5.49f},
     };
 };
 template <>
 struct Bf16Tiles<MAT_GATED> {
     static constexpr Bf16Tile T[] = {
-        {32, 32, 0.125f, 0.099f, 1.16f, 2.01f},   {64, 32, 0.186f, 0.158f, 1.04f, 2.20f},   {64, 64, 0.125f, 0.230f, 0.73f, 2.51f},
-        {64, 64, 0.267f, 0.207f, 2.30f, 0.63f},   {128, 64, 0.370f, 0.308f, 1.98f, 1.60f},  {128, 128, 0.462f, 0.469f, 0.00f, 4.28f},
-        {128, 192, 0.483f, 0.566f, 0.00f, 5.81f}, {192, 192, 0.544f, 0.733f, 0.00f, 8.11f}, {256, 192, 1.063f, 1.025f, 0.00f, 6.96f},
+        {32, 32, 0.112f, 0.102f, 1.26f, 1.94f},  {64, 32, 0.183f, 0.168f, 0.94f, 2.18f},  {64, 64, 0.244f, 0.251f, 0.75f, 2.36f},
+        {64, 64, 0.270f, 0.225f, 2.02f, 0.58f},  {64, 96, 0.285f, 0.293f, 0.60f, 3.19f},  {96, 96, 0.154f, 0.298f, 0.06f, 6.83f},
+        {128, 64, 0.252f, 0.308f, 0.25f, 5.13f}, {128, 128, 0.380f, 0.484f, 0.00f, 5.01f}, {128, 192, 0.596f, 0.597f, 0.00f, 5.06f},
+        {192, 192, 0.750f, 0.750f, 0.01f, 7.28f}, {256, 192, 1.077f, 1.081f, 0.00f, 6.24f},
     };
 };
 template <>
 struct Bf16Tiles<MAT_NN> {
     static constexpr Bf16Tile T[] = {
-        {32, 32, 0.102f, 0.143f, 1.29f, 1.53f},   {64, 32, 0.182f, 0.175f, 0.96f, 1.96f},   {64, 64, 0.183f, 0.223f, 0.62f, 2.44f},
-        {64, 64, 0.268f, 0.220f, 2.22f, 0.50f},   {128, 64, 0.348f, 0.304f, 2.08f, 1.04f},  {128, 128, 0.450f, 0.485f, 0.03f, 3.67f},
-        {128, 192, 0.574f, 0.606f, 0.00f, 4.12f}, {192, 192, 0.777f, 0.808f, 0.00f, 4.64f}, {256, 192, 0.956f, 0.956f, 0.01f, 4.39f},
-        {256, 256, 1.077f, 1.144f, 0.00f, 5.29f},
+        {32, 32, 0.086f, 0.145f, 1.17f, 1.50f},  {64, 32, 0.137f, 0.186f, 0.95f, 1.85f},  {64, 64, 0.038f, 0.242f, 0.55f, 2.21f},
+        {64, 64, 0.268f, 0.222f, 2.04f, 0.48f},  {64, 96, 0.174f, 0.287f, 0.50f, 2.73f},  {96, 96, 0.264f, 0.316f, 0.19f, 4.14f},
+        {128, 64, 0.019f, 0.302f, 0.36f, 3.59f}, {128, 128, 0.350f, 0.445f, 0.00f, 3.66f}, {128, 192, 0.425f, 0.588f, 0.00f, 3.93f},
+        {192, 192, 0.768f, 0.769f, 0.00f, 4.53f}, {256, 192, 0.964f, 0.989f, 0.00f, 4.18f}, {256, 256, 1.087f, 1.136f, 0.00f, 5.17f},
     };
 };
 template <>
 struct Bf16Tiles<MAT_TN> {
+    // (64 x 64 with two K groups is never the fastest here: not built)
     static constexpr Bf16Tile T[] = {
-        {32, 32, 0.120f, 0.163f, 1.46f, 1.46f},   {64, 32, 0.041f, 0.193f, 1.25f, 1.86f},   {64, 64, 0.198f, 0.238f, 1.31f, 1.75f},
-        {64, 64, 0.262f, 0.220f, 2.35f, 0.46f},   {128, 64, 0.191f, 0.338f, 2.51f, 0.66f},  {128, 128, 0.531f, 0.534f, 0.25f, 3.01f},
-        {128, 192, 0.533f, 0.638f, 0.00f, 3.78f}, {192, 192, 0.810f, 0.823f, 0.00f, 4.19f}, {256, 192, 0.950f, 0.959f, 0.00f, 4.71f},
-        {256, 256, 1.269f, 1.270f, 0.00f, 5.36f},
+        {32, 32, 0.164f, 0.177f, 1.21f, 1.42f},  {64, 32, 0.197f, 0.211f, 1.05f, 1.86f},  {64, 64, 9.0f, 9.0f, 9.0f, 9.0f},
+        {64, 64, 0.255f, 0.225f, 2.16f, 0.44f},  {64, 96, 0.294f, 0.307f, 0.98f, 2.37f},  {96, 96, 0.317f, 0.345f, 0.85f, 3.43f},
+        {128, 64, 0.297f, 0.324f, 0.98f, 3.01f}, {128, 128, 0.360f, 0.458f, 0.42f, 3.07f}, {128, 192, 0.614f, 0.653f, 0.00f, 3.59f},
+        {192, 192, 0.817f, 0.819f, 0.00f, 4.04f}, {256, 192, 0.995f, 0.995f, 0.00f, 4.43f}, {256, 256, 1.088f, 1.136f, 0.00f, 5.12f},
     };
 };
 
@@ -616,7 +622,7 @@ static float bf16_tile_us(const Bf16Tile& c, int64_t T, int64_t rows, int K) {
 template <int KIND, bool AD>
 static int pick_bf16_tile(int64_t T, int64_t rows, int K) {
     // (256 x 256 with adapters does not fit the registers either)
-    constexpr int n = KIND == MAT_NT && AD ? 9 : sizeof(Bf16Tiles<KIND>::T) / sizeof(Bf16Tile);
+    constexpr int n = KIND == MAT_NT && AD ? 11 : sizeof(Bf16Tiles<KIND>::T) / sizeof(Bf16Tile);
     int best = n - 1;
     float best_us = 1e30f;
     for (int i = 0; i < n; ++i) {
@@ -634,13 +640,17 @@ static hipError_t bf16_tiles(const MatBf16Params& p, hipStream_t s) {
     switch (pick_bf16_tile<KIND, AD>(p.T, static_cast<int64_t>(p.N) * (KIND == MAT_GATED ? 2 : 1), p.K)) {
         case 0: return bf16_tile<KIND, AD, 32, 32, 1, 1, 3, 4>(p, s);
         case 1: return bf16_tile<KIND, AD, 64, 32, 2, 1, 3, 4>(p, s);
-        case 2: return bf16_tile<KIND, AD, 64, 64, 2, 2, 4, 2>(p, s);
+        case 2:
+            if constexpr (KIND != MAT_TN) return bf16_tile<KIND, AD, 64, 64, 2, 2, 4, 2>(p, s);
+            break;
         case 3: return bf16_tile<KIND, AD, 64, 64, 2, 2, 3, 1>(p, s);
-        case 4: return bf16_tile<KIND, AD, 128, 64, 2, 2, 3, 1>(p, s);
-        case 5: return bf16_tile<KIND, AD, 128, 128, 2, 4, 4, 1>(p, s);
-        case 6: return bf16_tile<KIND, AD, 128, 192, 2, 4, 3, 1>(p, s);
-        case 7: return bf16_tile<KIND, AD, 192, 192, 2, 4, 3, 1>(p, s);
-        case 8: return bf16_tile<KIND, AD, 256, 192, AD ? 2 : 4, AD ? 4 : 2, 2, 1>(p, s);   // (64 tokens of a wave at most)
+        case 4: return bf16_tile<KIND, AD, 64, 96, 2, 2, 3, 2>(p, s);
+        case 5: return bf16_tile<KIND, AD, 96, 96, 1, 2, 3, 2>(p, s);
+        case 6: return bf16_tile<KIND, AD, 128, 64, 2, 1, 3, 2>(p, s);
+        case 7: return bf16_tile<KIND, AD, 128, 128, 2, 2, 3, 1>(p, s);
+        case 8: return bf16_tile<KIND, AD, 128, 192, 2, 4, 3, 1>(p, s);
+        case 9: return bf16_tile<KIND, AD, 192, 192, 2, 4, 3, 1>(p, s);
+        case 10: return bf16_tile<KIND, AD, 256, 192, AD ? 2 : 4, AD ? 4 : 2, 2, 1>(p, s);   // (64 tokens of a wave at most)
     }
     if constexpr (KIND != MAT_GATED && !AD) return bf16_tile<KIND, AD, 256, 256, 4, 2, 2, 1>(p, s);
     return hipErrorInvalidValue;   // not reached

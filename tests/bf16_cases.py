@@ -36,13 +36,13 @@ def tile_us(c, T, rows, K):
 
 def pick(kind, T, N, K, adapters=False):
     rows = 2 * N if kind == "MAT_GATED" else N
-    tiles = TILES[kind][:9] if adapters else TILES[kind]
+    tiles = TILES[kind][:11] if adapters else TILES[kind]
     return int(np.argmin([tile_us(c, T, rows, K) for c in tiles]))
 
 
 def pick_pair(T, N, K):
     """Tile of both gradients of [T, N] . [N, K] in one launch, -1 for one each."""
-    best, best_us = -1, f32(0.5) + tile_us(TILES["MAT_NN"][pick("MAT_NN", T, K, N)], T, K, N) + tile_us(
+    best, best_us = -1, tile_us(TILES["MAT_NN"][pick("MAT_NN", T, K, N)], T, K, N) + tile_us(
         TILES["MAT_TN"][pick("MAT_TN", N, K, T)], N, K, T)
     for i, factor in PAIR:
         work = alone = longest = fixed = f32(0)
@@ -51,7 +51,7 @@ def pick_pair(T, N, K):
             full = steps * c[3] + c[5]
             work += f32(-(-n // c[0]) * -(-t // c[1])) / f32(256) * full
             alone, longest, fixed = max(alone, steps * c[2] + c[5]), max(longest, full), max(fixed, c[4])
-        us = factor * (fixed + max(alone, work + f32(0.3) * longest))
+        us = factor * (fixed + max(alone, work + f32(0.2) * longest))
         if us < best_us:
             best, best_us = i, us
     return best

@@ -8,9 +8,10 @@ import bf16_cases as bc
 @pytest.mark.parametrize("kind,adapters", [("MAT_NT", False), ("MAT_NT", True), ("MAT_GATED", False), ("MAT_GATED", True),
                                            ("MAT_NN", False), ("MAT_TN", False)])
 def test_every_tile_has_a_shape(kind, adapters):
-    tiles = bc.TILES[kind][:9] if adapters else bc.TILES[kind]
-    assert len(bc.RINGS) == 10 and len(tiles) == (9 if adapters or kind == "MAT_GATED" else 10)
-    assert set(bc.shapes(kind, adapters)) == set(range(len(tiles)))
+    tiles = bc.TILES[kind][:11] if adapters else bc.TILES[kind]
+    assert len(bc.RINGS) == 12 and len(tiles) == (11 if adapters or kind == "MAT_GATED" else 12)
+    built = {i for i, t in enumerate(tiles) if t[2] < 9}     # (a row of nines: not built for this kind)
+    assert len(built) >= len(tiles) - 1 and set(bc.shapes(kind, adapters)) == built
 
 
 def test_every_pair_has_a_shape():
