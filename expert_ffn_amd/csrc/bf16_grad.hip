@@ -21,8 +21,8 @@ static hipError_t pair(const MatBf16Params& p, const MatBf16Params& r, hipStream
 
 // Both gradients in one launch, or one after the other: the smaller estimate.  In one
 // launch the workgroups of both fill the CUs together: the sum of their times over the
-// CUs, 0.2 of the longer one's for the uneven end, times a factor of the tile, fitted
-// to 91 shapes (T 16 to 8192) with seven tiles.  The choice is 2.2 % slower than the best of
+// CUs, 0.4 of the longer one's for the uneven end, times a factor of the tile, fitted
+// to 91 shapes (T 16 to 8192) with six tiles.  The choice is 2.5 % slower than the best of
 // eleven tiles and two launches on average, two launches always 36 %.  T = 333, 1408 x
 // 1424: 10.5 us in one launch, 14.2 in two; T = 43, 184 x 536: 3.4 and 6.2; T = 858, 5344 x
 // 2032: 51.7 and 59.3; T = 2009, 312 x 1976: 20.6 and 19.8.
@@ -30,7 +30,7 @@ struct PairTile {
     int tile;   // of Bf16Tiles
     float factor;
 };
-constexpr PairTile PAIR_TILES[] = {{0, 1.1f}, {1, 1.15f}, {3, 1.05f}, {4, 1.25f}, {7, 1.1f}, {8, 1.05f}, {9, 1.0f}};
+constexpr PairTile PAIR_TILES[] = {{0, 0.8f}, {1, 0.8f}, {3, 0.9f}, {7, 1.0f}, {8, 1.0f}, {9, 1.0f}};
 
 static int pick_pair(const MatBf16Params& p, const MatBf16Params& r) {
     int best = -1;
@@ -51,7 +51,7 @@ static int pick_pair(const MatBf16Params& p, const MatBf16Params& r) {
         add(Bf16Tiles<MAT_NN>::T[c.tile], p);
         add(Bf16Tiles<MAT_TN>::T[c.tile], r);
         if (groups >= (1 << 22)) continue;   // keeps every launch below 2^32 threads
-        const float us = c.factor * (fixed + std::max(alone, work + 0.2f * longest));
+        const float us = c.factor * (fixed + std::max(alone, work + 0.4f * longest));
         if (us < best_us) {
             best_us = us;
             best = c.tile;
@@ -65,10 +65,9 @@ hipError_t launch_matmul_bf16_pair(const MatBf16Params& p, const MatBf16Params& 
         case 0: return pair<32, 32, 1, 1, 3, 4>(p, r, s);
         case 1: return pair<64, 32, 2, 1, 3, 4>(p, r, s);
         case 3: return pair<64, 64, 2, 2, 3, 1>(p, r, s);
-        case 4: return pair<64, 96, 2, 2, 3, 2>(p, r, s);
         case 7: return pair<128, 128, 2, 2, 3, 1>(p, r, s);
         case 8: return pair<128, 192, 2, 4, 3, 1>(p, r, s);
-        case 9: return pair<192, 192, 2, 4, 3, 1>(p, r, s);
+        case 9: return pair<192, 192, 2, 2, 3, 1>(p, r, s);
     }
     const hipError_t e = tiles_nn(p, s);
     return e == hipSuccess ? tiles_tn(r, s) : e;

@@ -565,8 +565,9 @@ static hipError_t bf16_tile(const MatBf16Params& p, hipStream_t s) {
 // A tile's LDS reads a step, (BN / 16 * WT + BT / 16 * WN) KB at 128 bytes a cycle, take longer
 // than its MFMA where the waves' parts are small: 128 x 128 in four waves of 64 x 64 takes 33
 // us at T = 1024, N = 2816, K = 4224, NN, in eight 40.  192 x 192 is there for three stages of
-// copies under 160 KB (gated T = 2048, 2 x 2112 x 2816: 42 us, 256 x 192 48, 128 x 192 54).
-// Gated 256 x 256 does not fit the registers (T = 4096: 152 us, 192 x 192 85).
+// copies under 160 KB (gated T = 2048, 2 x 2112 x 2816: 42 us, 256 x 192 48, 128 x 192 54);
+// where operands are read by columns it has four waves (T = N = K = 4096, NN: 120 us, in
+// eight 126).
 struct Bf16Tile {
     int bn, bt;
     float alone, full, fixed, end;
@@ -576,38 +577,38 @@ struct Bf16Tiles;
 template <>
 struct Bf16Tiles<MAT_NT> {
     static constexpr Bf16Tile T[] = {
-        {32, 32, 0.077f, 0.090f, 1.07f, 2.17f},  {64, 32, 0.135f, 0.145f, 0.91f, 2.51f},  {64, 64, 0.100f, 0.213f, 0.54f, 2.90f},
-        {64, 64, 0.233f, 0.220f, 2.44f, 0.52f},  {64, 96, 0.240f, 0.240f, 0.47f, 4.06f},  {96, 96, 0.113f, 0.206f, 0.77f, 8.33f},
-        {128, 64, 0.194f, 0.243f, 0.17f, 6.29f}, {128, 128, 0.398f, 0.412f, 0.52f, 5.56f}, {128, 192, 0.566f, 0.566f, 2.57f, 2.79f},
-        {192, 192, 0.617f, 0.617f, 4.72f, 4.78f}, {256, 192, 0.961f, 0.967f, 0.00f, 7.65f}, {256, 256, 1.052f, 1.052f, 5.01f, 5.49f},
+        {32, 32, 0.074f, 0.087f, 1.25f, 2.10f},  {64, 32, 0.142f, 0.145f, 0.99f, 2.45f},  {64, 64, 0.205f, 0.213f, 0.70f, 2.84f},
+        {64, 64, 0.236f, 0.220f, 2.47f, 0.51f},  {64, 96, 0.231f, 0.252f, 1.06f, 3.42f},  {96, 96, 0.209f, 0.240f, 3.74f, 4.88f},
+        {128, 64, 0.111f, 0.263f, 1.87f, 4.45f}, {128, 128, 0.401f, 0.441f, 1.57f, 4.32f}, {128, 192, 0.586f, 0.587f, 0.00f, 5.31f},
+        {192, 192, 0.691f, 0.691f, 4.04f, 4.53f}, {256, 192, 0.994f, 1.014f, 0.00f, 7.44f}, {256, 256, 1.060f, 1.100f, 0.00f, 10.20f},
     };
 };
 template <>
 struct Bf16Tiles<MAT_GATED> {
     static constexpr Bf16Tile T[] = {
-        {32, 32, 0.112f, 0.102f, 1.26f, 1.94f},  {64, 32, 0.183f, 0.168f, 0.94f, 2.18f},  {64, 64, 0.244f, 0.251f, 0.75f, 2.36f},
-        {64, 64, 0.270f, 0.225f, 2.02f, 0.58f},  {64, 96, 0.285f, 0.293f, 0.60f, 3.19f},  {96, 96, 0.154f, 0.298f, 0.06f, 6.83f},
-        {128, 64, 0.252f, 0.308f, 0.25f, 5.13f}, {128, 128, 0.380f, 0.484f, 0.00f, 5.01f}, {128, 192, 0.596f, 0.597f, 0.00f, 5.06f},
-        {192, 192, 0.750f, 0.750f, 0.01f, 7.28f}, {256, 192, 1.077f, 1.081f, 0.00f, 6.24f},
+        {32, 32, 0.111f, 0.097f, 1.24f, 2.00f},  {64, 32, 0.183f, 0.157f, 0.83f, 2.31f},  {64, 64, 0.248f, 0.235f, 0.68f, 2.50f},
+        {64, 64, 0.270f, 0.211f, 1.97f, 0.64f},  {64, 96, 0.298f, 0.267f, 0.40f, 3.39f},  {96, 96, 0.297f, 0.271f, 0.21f, 6.76f},
+        {128, 64, 0.306f, 0.295f, 0.37f, 5.07f}, {128, 128, 0.487f, 0.467f, 0.00f, 5.09f}, {128, 192, 0.609f, 0.611f, 0.00f, 5.05f},
+        {192, 192, 0.751f, 0.763f, 0.00f, 7.31f}, {256, 192, 1.100f, 1.069f, 0.00f, 6.19f}, {256, 256, 1.252f, 1.255f, 0.00f, 8.23f},
     };
 };
 template <>
 struct Bf16Tiles<MAT_NN> {
     static constexpr Bf16Tile T[] = {
-        {32, 32, 0.086f, 0.145f, 1.17f, 1.50f},  {64, 32, 0.137f, 0.186f, 0.95f, 1.85f},  {64, 64, 0.038f, 0.242f, 0.55f, 2.21f},
-        {64, 64, 0.268f, 0.222f, 2.04f, 0.48f},  {64, 96, 0.174f, 0.287f, 0.50f, 2.73f},  {96, 96, 0.264f, 0.316f, 0.19f, 4.14f},
-        {128, 64, 0.019f, 0.302f, 0.36f, 3.59f}, {128, 128, 0.350f, 0.445f, 0.00f, 3.66f}, {128, 192, 0.425f, 0.588f, 0.00f, 3.93f},
-        {192, 192, 0.768f, 0.769f, 0.00f, 4.53f}, {256, 192, 0.964f, 0.989f, 0.00f, 4.18f}, {256, 256, 1.087f, 1.136f, 0.00f, 5.17f},
+        {32, 32, 0.052f, 0.143f, 1.22f, 1.53f},  {64, 32, 0.135f, 0.186f, 0.88f, 1.88f},  {64, 64, 0.239f, 0.242f, 0.49f, 2.29f},
+        {64, 64, 0.269f, 0.220f, 1.97f, 0.54f},  {64, 96, 0.046f, 0.296f, 0.26f, 2.84f},  {96, 96, 0.235f, 0.321f, 0.04f, 4.28f},
+        {128, 64, 0.296f, 0.305f, 0.27f, 3.70f}, {128, 128, 0.300f, 0.463f, 0.00f, 3.59f}, {128, 192, 0.499f, 0.609f, 0.00f, 3.88f},
+        {192, 192, 0.751f, 0.751f, 0.00f, 5.61f}, {256, 192, 0.926f, 1.026f, 0.00f, 4.04f}, {256, 256, 1.065f, 1.181f, 0.00f, 4.97f},
     };
 };
 template <>
 struct Bf16Tiles<MAT_TN> {
     // (64 x 64 with two K groups is never the fastest here: not built)
     static constexpr Bf16Tile T[] = {
-        {32, 32, 0.164f, 0.177f, 1.21f, 1.42f},  {64, 32, 0.197f, 0.211f, 1.05f, 1.86f},  {64, 64, 9.0f, 9.0f, 9.0f, 9.0f},
-        {64, 64, 0.255f, 0.225f, 2.16f, 0.44f},  {64, 96, 0.294f, 0.307f, 0.98f, 2.37f},  {96, 96, 0.317f, 0.345f, 0.85f, 3.43f},
-        {128, 64, 0.297f, 0.324f, 0.98f, 3.01f}, {128, 128, 0.360f, 0.458f, 0.42f, 3.07f}, {128, 192, 0.614f, 0.653f, 0.00f, 3.59f},
-        {192, 192, 0.817f, 0.819f, 0.00f, 4.04f}, {256, 192, 0.995f, 0.995f, 0.00f, 4.43f}, {256, 256, 1.088f, 1.136f, 0.00f, 5.12f},
+        {32, 32, 0.153f, 0.176f, 1.25f, 1.43f},  {64, 32, 0.205f, 0.209f, 1.08f, 1.88f},  {64, 64, 9.0f, 9.0f, 9.0f, 9.0f},
+        {64, 64, 0.253f, 0.223f, 2.22f, 0.42f},  {64, 96, 0.101f, 0.307f, 1.03f, 2.37f},  {96, 96, 0.242f, 0.347f, 0.77f, 3.53f},
+        {128, 64, 0.008f, 0.324f, 0.95f, 3.08f}, {128, 128, 0.440f, 0.465f, 0.16f, 3.32f}, {128, 192, 0.614f, 0.663f, 0.00f, 3.55f},
+        {192, 192, 0.671f, 0.776f, 0.00f, 5.51f}, {256, 192, 1.014f, 1.015f, 0.00f, 4.43f}, {256, 256, 1.096f, 1.158f, 0.00f, 5.09f},
     };
 };
 
@@ -621,8 +622,8 @@ static float bf16_tile_us(const Bf16Tile& c, int64_t T, int64_t rows, int K) {
 
 template <int KIND, bool AD>
 static int pick_bf16_tile(int64_t T, int64_t rows, int K) {
-    // (256 x 256 with adapters does not fit the registers either)
-    constexpr int n = KIND == MAT_NT && AD ? 11 : sizeof(Bf16Tiles<KIND>::T) / sizeof(Bf16Tile);
+    // (256 x 256 with adapters does not fit the registers)
+    constexpr int n = sizeof(Bf16Tiles<KIND>::T) / sizeof(Bf16Tile) - AD;
     int best = n - 1;
     float best_us = 1e30f;
     for (int i = 0; i < n; ++i) {
@@ -649,10 +650,10 @@ static hipError_t bf16_tiles(const MatBf16Params& p, hipStream_t s) {
         case 6: return bf16_tile<KIND, AD, 128, 64, 2, 1, 3, 2>(p, s);
         case 7: return bf16_tile<KIND, AD, 128, 128, 2, 2, 3, 1>(p, s);
         case 8: return bf16_tile<KIND, AD, 128, 192, 2, 4, 3, 1>(p, s);
-        case 9: return bf16_tile<KIND, AD, 192, 192, 2, 4, 3, 1>(p, s);
+        case 9: return bf16_tile<KIND, AD, 192, 192, 2, KIND == MAT_NN || KIND == MAT_TN ? 2 : 4, 3, 1>(p, s);
         case 10: return bf16_tile<KIND, AD, 256, 192, AD ? 2 : 4, AD ? 4 : 2, 2, 1>(p, s);   // (64 tokens of a wave at most)
     }
-    if constexpr (KIND != MAT_GATED && !AD) return bf16_tile<KIND, AD, 256, 256, 4, 2, 2, 1>(p, s);
+    if constexpr (!AD) return bf16_tile<KIND, AD, 256, 256, 4, 2, 2, 1>(p, s);
     return hipErrorInvalidValue;   // not reached
 }
 

@@ -25,6 +25,7 @@ TILES = {k: _table(k) for k in KINDS}
 # stages and K groups of the tiles in the same order
 RINGS = [(int(s), int(g)) for s, g in re.findall(r"return bf16_tile<KIND, AD, \d+, \d+, [^;]*?(\d), (\d)>\(p, s\)", _TILE)]
 PAIR = [(int(i), f32(f)) for i, f in re.findall(r"\{(\d), ([\d.]+)f\}", _GRAD[_GRAD.index("PAIR_TILES[]"):].split("};")[0])]
+_END = f32(re.search(r"work \+ ([\d.]+)f \* longest", _GRAD).group(1))
 _PAIR_RINGS = {int(c): (int(s), int(g)) for c, s, g in re.findall(r"case (\d): return pair<\d+, \d+, \d, \d, (\d), (\d)>", _GRAD)}
 
 
@@ -51,7 +52,7 @@ def pick_pair(T, N, K):
             full = steps * c[3] + c[5]
             work += f32(-(-n // c[0]) * -(-t // c[1])) / f32(256) * full
             alone, longest, fixed = max(alone, steps * c[2] + c[5]), max(longest, full), max(fixed, c[4])
-        us = factor * (fixed + max(alone, work + f32(0.2) * longest))
+        us = factor * (fixed + max(alone, work + _END * longest))
         if us < best_us:
             best, best_us = i, us
     return best

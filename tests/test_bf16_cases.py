@@ -9,7 +9,7 @@ import bf16_cases as bc
                                            ("MAT_NN", False), ("MAT_TN", False)])
 def test_every_tile_has_a_shape(kind, adapters):
     tiles = bc.TILES[kind][:11] if adapters else bc.TILES[kind]
-    assert len(bc.RINGS) == 12 and len(tiles) == (11 if adapters or kind == "MAT_GATED" else 12)
+    assert len(bc.RINGS) == 12 and len(tiles) == (11 if adapters else 12)
     built = {i for i, t in enumerate(tiles) if t[2] < 9}     # (a row of nines: not built for this kind)
     assert len(built) >= len(tiles) - 1 and set(bc.shapes(kind, adapters)) == built
 
