@@ -12,6 +12,7 @@ constexpr int32_t K_MAX = 1 << 20;
 constexpr int64_t LD_MAX = 1ll << 21;   // row stride of a tile's operand: 256 rows below 2 GiB
 constexpr int32_t ROWS_MAX = 1 << 24;
 constexpr int32_t RANK_MAX = 1024;
+constexpr int64_t OUT_MAX = 1ll << 36;  // elements of a result: every launch below 2^32 threads
 
 // an operand of the tiles: bf16 rows in 16-byte pieces
 moe_status check_operand(const char* fn, const char* name, const void* p, int64_t ld, int64_t cols) {
@@ -34,7 +35,7 @@ moe_status check_sizes(const char* fn, const char* name, int32_t T, int32_t N, i
     if (T < 0 || T > ROWS_MAX) return fail(MOE_E_SHAPE, fn, "T=%d outside [0, 2^24]", T);
     if (N < 1 || N > ROWS_MAX) return fail(MOE_E_SHAPE, fn, "%s=%d outside [1, 2^24]", name, N);
     if (K < 8 || K % 8 || K > K_MAX) return fail(MOE_E_SHAPE, fn, "K=%d is not a multiple of 8 in [8, 2^20]", K);
-    if (static_cast<int64_t>(T) * N > (1ll << 36)) return fail(MOE_E_SHAPE, fn, "T=%d %s=%d too large (T*%s <= 2^36)", T, name, N, name);
+    if (static_cast<int64_t>(T) * N > OUT_MAX) return fail(MOE_E_SHAPE, fn, "T=%d %s=%d too large (T*%s <= 2^36)", T, name, N, name);
     return MOE_OK;
 }
 bool act_ok(int32_t act) { return act == MOE_ACT_GELU_TANH || act == MOE_ACT_SILU; }
@@ -111,11 +112,15 @@ struct Gradients {
 moe_status check_gradients(const char* fn, const Gradients& g) {
     moe_status st;
     if (g.dx) {
+        if (static_cast<int64_t>(g.T) * g.K > OUT_MAX)
+            return fail(MOE_E_SHAPE, fn, "T=%d K=%d of dx too large (T*K <= 2^36)", g.T, g.K);
         if (g.T > 0 && !g.w) return fail(MOE_E_ARG, fn, "null pointer argument");
         if ((st = check_operand(fn, "w", g.w, g.ldw, g.K)) != MOE_OK) return st;
         if ((st = check_result(fn, "dx", g.dx, g.dx_dt, g.T, g.lddx, g.K)) != MOE_OK) return st;
     }
     if (g.dw) {
+        if (static_cast<int64_t>(g.M) * g.K > OUT_MAX)
+            return fail(MOE_E_SHAPE, fn, "%d rows and K=%d of dw too large (rows * K <= 2^36)", g.M, g.K);
         if (g.T > 0 && !g.x) return fail(MOE_E_ARG, fn, "null pointer argument");
         if ((st = check_operand(fn, "x", g.x, g.ldx, g.K)) != MOE_OK) return st;
         if ((st = check_result(fn, "dw", g.dw, g.dw_dt, g.M, g.lddw, g.K)) != MOE_OK) return st;

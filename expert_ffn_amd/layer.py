@@ -112,6 +112,8 @@ class Adapters:
     A request's tokens carry its slot's number; a slot that is not loaded has rank 0 and adds nothing."""
 
     def __init__(self, n, R, H, FF, device="cuda"):
+        if n < 1 or R < 8 or R > 1024 or R % 8:
+            raise ValueError(f"n={n} is not positive, or R={R} not a multiple of 8 in [8, 1024]")
         bf16 = dict(dtype=torch.bfloat16, device=device)
         self.n, self.R, self.H, self.FF = n, R, H, FF
         self.a13, self.b13 = torch.zeros((n, 2, R, H), **bf16), torch.zeros((n, 2 * FF, R), **bf16)
@@ -212,7 +214,7 @@ class MoeBlock:
         # enough for fewer tokens too: their slices of H are as many or fewer
         self.router_ws = torch.empty(max(router_ws_bytes(T, H, layer.E), 256), dtype=torch.uint8, device=d)
         self.x_next = torch.empty((T, H), dtype=bf16, device=d) if w_next is not None else None
-        self.codes = isinstance(dense, DenseExpert)
+        self.codes = dense is not None and not isinstance(dense, DenseExpertBf16)
         if dense is not None:
             self.hid = torch.empty((T, dense.FF), dtype=bf16, device=d)
             self.yd = torch.empty((T, H), dtype=bf16, device=d)

@@ -560,13 +560,13 @@ moe_status moe_gated_matmul_i8(const int8_t* xq, int64_t ldx, const float* x_sca
  *   sum over j < rank of s[t][j] * b[a][n][j]     a = adapter_ids[t], rank = ranks[a]
  * to the sum of channel n (gated: of gate channel f with s[t][j] and row f of b[a], of
  * up channel f with s[t][R + j] and row F + f), before the activation.
- *   s    device bf16 [T, R] (gated [T, 2R]): moe_adapter_shrink's
+ *   s    device bf16 [T, R] (gated [T, 2R]): moe_adapter_shrink's, zeros past the rank
  *   adapter_ids device int32 [T]; outside [0, n_adapters): no adapter
  *   b    device bf16: adapter a's [N, R] (gated [2F, R]) contiguous at b + a * b_stride
  *   ranks device int32 [n_adapters] or NULL: R of all; values outside [0, R] count as
  *        the nearest of the two
  * A token's row depends on its own adapter only (the order of its fp32 sums also on the
- * adapters of the tokens around it); what lies past a rank is not used.
+ * adapters of the tokens around it); what b holds past a rank is not used.
  *
  * K a multiple of 8 up to 2^20; rows of x, w and s 16-byte aligned with strides up to
  * 2^21 elements; R a multiple of 8 up to 1024, b 16-byte aligned and b_stride a
@@ -608,7 +608,7 @@ moe_status moe_adapter_shrink(const void* x, int64_t ldx, int32_t T, int32_t K, 
  * dw are those of the rounded values; sums are fp32 in a fixed order, rounded once.  w is
  * read for dx only, x for dw only: the other may be NULL where its result is not wanted.
  * N (F) and K multiples of 8; rows of x, w, dout, pre and dpre 16-byte aligned with
- * strides up to 2^21 elements.  T = 0 writes zeros into dw.
+ * strides up to 2^21 elements; dx and dw of up to 2^36 elements.  T = 0 writes zeros into dw.
  */
 moe_status moe_matmul_bf16_backward(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* dout, int64_t ldd,
                                     int32_t T, int32_t N, int32_t K, void* dx, int32_t dx_dtype, int64_t lddx, void* dw,

@@ -127,6 +127,16 @@ def test_backward_refusals(L, name, spec):  # noqa: F811
     r(1, "overlap", dx=A[6])
 
 
+@pytest.mark.parametrize("name,spec,half", [("moe_matmul_bf16_backward", MMB, 1), ("moe_gated_matmul_bf16_backward", GMB, 2)])
+def test_backward_refuses_gradients_that_no_launch_takes(L, name, spec, half):  # noqa: F811
+    """Before the activation's gradient is enqueued: dx or dw of more than 2^36 elements."""
+    r = lambda text, **kw: refused(L, name, spec, 2, text, **kw)
+    K = 1 << 17
+    wide = dict(K=K, ldx=K, ldw=K, lddx=K, lddw=K)
+    r("of dx too large", T=(1 << 19) + 1, **wide)
+    r("of dw too large", N=(1 << 19) // half + 8, ldd=1 << 20, dx=None, **wide, **(dict(ldp=1 << 21, ldg=1 << 21) if half == 2 else {}))
+
+
 def test_binding_refusals(L):  # noqa: F811
     """Tensors on the host, and arguments that do not go together."""
     x, w, y = (torch.zeros(s, dtype=torch.bfloat16) for s in ((4, 64), (32, 64), (4, 32)))
@@ -138,3 +148,45 @@ def test_binding_refusals(L):  # noqa: F811
             f(*a, nothing=1)
         with pytest.raises(TypeError, match="missing"):
             f(x)
+
+
+def test_experts_and_adapters_refuse_what_does_not_fit(L):  # noqa: F811
+    from expert_ffn_amd.layer import Adapters, DenseExpertBf16
+    H, FF = 128, 64
+    n = L.expert_bytes(L.W_BF16, H, FF)
+    blob = torch.zeros(n, dtype=torch.uint8)
+    e = DenseExpertBf16(blob, H, FF, adapters=Adapters(3, 16, H, FF, "cpu"))
+    assert e.w13.shape == (2 * FF, H) and e.w2.shape == (H, FF)
+    for bad in (blob[:n - 1], blob.view(torch.int8), torch.zeros(2 * n, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous bytes"):
+            DenseExpertBf16(bad, H, FF)
+    with pytest.raises(ValueError, match="the adapters have"):
+        DenseExpertBf16(blob, H, FF, adapters=Adapters(3, 16, H, FF + 8, "cpu"))
+    for n_, R in ((0, 16), (3, 0), (3, 12), (3, 1032)):
+        with pytest.raises(ValueError, match="R="):
+            Adapters(n_, R, H, FF, "cpu")
+    parts = lambda r, F=FF: [torch.ones(s) for s in ((2, r, H), (2 * F, r), (r, F), (H, r))]
+    with pytest.raises(ValueError, match="slot 3"):
+        e.adapters.load(3, *parts(16))
+    for p in (parts(17), parts(8, FF + 8), [parts(8)[0], *parts(4)[1:]]):
+        with pytest.raises(ValueError, match="do not fit"):
+            e.adapters.load(0, *p)
+    assert not e.adapters.ranks.any()
+    e.adapters.load(1, *parts(5), scale=0.5)
+    assert e.adapters.ranks.tolist() == [0, 5, 0] and e.adapters.scale.tolist() == [1.0, 0.5, 1.0]
+    assert e.adapters.a2[1, :5].all() and not e.adapters.a2[1, 5:].any()
+
+
+def test_block_takes_other_experts_as_before(L):  # noqa: F811
+    """A dense expert of the user's own, with DenseExpert's members, is one in 8 bits."""
+    from expert_ffn_amd.layer import DenseExpert, DenseExpertBf16, MoeBlock, MoeLayer
+
+    class Own:
+        H, FF = 128, 64
+
+    blob = lambda fmt: torch.zeros(L.expert_bytes(fmt, 128, 64), dtype=torch.uint8)
+    make = lambda d: MoeBlock(MoeLayer(8, 2, 128, 64, L.W_BF16, 4, device="cpu"), torch.zeros(128), torch.zeros(8, 128), dense=d)
+    for dense, codes in ((Own(), True), (DenseExpert(blob(L.W_INT8_ROW), 128, 64), True), (DenseExpertBf16(blob(L.W_BF16), 128, 64), False),
+                         (None, False)):
+        b = make(dense)
+        assert b.codes == codes and hasattr(b, "xq") == codes and b.low is None
