@@ -4,6 +4,10 @@
 // another before the sums are added.  MFMA 16x16x32: lane l holds row l & 15, chunk
 // 4 s + (l >> 4) of both operands; swz16 spreads the rows that are read together over
 // all banks.
+//
+// Bound by memory: T = 1, 2 x 2112 x 2816 reads 23.8 MB in 5.6 to 6.3 us (3.8 to 4.2 TB/s), of
+// which an empty launch is 1.6; T = 16 8.5 us, with 16 adapters of 2 x 16 ranks
+// among them 10.9.
 #include "bf16_tile.h"
 
 namespace moe {
