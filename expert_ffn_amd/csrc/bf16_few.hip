@@ -70,7 +70,7 @@ __global__ __launch_bounds__(64 * KG) void matmul_bf16_few_kernel(MatBf16Params 
     // have once.  The first ones are requested here, behind the first copies.  Each
     // adapter's product is taken from zero and added in the lanes of its own tokens only,
     // so that no value of one adapter, an infinity or NaN included, meets another
-    // request's row.
+    // request's row, and none of one half the other's sums.
     constexpr int H = GATED ? 2 : 1, NI = 8, LOADS = H * (TT + NI);
     static_assert(CPS * (NSTG - 1) + LOADS <= 63, "loads in flight");
     int rank_l = p.ad.R, aid[TT];              // the token's rank; the adapters of this lane's columns
@@ -169,10 +169,12 @@ __global__ __launch_bounds__(64 * KG) void matmul_bf16_few_kernel(MatBf16Params 
                 }
 #pragma unroll
                 for (int j = 0; j < TT; ++j) {
-                    f32x4 low = {};
+                    f32x4 low[H];
 #pragma unroll
-                    for (int h = 0; h < H; ++h) low = mfma16x16x32(va[n][h], vb[j][h], low);
-                    if (aid[j] == ia[n]) acc[j] += low;
+                    for (int h = 0; h < H; ++h) low[h] = mfma16x16x32(va[n][h], vb[j][h], f32x4{0, 0, 0, 0});
+                    // gated: D rows 0 .. 7 are gate's, 8 .. 15 up's; zeros in the other half's
+                    // rows of A do not keep its infinities out, so each half has its own product
+                    if (aid[j] == ia[n]) acc[j] += q < 2 ? low[0] : low[H - 1];
                 }
             }
             if (at >= count) {   // the next 32 ranks, of the adapters that have them
