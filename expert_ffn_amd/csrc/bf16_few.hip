@@ -162,7 +162,8 @@ __global__ __launch_bounds__(64 * KG) void matmul_bf16_few_kernel(MatBf16Params 
 #pragma unroll
             for (int n = 0; n < NI; ++n) {
                 if (ia[n] < 0) continue;
-                const int rank = __builtin_amdgcn_readlane(rank_l, __builtin_ctzll(__ballot(id_l == ia[n])));
+                // (at least 0, so that the lanes' differences stay inside 32 bits)
+                const int rank = max(__builtin_amdgcn_readlane(rank_l, __builtin_ctzll(__ballot(id_l == ia[n]))), 0);
                 if (rank < k0 + 32) {   // some lane holds less than 8 ranks
 #pragma unroll
                     for (int h = 0; h < H; ++h) va[n][h] = low_ranks(va[n][h], rank - k0 - 8 * q);
