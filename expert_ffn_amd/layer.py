@@ -154,7 +154,8 @@ class DenseExpertBf16:
 
     def run(self, x, hid, y, pre=None, low=None, adapter_ids=None, stream=None):
         """hid [T, FF] = act(gate) up of x [T, H], y [T, H] = hid . w2.  pre [T, 2FF] takes the sums of gate and up for
-        backward(); adapter_ids [T] the tokens' slots, with low [T, 2R] for the adapters' first products."""
+        backward(); adapter_ids [T] the tokens' slots, with low [T, 2R] for the adapters' first products.  Not both:
+        the backward pass has no adapters."""
         more, more2 = {}, {}
         if adapter_ids is not None:
             a = self.adapters
@@ -162,6 +163,8 @@ class DenseExpertBf16:
                 raise ValueError("adapter_ids are given, but the expert has no adapters")
             if low is None:
                 raise ValueError("adapter_ids need low")
+            if pre is not None:
+                raise ValueError("pre goes with a pass without adapters: backward() has none of their terms")
             low2 = low[:, :a.R]   # reused behind gate and up
             ops.adapter_shrink(x, adapter_ids, a.a13, a.scale, low, ranks=a.ranks, stream=stream)
             more = dict(s=low, adapter_ids=adapter_ids, b=a.b13, ranks=a.ranks)
@@ -173,8 +176,9 @@ class DenseExpertBf16:
         return y
 
     def backward(self, x, pre, hid, dy, dhid, dpre, dx=None, dw13=None, dw2=None, stream=None):
-        """Gradients of run() without adapters, from what it read and stored and dy [T, H]: dhid [T, FF] and dpre
-        [T, 2FF] (may be pre) on the way, dx [T, H], dw13 and dw2 where they are wanted."""
+        """Gradients of run() without adapters, from what it read and stored (pre and hid of one call without adapter_ids)
+        and dy [T, H]: dhid [T, FF] and dpre [T, 2FF] (may be pre) on the way, dx [T, H], dw13 and dw2 where they are
+        wanted.  dhid and dpre are bf16, so dx and dw13 carry their rounding in fp32 too."""
         ops.matmul_bf16_backward(hid, self.w2, dy, dx=dhid, dw=dw2, stream=stream)
         ops.gated_matmul_bf16_backward(x, self.w13, self.act, pre, dhid, dpre, dx=dx, dw=dw13, stream=stream)
 

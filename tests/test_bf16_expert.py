@@ -1,0 +1,26 @@
+"""The dense expert in bf16 and its adapters without a GPU: what run() and load() refuse or leave alone."""
+import pytest
+import torch
+
+from test_block_abi import L  # noqa: F401  (the fixture)
+
+H, FF, T = 128, 64, 4
+
+
+def expert(L, adapters=None):  # noqa: F811
+    from expert_ffn_amd.layer import DenseExpertBf16
+    return DenseExpertBf16(torch.zeros(L.expert_bytes(L.W_BF16, H, FF), dtype=torch.uint8), H, FF, adapters=adapters)
+
+
+def test_sums_for_the_backward_pass_are_refused_with_adapters(L):  # noqa: F811
+    """backward() has no adapter terms: run() does not store the sums of a pass with adapters for it."""
+    from expert_ffn_amd.layer import Adapters
+    new = lambda c, dt=torch.bfloat16: torch.zeros(T, c, dtype=dt)
+    x, hid, y, pre, low, ids = new(H), new(FF), new(H), new(2 * FF), new(32), torch.zeros(T, dtype=torch.int32)
+    e = expert(L, Adapters(3, 16, H, FF, "cpu"))
+    with pytest.raises(ValueError, match="pre goes with a pass without adapters"):
+        e.run(x, hid, y, pre=pre, low=low, adapter_ids=ids)
+    # either alone passes these checks (and ends at the tensors, which are on the host)
+    for more in (dict(pre=pre), dict(low=low, adapter_ids=ids), dict(pre=pre, low=low)):
+        with pytest.raises(ValueError, match="x is on cpu"):
+            e.run(x, hid, y, **more)
