@@ -121,6 +121,7 @@ class Adapters:
         self.scale = torch.ones(n, dtype=torch.float32, device=device)
         self.ranks = torch.zeros(n, dtype=torch.int32, device=device)
 
+    @torch.no_grad()   # the pools keep no graph of parameters that are loaded
     def load(self, slot, a13, b13, a2, b2, scale=1.0):
         """a13 [2, r, H] (gate, up), b13 [2FF, r], a2 [r, FF], b2 [H, r] into a slot, on the current stream."""
         r = a2.shape[0]

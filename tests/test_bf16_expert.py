@@ -24,3 +24,17 @@ def test_sums_for_the_backward_pass_are_refused_with_adapters(L):  # noqa: F811
     for more in (dict(pre=pre), dict(low=low, adapter_ids=ids), dict(pre=pre, low=low)):
         with pytest.raises(ValueError, match="x is on cpu"):
             e.run(x, hid, y, **more)
+
+
+def test_loaded_adapters_leave_no_graph(L):  # noqa: F811
+    """Adapters are often parameters of a training program: the pools stay plain buffers."""
+    from expert_ffn_amd.layer import Adapters
+    a = Adapters(2, 16, H, FF, "cpu")
+    parts = [torch.nn.Parameter(torch.full(s, 0.5)) for s in ((2, 8, H), (2 * FF, 8), (8, FF), (H, 8))]
+    scale = torch.tensor(2.0, requires_grad=True)
+    for slot in (1, 0, 1):
+        a.load(slot, *parts, scale=scale * 3)
+    for t in (a.a13, a.b13, a.a2, a.b2, a.scale, a.ranks):
+        assert not t.requires_grad and t.grad_fn is None
+    assert a.ranks.tolist() == [8, 8] and a.scale.tolist() == [6.0, 6.0]
+    assert (a.b13[1, :, :8] == 0.5).all() and not a.b13[1, :, 8:].any()
