@@ -227,7 +227,7 @@ class MoeBlock:
             self.xq = torch.empty((T, H), dtype=torch.int8, device=d)
             self.hq = torch.empty((T, dense.FF), dtype=torch.int8, device=d)
             self.xs, self.hs = (torch.empty(T, dtype=f32, device=d) for _ in range(2))
-        a = getattr(dense, "adapters", None)
+        a = dense.adapters if isinstance(dense, DenseExpertBf16) else None
         self.low = torch.empty((T, 2 * a.R), dtype=bf16, device=d) if a is not None else None
 
     def run_dense(self, T, stream=None, adapter_ids=None):

@@ -38,3 +38,23 @@ def test_loaded_adapters_leave_no_graph(L):  # noqa: F811
         assert not t.requires_grad and t.grad_fn is None
     assert a.ranks.tolist() == [8, 8] and a.scale.tolist() == [6.0, 6.0]
     assert (a.b13[1, :, :8] == 0.5).all() and not a.b13[1, :, 8:].any()
+
+
+def block(L, dense):  # noqa: F811
+    from expert_ffn_amd.layer import MoeBlock, MoeLayer
+    return MoeBlock(MoeLayer(8, 2, H, 64, L.W_BF16, T, device="cpu"), torch.zeros(H), torch.zeros(8, H), dense=dense)
+
+
+def test_block_asks_only_the_bf16_expert_for_adapters(L):  # noqa: F811
+    """A dense expert of the user's own may have any member of that name."""
+    from expert_ffn_amd.layer import Adapters
+
+    class Own:
+        H, FF, adapters = 128, 64, ["of", "its", "own"]
+
+    b = block(L, Own())
+    assert b.codes and b.low is None
+    with pytest.raises(ValueError, match="no adapters"):
+        b.run(torch.zeros(T, H), torch.zeros(T, H), adapter_ids=torch.zeros(T, dtype=torch.int32))
+    assert block(L, expert(L, Adapters(3, 16, H, FF, "cpu"))).low.shape == (T, 32)
+    assert block(L, expert(L)).low is None
