@@ -230,8 +230,13 @@ class MoeBlock:
         a = dense.adapters if isinstance(dense, DenseExpertBf16) else None
         self.low = torch.empty((T, 2 * a.R), dtype=bf16, device=d) if a is not None else None
 
+    def _check_ids(self, adapter_ids):
+        if adapter_ids is not None and self.low is None:
+            raise ValueError("adapter_ids are given, but the dense expert has no adapters")
+
     def run_dense(self, T, stream=None, adapter_ids=None):
         """The dense expert on the rows (or their codes) of the last norm: its rows in yd."""
+        self._check_ids(adapter_ids)
         e = self.dense
         if not self.codes:
             low = self.low[:T] if self.low is not None else None
@@ -243,8 +248,7 @@ class MoeBlock:
 
     def run(self, h, h_out, stream=None, adapter_ids=None):
         """adapter_ids: int32 [T], the slots of the tokens' adapters in the dense expert's pool (outside it: none)."""
-        if adapter_ids is not None and self.low is None:
-            raise ValueError("adapter_ids are given, but the dense expert has no adapters")
+        self._check_ids(adapter_ids)
         if h.shape[0] > self.layer.T_max:
             raise ValueError(f"T={h.shape[0]} exceeds the layer's T_max={self.layer.T_max}")
         if h.shape[0] == 0:

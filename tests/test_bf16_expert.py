@@ -58,3 +58,13 @@ def test_block_asks_only_the_bf16_expert_for_adapters(L):  # noqa: F811
         b.run(torch.zeros(T, H), torch.zeros(T, H), adapter_ids=torch.zeros(T, dtype=torch.int32))
     assert block(L, expert(L, Adapters(3, 16, H, FF, "cpu"))).low.shape == (T, 32)
     assert block(L, expert(L)).low is None
+
+
+def test_run_dense_refuses_ids_that_no_adapter_takes(L):  # noqa: F811
+    """Called by itself, with an expert in 8 bits: the ids were left out without a word."""
+    from expert_ffn_amd.layer import DenseExpert
+    d = DenseExpert(torch.zeros(L.expert_bytes(L.W_INT8_ROW, H, FF), dtype=torch.uint8), H, FF)
+    ids = torch.zeros(T, dtype=torch.int32)
+    for dense in (d, expert(L), None):
+        with pytest.raises(ValueError, match="no adapters"):
+            block(L, dense).run_dense(T, adapter_ids=ids)
