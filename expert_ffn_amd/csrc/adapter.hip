@@ -10,6 +10,11 @@
 // Tokens of other adapters are not read.  MFMA 16x16x32, A = ranks, B = tokens: D columns
 // are tokens, and each adapter's sums are stored for its own tokens only, so nothing of
 // one request meets another's.
+//
+// s is rounded to bf16, the type in which the second product reads it.  With low-rank parts
+// of about 0.4 times the product's size its results differ from 64 bits by 0.0006 to 0.0010 of
+// their norm where they are fp32, and by 0.0018 to 0.0020 where they are bf16 (their own
+// rounding 0.0017).
 #include <algorithm>
 
 #include "bf16_tile.h"

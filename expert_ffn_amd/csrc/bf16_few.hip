@@ -6,8 +6,8 @@
 // all banks.
 //
 // Bound by memory: T = 1, 2 x 2112 x 2816 reads 23.8 MB in 5.6 to 6.3 us (3.8 to 4.2 TB/s), of
-// which an empty launch is 1.6; T = 16 8.5 us, with 16 adapters of 2 x 16 ranks
-// among them 10.9.
+// which an empty launch is 1.6; T = 16 7.0 us, with an adapter of 2 x 16 ranks for each
+// token (of 32) 9.0.
 #include "bf16_tile.h"
 
 namespace moe {
@@ -234,7 +234,7 @@ hipError_t tiles_nn(const MatBf16Params& p, hipStream_t s);
 hipError_t tiles_tn(const MatBf16Params& p, hipStream_t s);
 
 // Up to 16 tokens the kernel for few tokens (T = 1 and 16: 1.1 to 1.8 times as fast as the
-// best tile from 64 to 8192 weight rows, K 136 to 4096: N = 2816, K = 2112 3.8 and 5.9 us).
+// best tile from 64 to 8192 weight rows, K 136 to 4096: N = 2816, K = 2112 3.6 and 3.8 us).
 // Further as long as every workgroup has a CU of its own: to 32 tokens 1.2 to 1.6 times as
 // fast (more workgroups: 5 to 10 % slower), to 48 1.0 to 1.3 times, to 64 as fast with K =
 // 1424, 1.1 to 1.2 times with K up to 1024.  Three stages against two: 4 to 9 % less

@@ -88,7 +88,11 @@ __device__ __forceinline__ void act_and_slope(int act, float g, float* value, fl
 
 // One thread takes 8 channels of one row: 16-byte reads of gate, up and the output's
 // gradient, 16-byte writes of both gradients.  Bound by memory: 10 bytes a channel, T = 8192,
-// F = 4096 54 us (335 MB, 6.2 TB/s: some of it stays in the memory-side cache).
+// F = 4096 53 us (335 MB, 6.3 TB/s: some of it stays in the memory-side cache).
+//
+// dpre is rounded to bf16, the type in which both products read it (a second bf16 term
+// would double their MFMA).  dx and dw differ from 64 bits by 0.0017 of their norm where they
+// are fp32, by 0.0023 where they are bf16, of which their own rounding is 0.0017.
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradParams p) {
     const int f = (blockIdx.x * 256 + threadIdx.x) * 8;
     if (f >= p.F) return;

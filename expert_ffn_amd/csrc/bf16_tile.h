@@ -6,7 +6,8 @@
 //
 // Sums are fp32 in the MFMA's accumulators, in a fixed order; the epilogue is fp32
 // and rounds once to the output type.  Operands are bf16, the MFMA's type: that is why
-// the adapters' s and the gradient of pre, fp32 where they are made, are rounded to it.
+// the adapters' s and the gradient of pre, fp32 where they are made, are rounded to it
+// (what that costs: adapter.hip, bf16_grad.hip).
 //
 // MFMA 16x16x32, A = channels, B = tokens, D column = token, so a lane holds 4
 // consecutive channels of one token.  Long products run at the power limit, where
@@ -14,9 +15,9 @@
 // zeros both 2.4): it moves half the accumulators per product.
 //
 // What bounds it: long products the power limit (T = 8192, 4096 x 8192: 404 us, 1.36 PFLOP/s,
-// MFMA busy 64 to 68 % of the cycles; on zeros 360 us), products of one or two turns of the CUs
-// the steps' waits and the last turn (T = 4096, 2 x 2112 x 2816 with pre: 89 us, 49 %), short ones
-// launch, first copies and epilogue (T = 77, 2 x 1411 x 1424: 7.5 us).
+// MFMA busy 64 to 68 % of the cycles; on zeros 360 to 373 us), products of one or two turns of
+// the CUs the steps' waits and the last turn (T = 4096, 2 x 2112 x 2816 with pre: 89 to 94 us,
+// 49 %), short ones launch, first copies and epilogue (T = 77, 2 x 1411 x 1424: 7.5 us).
 #pragma once
 
 #include <type_traits>
@@ -563,11 +564,13 @@ static hipError_t bf16_tile(const MatBf16Params& p, hipStream_t s) {
 // K steps about fixed + max(steps * alone + end, ceil(W / 256) * (steps * full + end)):
 // `full` is the time of a step, `alone` that of a workgroup that has its CU for itself
 // (several of the small ones fit on a CU), `end` that of prologue and epilogue.  The
-// figures (us) are fitted to times of 21 tiles at 80 to 90 shapes of each kind (T 16 to
-// 8192, the other sizes 64 to 8192); of those, these twelve lose 0.3 to 0.5 % on average
-// against the best of all 21 (the ends of the range: T = 752, N = 960, K = 536, TN: 64 x 64
-// 4.8 us, 256 x 256 15.5; T = 8192, N = 4096, K = 8192: 32 x 32 1612 us, 256 x 256 404),
-// and the choice by the estimate another 0.7 to 2.1 %.
+// figures (us) are fitted to times at 102 to 107 shapes of each kind, without adapters (T
+// 16 to 8192, the other sizes 64 to 8192).  There these twelve lose 0.1 to 0.6 % on average
+// against the best of 18 tiles (the ends of the range: T = 752, N = 960, K = 536, TN: 64 x 64
+// 4.8 us, 256 x 256 15.5; T = 8192, N = 4096, K = 8192, NN: 32 x 32 2229 us, 256 x 256 411),
+// and the choice by the estimate 0.3 to 0.9 % against the best of the twelve, for TN 1.7 %.
+// A product with adapters takes the tile of the same product without: what that loses is
+// not fitted (the adapters' part depends on how many of them a tile's tokens have).
 // A tile's LDS reads a step, (BN / 16 * WT + BT / 16 * WN) KB at 128 bytes a cycle, take longer
 // than its MFMA where the waves' parts are small: 128 x 128 in four waves of 64 x 64 takes 33
 // us at T = 1024, N = 2816, K = 4224, NN, in eight 40.  192 x 192 is there for three stages of

@@ -627,20 +627,20 @@ PyMethodDef methods[] = {
     METHOD(gated_matmul_bf16,
            "gated_matmul_bf16(x, w, act, out, pre=None, s=None, adapter_ids=None, b=None, ranks=None, stream=None)\n--\n\n"
            "out [T, F] = act(gate) * up of the bf16 product of x [T, K] with w [2F, K] (gate rows, then up rows, as an\n"
-           "expert's w13); pre [T, 2F] takes the sums for the backward pass.  Adapters as for matmul_bf16, before the\n"
-           "activation: s [T, 2R] and b [n, 2F, R], gate's then up's."),
+           "expert's w13); pre [T, 2F] takes the sums for the backward pass (without adapters).  Adapters as for\n"
+           "matmul_bf16, before the activation: s [T, 2R] and b [n, 2F, R], gate's then up's."),
     METHOD(adapter_shrink,
            "adapter_shrink(x, adapter_ids, a, scale, s, ranks=None, stream=None)\n--\n\n"
            "s[t] = scale[i] * (x[t] . a[i]), i = adapter_ids[t]: the first product of the tokens' low-rank adapters, zeros\n"
            "without one and past a rank.  a [n, R, K] with s [T, R], or [n, 2, R, K] (gate and up) with s [T, 2R]; scale\n"
-           "fp32 [n] or None."),
+           "fp32 [n] or None.  s is bf16: out carries its rounding in fp32 too."),
     METHOD(matmul_bf16_backward,
            "matmul_bf16_backward(x, w, dout, dx=None, dw=None, stream=None)\n--\n\n"
            "dx [T, K] = dout [T, N] . w, dw [N, K] = dout^T . x, each fp32 or bf16 or None."),
     METHOD(gated_matmul_bf16_backward,
            "gated_matmul_bf16_backward(x, w, act, pre, dout, dpre, dx=None, dw=None, stream=None)\n--\n\n"
-           "From pre [T, 2F] of the forward pass and dout [T, F]: dpre [T, 2F] (may be pre), dx [T, K] = dpre . w, dw\n"
-           "[2F, K] = dpre^T . x."),
+           "From pre [T, 2F] of a forward pass without adapters and dout [T, F]: dpre [T, 2F] (may be pre), dx [T, K] =\n"
+           "dpre . w, dw [2F, K] = dpre^T . x.  dpre is bf16: dx and dw carry its rounding in fp32 too."),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Operators around the expert FFN (see expert_ffn_amd).", -1, methods,

@@ -553,7 +553,8 @@ moe_status moe_gated_matmul_i8(const int8_t* xq, int64_t ldx, const float* x_sca
  *                          out[t][f] = act(g[t][f]) * u[t][f]
  *   x device bf16 [T, K], w device bf16 [N, K] (gated: [2F, K])
  *   out device [T, N] (gated: [T, F]), fp32 or bf16
- *   pre device bf16 [T, 2F] or NULL: g, then u of each row, for the backward pass
+ *   pre device bf16 [T, 2F] or NULL: g, then u of each row, for the backward pass (with
+ *        adapters the sums hold their part, of which the backward pass gives no gradients)
  * Sums are fp32, in a fixed order; each output is rounded once to its type.
  *
  * Low-rank adapters of many requests: with s not NULL, token t adds
@@ -590,7 +591,8 @@ moe_status moe_gated_matmul_bf16(const void* x, int64_t ldx, const void* w, int6
  *   x device bf16 [T, K]; a_pool device bf16: adapter a's [halves, R, K] contiguous at
  *   a_pool + a * a_stride; halves 1, or 2 (gate and up) for moe_gated_matmul_bf16
  *   scale device fp32 [n_adapters] or NULL: 1;  s device bf16 [T, halves * R]
- * Sums and the scale are fp32, rounded once.  Shapes and alignment as above.
+ * Sums and the scale are fp32, rounded once, to s: out carries that rounding in fp32 too.
+ * Shapes and alignment as above.
  */
 moe_status moe_adapter_shrink(const void* x, int64_t ldx, int32_t T, int32_t K, const int32_t* adapter_ids,
                               const void* a_pool, int64_t a_stride, int32_t n_adapters, int32_t R, int32_t halves,
@@ -605,7 +607,8 @@ moe_status moe_adapter_shrink(const void* x, int64_t ldx, int32_t T, int32_t K, 
  *                                   dx = dpre . w,  dw = dpre^T . x
  *   dx device [T, K] or NULL, dw device [N, K] (gated: [2F, K]) or NULL, each fp32 or bf16
  * dpre may be pre itself (same pointer and stride).  dpre is rounded to bf16, and dx and
- * dw are those of the rounded values; sums are fp32 in a fixed order, rounded once.  w is
+ * dw are those of the rounded values, in fp32 too; sums are fp32 in a fixed order, rounded
+ * once.  After a product with adapters dx = dpre . w lacks their part.  w is
  * read for dx only, x for dw only: the other may be NULL where its result is not wanted.
  * N (F) and K multiples of 8; rows of x, w, dout, pre and dpre 16-byte aligned with
  * strides up to 2^21 elements; dx and dw of up to 2^36 elements.  T = 0 writes zeros into dw.
